@@ -71,6 +71,16 @@ def lib() -> ctypes.CDLL:
             L.dflash2_chain.restype = i
             L.dflash2_topk.argtypes = [vp, i, i, i, i, vp, vp, vp]
             L.dflash2_topk.restype = i
+            ll, f = ctypes.c_longlong, ctypes.c_float
+            L.dflash2_sample.argtypes = [vp, ll, vp, vp, vp, vp, vp, f, i, f, f, i, i, i, vp, vp,
+                                         vp]
+            L.dflash2_sample.restype = i
+            L.dflash2_distill.argtypes = [vp, ll, vp, vp, vp, i, i, i, f, i, vp, vp, vp, ll, vp,
+                                          vp]
+            L.dflash2_distill.restype = i
+            L.dflash2_distill_backward.argtypes = [vp, vp, ll, vp, vp, vp, vp, i, i, i, f, i, vp,
+                                                   ll, vp, vp]
+            L.dflash2_distill_backward.restype = i
             L.dflash2_select_plan.argtypes = [i, i, i, i, i, i, ctypes.POINTER(ctypes.c_int)]
             L.dflash2_select_plan.restype = i
             L.dflash2_probe_gather.argtypes = [vp, ctypes.c_longlong, i, vp, i, vp, vp]
@@ -309,6 +319,139 @@ def chain(cand_ids, unary, edges, best_slot, p_min, start_slot=None, err_flag=No
                                _ptr(start_slot), S, n, K, float(p_min), _ptr(tokens), _ptr(probs),
                                _ptr(length), _ptr(err_flag), _stream(dev)))
     return tokens, probs, length
+
+
+def _logit_rows(t, name):
+    """(leading shape, rows, V, elements between two rows) of [..., V] logits: any
+    spacing of the rows, but one, and elements that lie side by side."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape, V = t.shape[:-1], t.shape[-1]
+    if t.is_contiguous():
+        return shape, t.numel() // V if V else 0, V, V
+    strides = t.stride()
+    if V > 1 and strides[-1] != 1:
+        raise ValueError(f"{name} must have its last dimension contiguous")
+    rows, ld = 1, None
+    for n, st in zip(reversed(shape), reversed(strides[:-1])):
+        if n != 1:
+            if ld is None:
+                ld = st
+            elif st != ld * rows:
+                raise ValueError(f"the rows of {name} must be evenly spaced")
+        rows *= n
+    return shape, rows, V, max(V, 1) if ld is None else ld
+
+
+def _need_rows(t, name, dtype, shape):
+    _need(t, name, dtype)
+    if t is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _setting(v, name, dtype, shape):
+    """(pointer, scalar) of a setting given for every row or once for all."""
+    if isinstance(v, torch.Tensor):
+        _need_rows(v, name, dtype, shape)
+        return v.data_ptr(), 0
+    return None, v
+
+
+def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None,
+           probs=None):
+    """One token of every row: logits [..., V] (fp32 or bf16; the rows may be evenly
+    spaced views), uniform [...] fp32 in [0, 1) -> (tokens [...] int32, probs [...]
+    fp32, the token's share among the entries that top_k, top_p and min_p keep).
+    Each setting is a number or a tensor [...] with one per row (top_k int32, the
+    others fp32).  The same row and number give the same token in any batch."""
+    shape, rows, V, ld = _logit_rows(logits, "logits")
+    _need_rows(uniform, "uniform", torch.float32, shape)
+    tp, t0 = _setting(temperature, "temperature", torch.float32, shape)
+    kp, k0 = _setting(top_k, "top_k", torch.int32, shape)
+    pp, p0 = _setting(top_p, "top_p", torch.float32, shape)
+    mp, m0 = _setting(min_p, "min_p", torch.float32, shape)
+    if tokens is None:
+        tokens = torch.empty(shape, dtype=torch.int32, device=logits.device)
+    else:
+        _need_rows(tokens, "tokens", torch.int32, shape)
+    if probs is None:
+        probs = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    else:
+        _need_rows(probs, "probs", torch.float32, shape)
+    _check(lib().dflash2_sample(logits.data_ptr(), ld, uniform.data_ptr(), tp, kp, pp, mp, t0, k0,
+                                p0, m0, rows, V, _code(logits.dtype), tokens.data_ptr(),
+                                probs.data_ptr(), _stream(logits.device)))
+    return tokens, probs
+
+
+def _teacher(teacher_ids, teacher_logits, weight, shape):
+    K = teacher_ids.shape[-1]
+    _need_rows(teacher_ids, "teacher_ids", torch.int32, shape + (K,))
+    _need_rows(teacher_logits, "teacher_logits", torch.float32, shape + (K,))
+    _need_rows(weight, "weight", torch.float32, shape)
+    return K
+
+
+def _grad_rows(grad, logits):
+    """The gradient tensor (allocated with the logits' strides when it is True) and the
+    elements between two of its rows."""
+    if grad is True:
+        grad = torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype,
+                                   device=logits.device)
+    if grad.shape != logits.shape or grad.dtype != logits.dtype:
+        raise ValueError("grad must have the shape and dtype of logits")
+    return grad, _logit_rows(grad, "grad")[3]
+
+
+def distill(logits, teacher_ids, teacher_logits, temperature=1.0, weight=None, grad=False,
+            loss=None, lse=None, err_flag=None):
+    """Distillation from a teacher's top K logits: logits [..., V] (fp32 or bf16; the
+    rows may be evenly spaced views), teacher_ids [..., K] int32 and teacher_logits
+    [..., K] fp32 as topk() returns them, weight [...] fp32 or None.  Returns
+    (loss [...] fp32, lse [...] fp32, grad): loss[r] = weight[r] * KL(teacher's
+    softmax over its K || student), lse for distill_backward, and with grad=True (or
+    a tensor to write, which may be logits) the gradient of the sum of the losses;
+    else None."""
+    shape, rows, V, ld = _logit_rows(logits, "logits")
+    K = _teacher(teacher_ids, teacher_logits, weight, shape)
+    if loss is None:
+        loss = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    else:
+        _need_rows(loss, "loss", torch.float32, shape)
+    if lse is None:
+        lse = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    else:
+        _need_rows(lse, "lse", torch.float32, shape)
+    _need(err_flag, "err_flag", torch.int32)
+    gld = 0
+    if grad is None or grad is False:
+        grad = None
+    else:
+        grad, gld = _grad_rows(grad, logits)
+    _check(lib().dflash2_distill(logits.data_ptr(), ld, teacher_ids.data_ptr(),
+                                 teacher_logits.data_ptr(), _ptr(weight), rows, V, K, temperature,
+                                 _code(logits.dtype), loss.data_ptr(), lse.data_ptr(), _ptr(grad),
+                                 gld, _ptr(err_flag), _stream(logits.device)))
+    return loss, lse, grad
+
+
+def distill_backward(grad_loss, logits, teacher_ids, teacher_logits, lse, temperature=1.0,
+                     weight=None, grad=True, err_flag=None):
+    """The gradient of distill() by its logits alone, from the gradient by its losses,
+    grad_loss [...] fp32, and the lse [...] that it returned.  grad may be a tensor to
+    write (also logits)."""
+    shape, rows, V, ld = _logit_rows(logits, "logits")
+    K = _teacher(teacher_ids, teacher_logits, weight, shape)
+    _need_rows(grad_loss, "grad_loss", torch.float32, shape)
+    _need_rows(lse, "lse", torch.float32, shape)
+    _need(err_flag, "err_flag", torch.int32)
+    grad, gld = _grad_rows(grad, logits)
+    _check(lib().dflash2_distill_backward(grad_loss.data_ptr(), logits.data_ptr(), ld,
+                                          teacher_ids.data_ptr(), teacher_logits.data_ptr(),
+                                          _ptr(weight), lse.data_ptr(), rows, V, K, temperature,
+                                          _code(logits.dtype), _ptr(grad), gld, _ptr(err_flag),
+                                          _stream(logits.device)))
+    return grad
 
 
 def take_device_faults() -> int:

@@ -2,6 +2,7 @@
 // then dispatch to the kernels.  Nothing here allocates device memory or
 // synchronises the host (except dflash2_take_device_faults, by contract).
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -189,6 +190,83 @@ int run_project(const void* h, const void* W, float* u, int P, int d, int R, int
                         ? df2::launch_project_bf16_tc(a, stream, num_sms_of_current_device())
                         : df2::launch_project_f32(a, stream);
     if (e != cudaSuccess) return cuda_fail(e, "project launch");
+    return DF2_OK;
+}
+
+// Checks shared by the operators on strided vocabulary rows: [rows, V] elements of
+// `dtype` at `p`, rows `ld` apart, from any element on.
+int validate_rows(const char* what, const char* name, const void* p, long long ld, int rows, int V,
+                  int dtype) {
+    if (ld < V)
+        return fail(DF2_ERR_INVALID_ARG, "%s: rows of %s are %lld apart, less than V=%d", what, name,
+                    ld, V);
+    if (reinterpret_cast<uintptr_t>(p) % esize(dtype) != 0)
+        return fail(DF2_ERR_INVALID_ARG, "%s: %s is not aligned to its elements", what, name);
+    if (rows > (1 << 24))  // a grid has at most 2^31 - 1 CTAs, several of them a row's
+        return fail(DF2_ERR_UNSUPPORTED, "%s: rows=%d > %d", what, rows, 1 << 24);
+    return DF2_OK;
+}
+
+// Bytes from the first to the last element of such rows.
+size_t rows_bytes(long long ld, int rows, int V, int dtype) {
+    return ((size_t)(rows - 1) * (size_t)ld + (size_t)V) * esize(dtype);
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int check_aligned4(const char* what, const Buf* bufs, int nb) {
+    for (int i = 0; i < nb; ++i)
+        if (!aligned4(bufs[i].p))
+            return fail(DF2_ERR_INVALID_ARG, "%s: %s is not 4-byte aligned", what, bufs[i].name);
+    return DF2_OK;
+}
+
+// The checks and the launch of dflash2_distill and dflash2_distill_backward (which
+// has grad_loss and takes lse as an input).
+int run_distill(const char* what, bool backward, df2::DistillArgs a, float temperature, int dtype,
+                void* stream) {
+    if (a.rows < 0 || a.V <= 0 || a.K <= 0)
+        return fail(DF2_ERR_INVALID_ARG, "%s: bad sizes rows=%d V=%d K=%d", what, a.rows, a.V, a.K);
+    if (!valid_dtype(dtype)) return fail(DF2_ERR_INVALID_ARG, "%s: bad dtype %d", what, dtype);
+    a.inv_t = 1.f / temperature;
+    a.c = a.inv_t * 1.44269504088896341f;
+    if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(a.c) || a.c == 0.f)
+        return fail(DF2_ERR_INVALID_ARG, "%s: temperature=%g must be positive and finite", what,
+                    (double)temperature);
+    if (a.rows == 0) return DF2_OK;
+    if (a.logits == nullptr || a.ids == nullptr || a.teacher == nullptr || a.lse == nullptr ||
+        (backward ? a.grad == nullptr || a.grad_loss == nullptr : a.loss == nullptr))
+        return fail(DF2_ERR_INVALID_ARG, "%s: NULL required pointer", what);
+    int st = validate_rows(what, "logits", a.logits, a.ld, a.rows, a.V, dtype);
+    if (st == DF2_OK && a.grad != nullptr)
+        st = validate_rows(what, "grad", a.grad, a.grad_ld, a.rows, a.V, dtype);
+    if (st != DF2_OK) return st;
+    const size_t RK = (size_t)a.rows * a.K * 4, R4 = (size_t)a.rows * 4;
+    const Buf ins[6] = {{a.ids, RK, "teacher_ids"},
+                        {a.teacher, RK, "teacher_logits"},
+                        {a.weight, R4, "weight"},
+                        {a.grad_loss, R4, "grad_loss"},
+                        {backward ? a.lse : nullptr, R4, "lse"},
+                        {a.logits, rows_bytes(a.ld, a.rows, a.V, dtype), "logits"}};
+    const Buf outs[4] = {{a.loss, R4, "loss"},
+                         {backward ? nullptr : a.lse, R4, "lse"},
+                         {a.err_flag, 4, "err_flag"},
+                         {a.grad, a.grad ? rows_bytes(a.grad_ld, a.rows, a.V, dtype) : 0, "grad"}};
+    st = check_aligned4(what, ins, 5);
+    if (st == DF2_OK) st = check_aligned4(what, outs, 3);
+    // the gradient may take the logits' place, exactly
+    const bool in_place = a.grad == a.logits && (a.grad_ld == a.ld || a.rows == 1);
+    if (st == DF2_OK) st = check_disjoint(outs, 4, ins, 5);
+    if (st == DF2_OK) st = check_disjoint(outs, in_place ? 3 : 4, ins + 5, 1);
+    if (st != DF2_OK) return st;
+    if (a.K > df2::kDistillMaxK)
+        return fail(DF2_ERR_UNSUPPORTED, "%s: K=%d > %d", what, a.K, df2::kDistillMaxK);
+    if (a.V > df2::kDistillMaxV)
+        return fail(DF2_ERR_UNSUPPORTED, "%s: V=%d > %d", what, a.V, df2::kDistillMaxV);
+    cudaError_t e = df2::launch_distill(a, dtype == DF2_BF16, static_cast<cudaStream_t>(stream),
+                                        num_sms_of_current_device(),
+                                        max_smem_optin_of_current_device());
+    if (e != cudaSuccess) return cuda_fail(e, what);
     return DF2_OK;
 }
 
@@ -532,6 +610,71 @@ int dflash2_chain(const int32_t* cand_ids, const float* unary, const float* edge
     cudaError_t e = df2::launch_chain(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "chain launch");
     return DF2_OK;
+}
+
+int dflash2_sample(const void* logits, long long ld, const float* uniform,
+                   const float* temperature, const int32_t* top_k, const float* top_p,
+                   const float* min_p, float temperature_all, int top_k_all, float top_p_all,
+                   float min_p_all, int rows, int V, int in_dtype, int32_t* tokens, float* probs,
+                   void* stream) {
+    g_err[0] = 0;
+    if (rows < 0 || V <= 0)
+        return fail(DF2_ERR_INVALID_ARG, "sample: bad sizes rows=%d V=%d", rows, V);
+    if (!valid_dtype(in_dtype)) return fail(DF2_ERR_INVALID_ARG, "sample: bad dtype %d", in_dtype);
+    if (temperature == nullptr && !(temperature_all >= 0.f))
+        return fail(DF2_ERR_INVALID_ARG, "sample: temperature=%g must not be negative",
+                    (double)temperature_all);
+    if (top_p == nullptr && std::isnan(top_p_all))
+        return fail(DF2_ERR_INVALID_ARG, "sample: top_p is not a number");
+    if (min_p == nullptr && std::isnan(min_p_all))
+        return fail(DF2_ERR_INVALID_ARG, "sample: min_p is not a number");
+    if (rows == 0) return DF2_OK;
+    if (logits == nullptr || uniform == nullptr || tokens == nullptr)
+        return fail(DF2_ERR_INVALID_ARG, "sample: NULL logits, uniform or tokens");
+    int st = validate_rows("sample", "logits", logits, ld, rows, V, in_dtype);
+    if (st != DF2_OK) return st;
+    const size_t R4 = (size_t)rows * 4;
+    const Buf ins[6] = {{uniform, R4, "uniform"},
+                        {temperature, R4, "temperature"},
+                        {top_k, R4, "top_k"},
+                        {top_p, R4, "top_p"},
+                        {min_p, R4, "min_p"},
+                        {logits, rows_bytes(ld, rows, V, in_dtype), "logits"}};
+    const Buf outs[2] = {{tokens, R4, "tokens"}, {probs, R4, "probs"}};
+    st = check_aligned4("sample", ins, 5);
+    if (st == DF2_OK) st = check_aligned4("sample", outs, 2);
+    if (st == DF2_OK) st = check_disjoint(outs, 2, ins, 6);
+    if (st != DF2_OK) return st;
+    if (V > df2::kSampleMaxV)
+        return fail(DF2_ERR_UNSUPPORTED, "sample: V=%d > %d", V, df2::kSampleMaxV);
+    df2::SampleArgs a{logits, ld, uniform, temperature, top_k, top_p, min_p, temperature_all,
+                      top_k_all, top_p_all, min_p_all, rows, V, tokens, probs};
+    cudaError_t e = df2::launch_sample(a, in_dtype == DF2_BF16, static_cast<cudaStream_t>(stream),
+                                       num_sms_of_current_device(),
+                                       max_smem_optin_of_current_device());
+    if (e != cudaSuccess) return cuda_fail(e, "sample launch");
+    return DF2_OK;
+}
+
+int dflash2_distill(const void* logits, long long ld, const int32_t* teacher_ids,
+                    const float* teacher_logits, const float* weight, int rows, int V, int K,
+                    float temperature, int dtype, float* loss, float* lse, void* grad,
+                    long long grad_ld, int32_t* err_flag, void* stream) {
+    g_err[0] = 0;
+    df2::DistillArgs a{logits, ld, teacher_ids, teacher_logits, weight, nullptr, rows, V, K, 0.f,
+                       0.f, loss, lse, grad, grad_ld, err_flag};
+    return run_distill("distill", false, a, temperature, dtype, stream);
+}
+
+int dflash2_distill_backward(const float* grad_loss, const void* logits, long long ld,
+                             const int32_t* teacher_ids, const float* teacher_logits,
+                             const float* weight, const float* lse, int rows, int V, int K,
+                             float temperature, int dtype, void* grad, long long grad_ld,
+                             int32_t* err_flag, void* stream) {
+    g_err[0] = 0;
+    df2::DistillArgs a{logits, ld, teacher_ids, teacher_logits, weight, grad_loss, rows, V, K, 0.f,
+                       0.f, nullptr, const_cast<float*>(lse), grad, grad_ld, err_flag};
+    return run_distill("distill_backward", true, a, temperature, dtype, stream);
 }
 
 int dflash2_probe_gather(const void* table, long long rows, int row_bytes, const int32_t* ids,

@@ -161,6 +161,54 @@ bool select_fused_plan(int S, int n, int d, int K, int R, int num_sms, size_t ma
 // Reads and clears the fused selector's device fault word (synchronous).
 cudaError_t take_select_faults(unsigned* flags);
 
+// Distillation from a teacher's top-K logits (distill.cu).  loss and lse, with
+// grad when it is not nullptr; or, when grad_loss is not nullptr, the gradient
+// alone from it and lse.
+struct DistillArgs {
+    const void* logits;    // [rows, V], rows `ld` elements apart
+    long long ld;
+    const int32_t* ids;    // [rows, K]
+    const float* teacher;  // [rows, K]
+    const float* weight;   // [rows] or nullptr (1)
+    const float* grad_loss;  // [rows] or nullptr
+    int rows, V, K;
+    float inv_t, c;        // 1 / T and log2(e) / T
+    float* loss;
+    float* lse;
+    void* grad;            // [rows, V], rows `grad_ld` elements apart
+    long long grad_ld;
+    int32_t* err_flag;
+    int cs = 1, slice = 0; // set by the launcher: CTAs per row, bytes of a staged slice
+};
+constexpr int kDistillMaxK = 1024;
+constexpr int kDistillMaxV = 1 << 28;
+cudaError_t launch_distill(DistillArgs a, int bf16, cudaStream_t stream, int num_sms,
+                           size_t max_smem);
+
+// One token of every row by temperature, top-k, top-p and min-p (sample.cu).  A
+// setting's pointer, when not nullptr, has a value for every row.
+struct SampleArgs {
+    const void* logits;  // [rows, V], rows `ld` elements apart
+    long long ld;
+    const float* uniform;
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    float temperature0;
+    int top_k0;
+    float top_p0, min_p0;
+    int rows, V;
+    int32_t* tokens;
+    float* probs;        // [rows] or nullptr
+    int cs = 1, slice = 0;
+};
+// Largest V: the fixed-point sums of a row stay inside 62 bits, and those of a
+// CTA's histogram inside their words.
+constexpr int kSampleMaxV = 1 << 21;
+cudaError_t launch_sample(SampleArgs a, int bf16, cudaStream_t stream, int num_sms,
+                          size_t max_smem);
+
 // Measurement aid: random-row gather (probe.cu).  out[i] = XOR of the 32-bit
 // words of row ids[i] (ids clamped into [0, rows)); row_bytes a power of two
 // in [16, 512].

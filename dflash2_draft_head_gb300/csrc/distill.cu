@@ -1,0 +1,405 @@
+// Distillation from a teacher's top-K logits: the loss of every row, its
+// gradient, or both in one pass over the student's logits.
+//
+//   q_k   = softmax over the row's K teacher logits / T   (id < 0: an empty slot)
+//   lse   = log sum_j exp(z_j / T)
+//   loss  = weight * sum_k q_k (log q_k - z[id_k] / T + lse)
+//   dz_j  = weight * g * (exp(z_j / T - lse) - sum_{k: id_k = j} q_k) / T
+//
+// Bound by HBM: the logits are read once and the gradient is written once.  A
+// row is split over the CTAs of a cluster, each holding its slice in shared
+// memory between the two uses (the sum of exponentials, then the gradient),
+// which only a (max, sum) pair per CTA crosses.
+//
+// All exponentials are powers of two with c = log2(e)/T folded in: a slice's
+// sum is taken against its own rounded base b = c * max, 2^(c*z - b) being one
+// fused multiply-add and one ex2, and the same b goes into lse, so the rounding
+// of b cancels.  The loss takes c * z - b the same way (in 64 bits, K terms).
+// Where c * max leaves fp32's range (a row masked by the type's lowest value all
+// over) the power is 2^((z - max) * c).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "common.cuh"
+#include "dflash2.h"
+#include "rows.cuh"
+
+namespace df2 {
+namespace {
+
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLog2e = 1.44269504088896341f;
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+template <typename S>
+__device__ __forceinline__ S warp_sum(S v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A row's teacher entries in shared memory.
+struct Teacher {
+    int* id;     // token, -1 for an empty slot
+    float* q;    // its share
+    float* lq;   // log of it
+    float* z;    // the student's logit there (this CTA's tokens only)
+    __device__ __forceinline__ Teacher(char* at, int K) {
+        id = reinterpret_cast<int*>(at);
+        q = reinterpret_cast<float*>(at) + K;
+        lq = q + K;
+        z = lq + K;
+    }
+};
+
+// Softmax of the row's K teacher logits by one warp; returns 1, or 0 when the
+// row has no entry with a share.  A token outside [0, V) is an empty slot; one
+// that is not negative is flagged too.
+__device__ float teacher_softmax(const Teacher& t, const int32_t* ids, const float* logits, int K,
+                                 int V, float inv_t, int32_t* err_flag) {
+    const int lane = threadIdx.x & 31;
+    float m = neg_inf();
+    bool nan = false;  // fmaxf drops it
+    for (int k = lane; k < K; k += 32) {
+        int id = ids[k];
+        float y = logits[k];
+        if (id < 0 || id >= V) {
+            if (id >= V && err_flag != nullptr) atomicOr(err_flag, DF2_FLAG_BAD_ID);
+            id = -1;
+            y = neg_inf();
+        }
+        t.id[k] = id;
+        t.lq[k] = y;
+        m = fmaxf(m, y);
+        nan = nan || y != y;
+    }
+    m = __any_sync(0xffffffffu, nan) ? __int_as_float(0x7fffffff) : warp_max(m);
+    if (m == neg_inf()) {
+        for (int k = lane; k < K; k += 32) t.q[k] = 0.f;
+        __syncwarp();
+        return 0.f;
+    }
+    float s = 0.f;
+    for (int k = lane; k < K; k += 32) s += expf((t.lq[k] - m) * inv_t);
+    s = warp_sum(s);
+    const float ls = logf(s);
+    for (int k = lane; k < K; k += 32) {
+        const float y = (t.lq[k] - m) * inv_t;
+        t.q[k] = t.id[k] < 0 ? 0.f : expf(y) / s;
+        t.lq[k] = y - ls;
+    }
+    __syncwarp();
+    return 1.f;
+}
+
+// 2^(c * z - base), base = c * max: rounded to fp32 and by a fused multiply-add, or
+// with the maximum taken off first where the base is too large for that.
+constexpr float kFastBase = 1e38f;
+struct Power {
+    bool fast;
+    float c, m, nb;  // the maximum (0 for -inf: every z is), -base
+    __device__ __forceinline__ Power(float m_, float c_) : c(c_), m(m_ == neg_inf() ? 0.f : m_) {
+        nb = -__fmul_rn(m, c);
+        fast = fabsf(nb) < kFastBase;
+    }
+    template <bool FAST>
+    __device__ __forceinline__ float of(float z) const {
+        return ex2(FAST ? fmaf(z, c, nb) : (z - m) * c);
+    }
+    __device__ __forceinline__ float operator()(float z) const {
+        return fast ? of<true>(z) : of<false>(z);
+    }
+    // 2^(another's base - base)
+    __device__ __forceinline__ float against(const Power& o) const {
+        return ex2(fast ? nb - o.nb : (o.m - m) * c);
+    }
+    __device__ __forceinline__ double base() const { return fast ? -(double)nb : (double)m * c; }
+    // c * z - base in 64 bits
+    __device__ __forceinline__ double depth(float z) const {
+        return fast ? (double)z * c + nb : ((double)z - m) * c;
+    }
+};
+
+// A slice's largest logit and the sum of its powers against that (0, or NaN, where
+// nothing is above -inf).
+struct alignas(8) MaxSum {  // goes to other CTAs as one 64-bit store
+    float max, sum;
+};
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+    return __float2bfloat16_rn(x);
+}
+
+// Writes vector v of a gradient row: one 16-byte store where the gradient's row
+// lies on the logits' grid, else (and at the row's edges) element by element.
+template <typename T>
+__device__ __forceinline__ void store_vec(const RowView<T>& r, T* out, bool on_grid, int v,
+                                          const float (&f)[VecOf<T>::kElems]) {
+    constexpr int E = VecOf<T>::kElems;
+    const int e0 = v * E - r.head;
+    if (on_grid && r.inner(v)) {
+        __stcs(reinterpret_cast<uint4*>(out + e0), pack(f));
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        if (e0 + j >= 0 && e0 + j < r.V) out[e0 + j] = from_f32<T>(f[j]);
+}
+
+// Rewrites the gradient at the teacher's tokens among elements [e_lo, e_hi):
+// (share(z) - sum of q over the slots of that token) * scale, by the first slot of
+// each token.  Call after a barrier behind the plain writes.
+template <typename T, typename F>
+__device__ __forceinline__ void fix_tokens(const Teacher& t, int K, T* out, int e_lo, int e_hi,
+                                           float scale, F share) {
+    for (int k = threadIdx.x; k < K; k += kRowThreads) {
+        const int id = t.id[k];
+        if (id < e_lo || id >= e_hi) continue;
+        bool first = true;
+        float q = 0.f;
+        for (int j = 0; j < K; ++j) {
+            if (t.id[j] != id) continue;
+            first = first && j >= k;
+            q += t.q[j];
+        }
+        if (first) out[id] = from_f32<T>((share(t.z[k]) - q) * scale);
+    }
+}
+
+// One cluster per row: lse and loss, and the gradient when GRAD.
+template <typename T, bool GRAD, bool STAGED>
+__global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
+    constexpr int E = VecOf<T>::kElems;
+    extern __shared__ __align__(16) char smem[];
+    __shared__ MaxSum warp_ms[kRowWarps];
+    __shared__ float warp_q;                      // 1, or 0 without a teacher
+    __shared__ MaxSum cta_ms[kRowMaxCluster];     // every CTA's
+
+    const int cs = a.cs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = cs > 1 ? (int)cluster_ctarank() : 0;
+    const int row = blockIdx.x / cs;
+    const RowView<T> r(a.logits, a.ld, row, a.V);
+    const RowSlice sl(r.nvec, rank, cs, warp);
+    const int e_lo = max(sl.lo * E - r.head, 0), e_hi = min(sl.hi * E - r.head, a.V);
+    T* out = GRAD ? static_cast<T*>(a.grad) + (long long)row * a.grad_ld : nullptr;
+    const bool on_grid =
+        GRAD && ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(r.row)) & 15u) == 0;
+    const float weight = a.weight != nullptr ? a.weight[row] : 1.f;
+    if (weight == 0.f) {  // the whole cluster leaves: the row's logits are not read
+        if (GRAD) {
+            const float zero[E] = {};
+            for (int v = sl.wlo + lane; v < sl.whi; v += 32) store_vec<T>(r, out, on_grid, v, zero);
+        }
+        if (rank == 0 && tid == 0) {
+            a.loss[row] = 0.f;
+            a.lse[row] = 0.f;
+        }
+        return;
+    }
+    if (cs > 1) cluster_arrive();  // met by cluster_wait below: every CTA has started
+
+    const uint32_t stage0 = smem_u32(smem) - (uint32_t)sl.lo * 16u;
+    if (STAGED) {
+        for (int v = sl.wlo + lane; v < sl.whi; v += 32) r.stage(v, stage0 + (uint32_t)v * 16u);
+    }
+    auto vec = [&](int v) { return STAGED ? lds_v4(stage0 + (uint32_t)v * 16u) : r.load(v); };
+
+    const Teacher t(smem + a.slice, a.K);
+    if (warp == 0) {
+        const float q = teacher_softmax(t, a.ids + (long long)row * a.K,
+                                        a.teacher + (long long)row * a.K, a.K, a.V, a.inv_t,
+                                        rank == 0 ? a.err_flag : nullptr);
+        // z at the teacher's tokens: rank 0 needs all of them, the others their own
+        for (int k = lane; k < a.K; k += 32) {
+            const int id = t.id[k];
+            if (id >= 0 && (rank == 0 || (id >= e_lo && id < e_hi))) t.z[k] = to_f32(r.row[id]);
+        }
+        if (lane == 0) warp_q = q;
+    }
+    if (STAGED) cp_async_wait_all();
+
+    // this warp's base and sum
+    float m = neg_inf();
+    for (int v = sl.wlo + lane; v < sl.whi; v += 32) m = fmaxf(m, vec_max<T>(vec(v)));
+    m = warp_max(m);
+    const Power pw(m, a.c);
+    float s = 0.f;
+    auto sum_up = [&](auto fast) {
+        for (int v = sl.wlo + lane; v < sl.whi; v += 32) {
+            float f[E];
+            unpack(vec(v), f);
+#pragma unroll
+            for (int j = 0; j < E; ++j) s += pw.template of<fast.value>(f[j]);
+        }
+    };
+    if (pw.fast)
+        sum_up(std::true_type{});
+    else
+        sum_up(std::false_type{});
+    s = warp_sum(s);
+    if (lane == 0) warp_ms[warp] = {m, s};
+    __syncthreads();
+    auto join = [&](const MaxSum* ms, int n) {
+        MaxSum all{neg_inf(), 0.f};
+        for (int i = 0; i < n; ++i) all.max = fmaxf(all.max, ms[i].max);
+        const Power p(all.max, a.c);
+        for (int i = 0; i < n; ++i)
+            all.sum += ms[i].max == neg_inf() ? ms[i].sum
+                                              : ms[i].sum * p.against(Power(ms[i].max, a.c));
+        return all;
+    };
+    MaxSum all = join(warp_ms, kRowWarps);
+    if (cs > 1) {
+        cluster_wait();
+        if (tid < cs)
+            st_cluster_b64(map_cluster(smem_u32(&cta_ms[rank]), tid),
+                           __builtin_bit_cast(uint64_t, all));
+        __syncwarp();
+        cluster_sync();  // no CTA's shared memory is touched from outside after this
+        all = join(cta_ms, cs);
+    }
+    const Power pg(all.max, a.c);
+    const float S = all.sum;
+    if (rank == 0 && warp == 0) {
+        const float ls = log2f(S);
+        double loss = 0;
+        for (int k = lane; k < a.K; k += 32)
+            if (t.q[k] != 0.f)
+                loss += (double)t.q[k] * (t.lq[k] - (double)kLn2 * (pg.depth(t.z[k]) - ls));
+        loss = warp_sum(loss);
+        if (lane == 0) {
+            // no logit above -inf: the student gives the teacher's tokens no share
+            if (S == 0.f) loss = warp_q == 0.f ? 0.0 : (double)INFINITY;
+            a.loss[row] = (float)(weight * loss);
+            a.lse[row] = S == 0.f ? neg_inf() : (float)((double)kLn2 * (pg.base() + ls));
+        }
+    }
+    if (GRAD) {
+        // without a teacher the whole gradient is 0
+        const float scale = weight * a.inv_t;
+        const float per_s = S == 0.f || warp_q == 0.f ? 0.f : 1.f / S;
+        const float k = scale * per_s;
+        auto write = [&](auto fast) {
+            for (int v = sl.wlo + lane; v < sl.whi; v += 32) {
+                float f[E];
+                unpack(vec(v), f);
+#pragma unroll
+                for (int j = 0; j < E; ++j) f[j] = pg.template of<fast.value>(f[j]) * k;
+                store_vec<T>(r, out, on_grid, v, f);
+            }
+        };
+        if (pg.fast)
+            write(std::true_type{});
+        else
+            write(std::false_type{});
+        if (warp_q == 0.f) return;
+        __syncthreads();
+        fix_tokens<T>(t, a.K, out, e_lo, e_hi, scale,
+                      [&](float z) { return pg(z) * per_s; });
+    }
+}
+
+// The gradient alone, from lse and the upstream gradient: `cs` CTAs a row, which
+// do not wait on one another.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) distill_grad_kernel(DistillArgs a) {
+    constexpr int E = VecOf<T>::kElems;
+    extern __shared__ __align__(16) char smem[];
+    __shared__ float warp_q;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row = blockIdx.x / a.cs, rank = blockIdx.x % a.cs;
+    const RowView<T> r(a.logits, a.ld, row, a.V);
+    const RowSlice sl(r.nvec, rank, a.cs, warp);
+    const int e_lo = max(sl.lo * E - r.head, 0), e_hi = min(sl.hi * E - r.head, a.V);
+    T* out = static_cast<T*>(a.grad) + (long long)row * a.grad_ld;
+    const bool on_grid =
+        ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(r.row)) & 15u) == 0;
+    const float weight = a.weight != nullptr ? a.weight[row] : 1.f;
+    const float up = a.grad_loss[row];
+    if (weight == 0.f || up == 0.f) {
+        const float zero[E] = {};
+        for (int v = sl.wlo + lane; v < sl.whi; v += 32) store_vec<T>(r, out, on_grid, v, zero);
+        return;
+    }
+    const Teacher t(smem, a.K);
+    if (warp == 0) {
+        const float q = teacher_softmax(t, a.ids + (long long)row * a.K,
+                                        a.teacher + (long long)row * a.K, a.K, a.V, a.inv_t,
+                                        rank == 0 ? a.err_flag : nullptr);
+        for (int k = lane; k < a.K; k += 32) {
+            const int id = t.id[k];
+            if (id >= e_lo && id < e_hi) t.z[k] = to_f32(r.row[id]);
+        }
+        if (lane == 0) warp_q = q;
+    }
+    __syncthreads();  // also: z is read before the gradient may take its place
+    const float scale = up * weight * a.inv_t;
+    const float lse = a.lse[row];
+    const bool none = warp_q == 0.f;
+    auto share = [&](float z) {
+        return lse == neg_inf() ? 0.f : ex2(fmaf(z, a.inv_t, -lse) * kLog2e);
+    };
+    for (int v = sl.wlo + lane; v < sl.whi; v += 32) {
+        float f[E];
+        unpack(r.load(v), f);
+#pragma unroll
+        for (int j = 0; j < E; ++j) f[j] = none ? 0.f : share(f[j]) * scale;
+        store_vec<T>(r, out, on_grid, v, f);
+    }
+    if (none) return;
+    __syncthreads();
+    fix_tokens<T>(t, a.K, out, e_lo, e_hi, scale, share);
+}
+
+template <typename T, bool GRAD>
+cudaError_t launch_typed(const DistillArgs& a, bool staged, size_t smem, cudaStream_t stream) {
+    return launch_rows(staged ? distill_kernel<T, GRAD, true> : distill_kernel<T, GRAD, false>, a,
+                       a.rows, a.cs, smem, stream);
+}
+
+template <typename T>
+cudaError_t launch_grad(DistillArgs a, size_t smem, cudaStream_t stream, int num_sms) {
+    // The CTAs of a row do not wait on one another, so any number of them will do:
+    // slices of kGradSlice bytes, smaller ones down to kRowSliceMin with few rows.
+    constexpr long long kGradSlice = 32 * 1024;
+    const long long bytes = row_max_vecs(a.V, sizeof(T)) * 16;
+    const long long want = std::min((2LL * num_sms + a.rows - 1) / a.rows, bytes / kRowSliceMin);
+    a.cs = (int)std::min(std::max({1LL, (bytes + kGradSlice - 1) / kGradSlice, want}),
+                         0x7fffffffLL / a.rows);
+    distill_grad_kernel<T><<<(unsigned)((long long)a.rows * a.cs), kRowThreads, smem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_distill(DistillArgs a, int bf16, cudaStream_t stream, int num_sms,
+                           size_t max_smem) {
+    const size_t teacher = (size_t)a.K * 16;
+    if (a.grad_loss != nullptr)
+        return bf16 ? launch_grad<__nv_bfloat16>(a, teacher, stream, num_sms)
+                    : launch_grad<float>(a, teacher, stream, num_sms);
+    const RowPlan p = plan_rows(a.rows, a.V, bf16 ? 2 : 4, num_sms, max_smem - teacher - 1024);
+    a.cs = p.cs;
+    a.slice = (int)p.slice;
+    const size_t smem = p.slice + teacher;
+    if (bf16)
+        return a.grad != nullptr ? launch_typed<__nv_bfloat16, true>(a, p.staged, smem, stream)
+                                 : launch_typed<__nv_bfloat16, false>(a, p.staged, smem, stream);
+    return a.grad != nullptr ? launch_typed<float, true>(a, p.staged, smem, stream)
+                             : launch_typed<float, false>(a, p.staged, smem, stream);
+}
+
+}  // namespace df2

@@ -1,0 +1,204 @@
+// Shared by the operators that work on whole vocabulary rows (sampling and
+// distillation): a row of V elements as 16-byte vectors, split over the CTAs of
+// a thread-block cluster and, inside a CTA, over its warps in index order.
+//
+// A row may start at any element: the vectors lie on the 16-byte grid of memory,
+// so the first and the last one may hold places that are not the row's.  Those
+// are never read; they get the fill value -inf, which no operator counts.
+// Each thread copies the vectors that it works on itself (cp.async into shared
+// memory), so a row's slice needs no barrier before it is read.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace df2 {
+
+constexpr int kRowThreads = 256;
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kRowMaxCluster = 8;
+
+template <typename T>
+struct VecOf;
+template <>
+struct VecOf<float> {
+    static constexpr int kElems = 4;
+};
+template <>
+struct VecOf<__nv_bfloat16> {
+    static constexpr int kElems = 8;
+};
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+
+// One vector's elements in fp32, in index order.
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// One vector's largest element; a NaN is passed over.
+template <typename T>
+__device__ __forceinline__ float vec_max(const uint4& v);
+template <>
+__device__ __forceinline__ float vec_max<float>(const uint4& v) {
+    float f[4];
+    unpack(v, f);
+    return fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));
+}
+template <>
+__device__ __forceinline__ float vec_max<__nv_bfloat16>(const uint4& v) {
+    const __nv_bfloat162 a = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&v.x),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&v.y));
+    const __nv_bfloat162 b = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&v.z),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&v.w));
+    const __nv_bfloat162 c = __hmax2(a, b);
+    return fmaxf(__low2float(c), __high2float(c));
+}
+
+__device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 2^x, flushing results below 2^-126 to 0 (relative error about 2^-22).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Row `r` of a [rows, V] array whose rows are `ld` elements apart.
+template <typename T>
+struct RowView {
+    static constexpr int E = VecOf<T>::kElems;
+    const T* row;   // element 0
+    const T* grid;  // start of the vector that holds element 0 (16-byte aligned)
+    int head;       // places before element 0 in that vector
+    int V;
+    int nvec;
+
+    __device__ __forceinline__ RowView(const void* base, long long ld, int r, int V_) : V(V_) {
+        row = static_cast<const T*>(base) + (long long)r * ld;
+        head = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+        grid = row - head;
+        nvec = (head + V + E - 1) / E;
+    }
+    // Whether every place of vector v is an element of the row.
+    __device__ __forceinline__ bool inner(int v) const {
+        return v * E >= head && v * E + E <= head + V;
+    }
+    // Vector v by guarded loads of single elements, -inf in the places outside the row.
+    __device__ __forceinline__ uint4 edge(int v) const {
+        float f[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const int e = v * E + j - head;
+            f[j] = e >= 0 && e < V ? to_f32(row[e]) : neg_inf();
+        }
+        return pack(f);
+    }
+    __device__ __forceinline__ uint4 load(int v) const {
+        return inner(v) ? *reinterpret_cast<const uint4*>(grid + (long long)v * E) : edge(v);
+    }
+    // Vector v into shared memory at dst: asynchronous but for the row's two edges.
+    __device__ __forceinline__ void stage(int v, uint32_t dst) const {
+        if (inner(v))
+            cp_async16(dst, grid + (long long)v * E);
+        else
+            st_shared_v4(dst, edge(v));
+    }
+};
+
+// Which vectors of a row a CTA (rank of cs) and one of its warps work on: both
+// splits are in index order.  Warp slices start on 128-byte lines.
+struct RowSlice {
+    int lo, hi;    // the CTA's vectors
+    int wlo, whi;  // this warp's
+    __device__ __forceinline__ RowSlice(int nvec, int rank, int cs, int warp) {
+        const int per = (nvec + cs - 1) / cs;
+        lo = min(rank * per, nvec);
+        hi = min(lo + per, nvec);
+        const int pw = ((hi - lo + kRowWarps - 1) / kRowWarps + 7) & ~7;
+        wlo = min(lo + warp * pw, hi);
+        whi = min(wlo + pw, hi);
+    }
+};
+
+// How a [rows, V] array is split over clusters (host).
+struct RowPlan {
+    int cs;        // CTAs per row (the cluster's size, a power of two)
+    bool staged;   // a CTA's slice is held in shared memory
+    size_t slice;  // bytes of it (0 when not staged)
+};
+
+// 16-byte vectors of a row of V elements of `es` bytes, wherever it starts.
+inline long long row_max_vecs(long long V, size_t es) {
+    const long long E = 16 / (long long)es;
+    return (V + 2 * (E - 1)) / E;
+}
+
+// Slices of at most kRowSliceBytes (several CTAs of an SM then overlap one's loads
+// with another's arithmetic); with few rows, smaller ones, so that more SMs take part.
+constexpr long long kRowSliceBytes = 40 * 1024;
+constexpr long long kRowSliceMin = 8 * 1024;
+inline RowPlan plan_rows(int rows, int V, size_t es, int num_sms, size_t max_slice) {
+    const long long vecs = row_max_vecs(V, es), bytes = vecs * 16;
+    int cs = 1;
+    while (cs < kRowMaxCluster && bytes / cs > kRowSliceBytes) cs *= 2;
+    while (cs < kRowMaxCluster && (long long)rows * cs < 2LL * num_sms && bytes / cs > kRowSliceMin)
+        cs *= 2;
+    const long long slice = (vecs + cs - 1) / cs * 16;
+    const bool staged = slice <= (long long)max_slice;
+    return {cs, staged, staged ? (size_t)slice : 0};
+}
+
+// Launches `rows` clusters of cs CTAs.
+template <typename Args>
+cudaError_t launch_rows(void (*kernel)(Args), const Args& a, int rows, int cs, size_t smem,
+                        cudaStream_t stream) {
+    if (smem > 32 * 1024) {  // with the static arrays this may pass the default 48 KB
+        const cudaError_t e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)rows * cs));
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)cs;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = cs > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace df2

@@ -15,8 +15,9 @@
  *
  * Conventions shared by every call:
  *   - All tensor pointers are DEVICE pointers to contiguous row-major arrays,
- *     16-byte aligned.  The caller allocates and owns them; the library never
- *     allocates, frees or keeps a pointer past the call.
+ *     16-byte aligned, where a call does not say otherwise.  The caller allocates
+ *     and owns them; the library never allocates, frees or keeps a pointer past the
+ *     call.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *     Every call only enqueues work on that stream and returns; it never
  *     synchronises the host.
@@ -311,6 +312,94 @@ int dflash2_chain(const int32_t* cand_ids, const float* unary, const float* edge
                   const int32_t* best_slot, const int32_t* start_slot, int S, int n, int K,
                   float p_min, int32_t* tokens, float* probs, int32_t* length, int32_t* err_flag,
                   void* stream);
+
+/*
+ * Sampling: one token of every logit row, from a given uniform number, after
+ * temperature, top-k, top-p and min-p.  Next to the greedy chain readout it
+ * verifies drafts: a drafted token stands when it is the token sampled from the
+ * target's row.  For row r, with m = max_j x_j and T, k, p, q the row's
+ * temperature, top_k, top_p and min_p:
+ *   w_j = 2^((x_j - m) * (log2(e) / T))      (= exp((x_j - m) / T), in fp32)
+ *   W_j = round(w_j * 2^40), a whole number (an entry that is NaN or -inf: 0)
+ *   in order of falling x (equal values: lowest index first; -0 equals +0) entry
+ *   j is kept while fewer than k entries stand before it, the sum of the W before
+ *   it is below p * (sum of W over the first k), and w_j >= q; the first entry
+ *   is always kept
+ *   token = the first j, in order of index, at which the running sum of the kept
+ *           W passes floor(uniform[r] * S), S the kept entries' sum
+ *   prob  = W_token / S
+ * Sums of whole numbers are exact, so the token does not depend on the number of
+ * rows or on how a row is split over the GPU.  T <= 0 (or NaN): the largest entry
+ * (lowest index).  top_k <= 0 or >= V, top_p >= 1 (or NaN), min_p <= 0 (or NaN): no
+ * such limit; top_p <= 0 or min_p > 1: the first entry alone.  A row whose maximum is
+ * +inf samples among its +inf entries.  A row with no entry above -inf gives token -1
+ * and prob 0.  uniform is in [0, 1); a value outside is taken to the nearer end, NaN
+ * to 0.
+ *   logits  [rows,V] in_dtype, element (r, j) at r * ld + j, ld >= V; any start
+ *           aligned to an element
+ *   uniform [rows] fp32
+ *   temperature [rows] fp32, top_k [rows] int32, top_p [rows] fp32, min_p [rows]
+ *           fp32: one setting per row, or NULL to use the *_all value for every row
+ *   tokens  [rows] int32 out;  probs [rows] fp32 out, or NULL
+ * The vectors of one value per row are aligned to 4 bytes.  rows == 0 launches nothing.
+ * INVALID_ARG: rows < 0; V <= 0; ld < V; NULL required pointer; misalignment;
+ * temperature_all negative or NaN, top_p_all or min_p_all NaN (where used); an output
+ * overlapping another buffer.  UNSUPPORTED: V > 2^21; rows > 2^24.
+ */
+int dflash2_sample(const void* logits, long long ld, const float* uniform,
+                   const float* temperature, const int32_t* top_k, const float* top_p,
+                   const float* min_p, float temperature_all, int top_k_all, float top_p_all,
+                   float min_p_all, int rows, int V, int in_dtype, int32_t* tokens, float* probs,
+                   void* stream);
+
+/*
+ * Distillation from a teacher's top-K logits (such as dflash2_topk extracts from the
+ * target's rows): the loss of every row of the student's logits and, when grad is
+ * not NULL, its gradient, in one pass.  For row r with logits z, T = temperature:
+ *   q_k   = softmax over the row's K teacher logits / T
+ *   lse   = log sum_j exp(z_j / T)
+ *   loss  = weight[r] * sum_k q_k * (log q_k - (z[id_k] / T - lse))
+ *   grad_j = weight[r] * (exp(z_j / T - lse) - sum_{k: id_k = j} q_k) / T
+ * i.e. the Kullback-Leibler divergence of the teacher's renormalised top K from the
+ * student, and d loss / d z_j.  Fold a mean, position weights or T^2 into weight.
+ *   logits  [rows,V] in `dtype`, element (r, j) at r * ld + j, ld >= V; any start
+ *           aligned to an element
+ *   teacher_ids [rows,K] int32, teacher_logits [rows,K] fp32; a negative id is an empty
+ *           slot (as dflash2_topk pads a row), its logit is not used; a token may
+ *           stand in several slots
+ *   weight  [rows] fp32, or NULL for 1
+ *   loss, lse [rows] fp32 out
+ *   grad    [rows,V] in `dtype` out (rounded once), rows grad_ld elements apart, or NULL;
+ *           may be the logits themselves (same pointer and spacing).  Stores are 16 bytes
+ *           wide where a row of grad and of logits start at the same place modulo 16
+ *           bytes, single elements otherwise
+ *   err_flag one device int32 or NULL: DF2_FLAG_BAD_ID when an id is >= V (an empty slot)
+ * A row with weight 0 is not read: its loss, lse and gradient are 0.  A row whose slots
+ * are all empty or -inf has loss and gradient 0.  A token at -inf in z with q > 0 makes the
+ * loss +inf, the gradient stays finite; a row with no z above -inf counts as a softmax
+ * that is 0 everywhere (lse -inf).  NaN or +inf in a row's z or teacher logits makes its
+ * outputs NaN.  All sums are in fp32 or more.  rows == 0 launches nothing.
+ * INVALID_ARG: rows < 0; V or K <= 0; ld or grad_ld < V; a temperature that is not
+ * positive and finite; NULL required pointer; misalignment (vectors of one or K values
+ * per row: 4 bytes); an output overlapping another buffer, other than grad in place.
+ * UNSUPPORTED: K > 1024; V > 2^28; rows > 2^24.
+ */
+int dflash2_distill(const void* logits, long long ld, const int32_t* teacher_ids,
+                    const float* teacher_logits, const float* weight, int rows, int V, int K,
+                    float temperature, int dtype, float* loss, float* lse, void* grad,
+                    long long grad_ld, int32_t* err_flag, void* stream);
+
+/*
+ * The gradient of dflash2_distill alone, for an upstream gradient known only after the
+ * loss:  grad_j = grad_loss[r] * weight[r] * (exp(z_j / T - lse[r]) - sum q) / T.
+ *   grad_loss [rows] fp32; lse [rows] as dflash2_distill wrote it; the rest as there.
+ * A row with grad_loss or weight 0 is not read and its gradient is 0.
+ */
+int dflash2_distill_backward(const float* grad_loss, const void* logits, long long ld,
+                             const int32_t* teacher_ids, const float* teacher_logits,
+                             const float* weight, const float* lse, int rows, int V, int K,
+                             float temperature, int dtype, void* grad, long long grad_ld,
+                             int32_t* err_flag, void* stream);
 
 /*
  * Measurement aid (no counterpart in the DFlash2 pull request): the rate at
