@@ -110,12 +110,14 @@ struct Power {
         nb = -__fmul_rn(m, c);
         fast = fabsf(nb) < kFastBase;
     }
-    template <bool FAST>
-    __device__ __forceinline__ float of(float z) const {
-        return ex2(FAST ? fmaf(z, c, nb) : (z - m) * c);
-    }
     __device__ __forceinline__ float operator()(float z) const {
-        return fast ? of<true>(z) : of<false>(z);
+        return ex2(fast ? fmaf(z, c, nb) : (z - m) * c);
+    }
+    template <bool FAST>
+    __device__ __forceinline__ float2 of(f32x2 z) const {
+        const float2 d = halves(FAST ? fma2(z, pair(c, c), pair(nb, nb))
+                                     : mul2(add2(z, pair(-m, -m)), pair(c, c)));
+        return make_float2(ex2(d.x), ex2(d.y));
     }
     // 2^(another's base - base)
     __device__ __forceinline__ float against(const Power& o) const {
@@ -147,9 +149,16 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
 // lies on the logits' grid, else (and at the row's edges) element by element.
 template <typename T>
 __device__ __forceinline__ void store_vec(const RowView<T>& r, T* out, bool on_grid, int v,
-                                          const float (&f)[VecOf<T>::kElems]) {
+                                          const f32x2 (&p)[VecOf<T>::kElems / 2]) {
     constexpr int E = VecOf<T>::kElems;
     const int e0 = v * E - r.head;
+    float f[E];
+#pragma unroll
+    for (int j = 0; j < E / 2; ++j) {
+        const float2 h = halves(p[j]);
+        f[2 * j] = h.x;
+        f[2 * j + 1] = h.y;
+    }
     if (on_grid && r.inner(v)) {
         __stcs(reinterpret_cast<uint4*>(out + e0), pack(f));
         return;
@@ -161,22 +170,45 @@ __device__ __forceinline__ void store_vec(const RowView<T>& r, T* out, bool on_g
 
 // Rewrites the gradient at the teacher's tokens among elements [e_lo, e_hi):
 // (share(z) - sum of q over the slots of that token) * scale, by the first slot of
-// each token.  Call after a barrier behind the plain writes.
+// each token, whose warp adds up the others in a fixed order.  Call after a barrier
+// behind the plain writes.
 template <typename T, typename F>
 __device__ __forceinline__ void fix_tokens(const Teacher& t, int K, T* out, int e_lo, int e_hi,
                                            float scale, F share) {
-    for (int k = threadIdx.x; k < K; k += kRowThreads) {
-        const int id = t.id[k];
-        if (id < e_lo || id >= e_hi) continue;
-        bool first = true;
-        float q = 0.f;
-        for (int j = 0; j < K; ++j) {
-            if (t.id[j] != id) continue;
-            first = first && j >= k;
-            q += t.q[j];
+    const int lane = threadIdx.x & 31;
+    for (int k0 = threadIdx.x - lane; k0 < K; k0 += kRowThreads) {
+        const int mine = k0 + lane < K ? t.id[k0 + lane] : -1;
+        unsigned left = __ballot_sync(0xffffffffu, mine >= e_lo && mine < e_hi);
+        while (left != 0) {
+            const int k = k0 + __ffs(left) - 1;
+            left &= left - 1;
+            const int id = t.id[k];
+            int first = K;
+            float q = 0.f;
+            for (int j = lane; j < K; j += 32) {
+                if (t.id[j] != id) continue;
+                first = min(first, j);
+                q += t.q[j];
+            }
+            first = __reduce_min_sync(0xffffffffu, first);
+            q = warp_sum(q);
+            if (lane == 0 && first == k) out[id] = from_f32<T>((share(t.z[k]) - q) * scale);
         }
-        if (first) out[id] = from_f32<T>((share(t.z[k]) - q) * scale);
     }
+}
+
+// Joins up to 8 slices' (maximum, sum); every lane gets the result.
+__device__ __forceinline__ MaxSum join(const MaxSum* ms, int n, float c) {
+    const int i = threadIdx.x & 7;
+    const MaxSum one = i < n ? ms[i] : MaxSum{neg_inf(), 0.f};
+    float m = one.max;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float s = one.sum;
+    if (one.max != neg_inf()) s *= Power(m, c).against(Power(one.max, c));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return {m, s};
 }
 
 // One cluster per row: lse and loss, and the gradient when GRAD.
@@ -200,7 +232,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
     const float weight = a.weight != nullptr ? a.weight[row] : 1.f;
     if (weight == 0.f) {  // the whole cluster leaves: the row's logits are not read
         if (GRAD) {
-            const float zero[E] = {};
+            const f32x2 zero[E / 2] = {};
             for (int v = sl.wlo + lane; v < sl.whi; v += 32) store_vec<T>(r, out, on_grid, v, zero);
         }
         if (rank == 0 && tid == 0) {
@@ -211,14 +243,14 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
     }
     if (cs > 1) cluster_arrive();  // met by cluster_wait below: every CTA has started
 
-    const uint32_t stage0 = smem_u32(smem) - (uint32_t)sl.lo * 16u;
+    const uint4* staged = reinterpret_cast<const uint4*>(smem) - sl.lo;
     if (STAGED) {
-        for (int v = sl.wlo + lane; v < sl.whi; v += 32) r.stage(v, stage0 + (uint32_t)v * 16u);
+        for (int v = sl.wlo + lane; v < sl.whi; v += 32) r.stage(v, smem_u32(staged + v));
     }
-    auto vec = [&](int v) { return STAGED ? lds_v4(stage0 + (uint32_t)v * 16u) : r.load(v); };
+    auto vec = [&](int v) { return STAGED ? staged[v] : r.load(v); };
 
     const Teacher t(smem + a.slice, a.K);
-    if (warp == 0) {
+    if (warp == kRowWarps - 1) {
         const float q = teacher_softmax(t, a.ids + (long long)row * a.K,
                                         a.teacher + (long long)row * a.K, a.K, a.V, a.inv_t,
                                         rank == 0 ? a.err_flag : nullptr);
@@ -236,32 +268,28 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
     for (int v = sl.wlo + lane; v < sl.whi; v += 32) m = fmaxf(m, vec_max<T>(vec(v)));
     m = warp_max(m);
     const Power pw(m, a.c);
-    float s = 0.f;
+    f32x2 sums[2] = {};
     auto sum_up = [&](auto fast) {
+#pragma unroll 2
         for (int v = sl.wlo + lane; v < sl.whi; v += 32) {
-            float f[E];
+            f32x2 f[E / 2];
             unpack(vec(v), f);
 #pragma unroll
-            for (int j = 0; j < E; ++j) s += pw.template of<fast.value>(f[j]);
+            for (int j = 0; j < E / 2; ++j) {
+                const float2 e = pw.template of<fast.value>(f[j]);
+                sums[j & 1] = add2(sums[j & 1], pair(e.x, e.y));
+            }
         }
     };
     if (pw.fast)
         sum_up(std::true_type{});
     else
         sum_up(std::false_type{});
-    s = warp_sum(s);
+    const float2 lanes = halves(add2(sums[0], sums[1]));
+    const float s = warp_sum(lanes.x + lanes.y);
     if (lane == 0) warp_ms[warp] = {m, s};
     __syncthreads();
-    auto join = [&](const MaxSum* ms, int n) {
-        MaxSum all{neg_inf(), 0.f};
-        for (int i = 0; i < n; ++i) all.max = fmaxf(all.max, ms[i].max);
-        const Power p(all.max, a.c);
-        for (int i = 0; i < n; ++i)
-            all.sum += ms[i].max == neg_inf() ? ms[i].sum
-                                              : ms[i].sum * p.against(Power(ms[i].max, a.c));
-        return all;
-    };
-    MaxSum all = join(warp_ms, kRowWarps);
+    MaxSum all = join(warp_ms, kRowWarps, a.c);
     if (cs > 1) {
         cluster_wait();
         if (tid < cs)
@@ -269,7 +297,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
                            __builtin_bit_cast(uint64_t, all));
         __syncwarp();
         cluster_sync();  // no CTA's shared memory is touched from outside after this
-        all = join(cta_ms, cs);
+        all = join(cta_ms, cs, a.c);
     }
     const Power pg(all.max, a.c);
     const float S = all.sum;
@@ -293,11 +321,15 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
         const float per_s = S == 0.f || warp_q == 0.f ? 0.f : 1.f / S;
         const float k = scale * per_s;
         auto write = [&](auto fast) {
+#pragma unroll 2
             for (int v = sl.wlo + lane; v < sl.whi; v += 32) {
-                float f[E];
+                f32x2 f[E / 2];
                 unpack(vec(v), f);
 #pragma unroll
-                for (int j = 0; j < E; ++j) f[j] = pg.template of<fast.value>(f[j]) * k;
+                for (int j = 0; j < E / 2; ++j) {
+                    const float2 e = pg.template of<fast.value>(f[j]);
+                    f[j] = mul2(pair(e.x, e.y), pair(k, k));
+                }
                 store_vec<T>(r, out, on_grid, v, f);
             }
         };
@@ -330,7 +362,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_grad_kernel(DistillArgs a
     const float weight = a.weight != nullptr ? a.weight[row] : 1.f;
     const float up = a.grad_loss[row];
     if (weight == 0.f || up == 0.f) {
-        const float zero[E] = {};
+        const f32x2 zero[E / 2] = {};
         for (int v = sl.wlo + lane; v < sl.whi; v += 32) store_vec<T>(r, out, on_grid, v, zero);
         return;
     }
@@ -352,11 +384,17 @@ __global__ void __launch_bounds__(kRowThreads) distill_grad_kernel(DistillArgs a
     auto share = [&](float z) {
         return lse == neg_inf() ? 0.f : ex2(fmaf(z, a.inv_t, -lse) * kLog2e);
     };
+    const float k = none || lse == neg_inf() ? 0.f : scale;
+    const f32x2 it = pair(a.inv_t, a.inv_t), nl = pair(-lse, -lse), le = pair(kLog2e, kLog2e);
+#pragma unroll 4
     for (int v = sl.wlo + lane; v < sl.whi; v += 32) {
-        float f[E];
+        f32x2 f[E / 2];
         unpack(r.load(v), f);
 #pragma unroll
-        for (int j = 0; j < E; ++j) f[j] = none ? 0.f : share(f[j]) * scale;
+        for (int j = 0; j < E / 2; ++j) {
+            const float2 d = halves(mul2(fma2(f[j], it, nl), le));
+            f[j] = k == 0.f ? 0 : mul2(pair(ex2(d.x), ex2(d.y)), pair(k, k));
+        }
         store_vec<T>(r, out, on_grid, v, f);
     }
     if (none) return;

@@ -37,19 +37,55 @@ __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
-// One vector's elements in fp32, in index order.
-__device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
-    f[0] = __uint_as_float(v.x);
-    f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z);
-    f[3] = __uint_as_float(v.w);
+// Two fp32 values in a register pair: one instruction works on both, which
+// leaves the issue slots that these kernels run out of first.
+using f32x2 = uint64_t;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
 }
-__device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+__device__ __forceinline__ float2 halves(f32x2 p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// One vector's elements in fp32, in index order.
+__device__ __forceinline__ void unpack(const uint4& v, f32x2 (&f)[2]) {
+    f[0] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ void unpack(const uint4& v, f32x2 (&f)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i)
+        f[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+template <int E>
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[E]) {
+    f32x2 p[E / 2];
+    unpack(v, p);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+        const float2 h = halves(p[i]);
+        f[2 * i] = h.x;
+        f[2 * i + 1] = h.y;
     }
 }
 
@@ -72,6 +108,30 @@ __device__ __forceinline__ float vec_max<__nv_bfloat16>(const uint4& v) {
     return fmaxf(__low2float(c), __high2float(c));
 }
 
+// The same, but NaN where one of the elements is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+template <typename T>
+__device__ __forceinline__ float vec_max_or_nan(const uint4& v);
+template <>
+__device__ __forceinline__ float vec_max_or_nan<float>(const uint4& v) {
+    return max_or_nan(max_or_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                      max_or_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+template <>
+__device__ __forceinline__ float vec_max_or_nan<__nv_bfloat16>(const uint4& v) {
+    const __nv_bfloat162 a = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v.x),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&v.y));
+    const __nv_bfloat162 b = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v.z),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&v.w));
+    const __nv_bfloat162 c = __hmax2_nan(a, b);
+    return max_or_nan(__low2float(c), __high2float(c));
+}
+
+// Four or eight fp32 values as one vector, rounded to the row's type.
 __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                       __float_as_uint(f[3]));
@@ -102,17 +162,17 @@ struct RowView {
     int head;       // places before element 0 in that vector
     int V;
     int nvec;
+    int ilo, ihi;   // the vectors that hold nothing else than the row's elements
 
     __device__ __forceinline__ RowView(const void* base, long long ld, int r, int V_) : V(V_) {
         row = static_cast<const T*>(base) + (long long)r * ld;
         head = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
         grid = row - head;
         nvec = (head + V + E - 1) / E;
+        ilo = head > 0 ? 1 : 0;
+        ihi = (head + V) / E;
     }
-    // Whether every place of vector v is an element of the row.
-    __device__ __forceinline__ bool inner(int v) const {
-        return v * E >= head && v * E + E <= head + V;
-    }
+    __device__ __forceinline__ bool inner(int v) const { return v >= ilo && v < ihi; }
     // Vector v by guarded loads of single elements, -inf in the places outside the row.
     __device__ __forceinline__ uint4 edge(int v) const {
         float f[E];
