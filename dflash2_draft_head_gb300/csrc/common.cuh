@@ -178,7 +178,7 @@ struct DistillArgs {
     void* grad;            // [rows, V], rows `grad_ld` elements apart
     long long grad_ld;
     int32_t* err_flag;
-    int cs = 1, slice = 0; // set by the launcher: CTAs per row, bytes of a staged slice
+    int lg = 0, per = 0, slice = 0;  // the split of a row, set by the launcher
 };
 constexpr int kDistillMaxK = 1024;
 constexpr int kDistillMaxV = 1 << 28;
@@ -201,7 +201,7 @@ struct SampleArgs {
     int rows, V;
     int32_t* tokens;
     float* probs;        // [rows] or nullptr
-    int cs = 1, slice = 0;
+    int lg = 0, per = 0;  // the split of a row, set by the launcher
 };
 // Largest V: the fixed-point sums of a row stay inside 62 bits, and those of a
 // CTA's histogram inside their words.

@@ -60,31 +60,39 @@ struct Teacher {
     }
 };
 
-// Softmax of the row's K teacher logits by one warp; returns 1, or 0 when the
-// row has no entry with a share.  A token outside [0, V) is an empty slot; one
-// that is not negative is flagged too.
-__device__ float teacher_softmax(const Teacher& t, const int32_t* ids, const float* logits, int K,
-                                 int V, float inv_t, int32_t* err_flag) {
+// A row's tokens, teacher logits and, for the tokens among elements [e_lo, e_hi), the
+// student's logits, by one warp.  A token outside [0, V) is an empty slot; one that
+// is not negative is flagged too.
+template <typename T>
+__device__ __forceinline__ void teacher_load(const Teacher& t, const DistillArgs& a, int row,
+                                             const T* z, int e_lo, int e_hi, bool flag) {
+    const int lane = threadIdx.x & 31;
+    for (int k = lane; k < a.K; k += 32) {
+        int id = a.ids[(long long)row * a.K + k];
+        t.lq[k] = a.teacher[(long long)row * a.K + k];
+        if (id < 0 || id >= a.V) {
+            if (id >= a.V && flag && a.err_flag != nullptr) atomicOr(a.err_flag, DF2_FLAG_BAD_ID);
+            id = -1;
+        }
+        t.id[k] = id;
+        if (id >= e_lo && id < e_hi) t.z[k] = to_f32(z[id]);
+    }
+}
+
+// Softmax of the loaded teacher logits by the same warp; returns 1, or 0 when the row
+// has no entry with a share.
+__device__ __forceinline__ float teacher_softmax(const Teacher& t, int K, float inv_t) {
     const int lane = threadIdx.x & 31;
     float m = neg_inf();
     bool nan = false;  // fmaxf drops it
     for (int k = lane; k < K; k += 32) {
-        int id = ids[k];
-        float y = logits[k];
-        if (id < 0 || id >= V) {
-            if (id >= V && err_flag != nullptr) atomicOr(err_flag, DF2_FLAG_BAD_ID);
-            id = -1;
-            y = neg_inf();
-        }
-        t.id[k] = id;
-        t.lq[k] = y;
-        m = fmaxf(m, y);
-        nan = nan || y != y;
+        if (t.id[k] < 0) t.lq[k] = neg_inf();
+        m = fmaxf(m, t.lq[k]);
+        nan = nan || t.lq[k] != t.lq[k];
     }
     m = __any_sync(0xffffffffu, nan) ? __int_as_float(0x7fffffff) : warp_max(m);
     if (m == neg_inf()) {
         for (int k = lane; k < K; k += 32) t.q[k] = 0.f;
-        __syncwarp();
         return 0.f;
     }
     float s = 0.f;
@@ -96,7 +104,6 @@ __device__ float teacher_softmax(const Teacher& t, const int32_t* ids, const flo
         t.q[k] = t.id[k] < 0 ? 0.f : expf(y) / s;
         t.lq[k] = y - ls;
     }
-    __syncwarp();
     return 1.f;
 }
 
@@ -197,18 +204,24 @@ __device__ __forceinline__ void fix_tokens(const Teacher& t, int K, T* out, int 
     }
 }
 
-// Joins up to 8 slices' (maximum, sum); every lane gets the result.
+// Joins n slices' (maximum, sum); every lane gets the result.
 __device__ __forceinline__ MaxSum join(const MaxSum* ms, int n, float c) {
-    const int i = threadIdx.x & 7;
-    const MaxSum one = i < n ? ms[i] : MaxSum{neg_inf(), 0.f};
-    float m = one.max;
+    constexpr int kPer = kRowMaxCluster * kRowWarps / 32;
+    const int lane = threadIdx.x & 31;
+    MaxSum one[kPer];
+    float m = neg_inf(), s = 0.f;
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float s = one.sum;
-    if (one.max != neg_inf()) s *= Power(m, c).against(Power(one.max, c));
+    for (int i = 0; i < kPer; ++i) {
+        one[i] = lane + 32 * i < n ? ms[lane + 32 * i] : MaxSum{neg_inf(), 0.f};
+        m = fmaxf(m, one[i].max);
+    }
+    m = warp_max(m);
+    const Power p(m, c);
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return {m, s};
+    for (int i = 0; i < kPer; ++i)
+        s += one[i].max == neg_inf() ? one[i].sum
+                                     : one[i].sum * p.against(Power(one[i].max, c));
+    return {m, warp_sum(s)};
 }
 
 // One cluster per row: lse and loss, and the gradient when GRAD.
@@ -216,15 +229,14 @@ template <typename T, bool GRAD, bool STAGED>
 __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
     constexpr int E = VecOf<T>::kElems;
     extern __shared__ __align__(16) char smem[];
-    __shared__ MaxSum warp_ms[kRowWarps];
-    __shared__ float warp_q;                      // 1, or 0 without a teacher
-    __shared__ MaxSum cta_ms[kRowMaxCluster];     // every CTA's
+    __shared__ MaxSum parts[kRowMaxCluster * kRowWarps];  // every warp of the row
+    __shared__ float has_teacher;                         // 1 or 0
 
-    const int cs = a.cs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cs = 1 << a.lg, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = cs > 1 ? (int)cluster_ctarank() : 0;
-    const int row = blockIdx.x / cs;
+    const int row = blockIdx.x >> a.lg;
     const RowView<T> r(a.logits, a.ld, row, a.V);
-    const RowSlice sl(r.nvec, rank, cs, warp);
+    const RowSlice sl(r.nvec, a.per, rank, warp);
     const int e_lo = max(sl.lo * E - r.head, 0), e_hi = min(sl.hi * E - r.head, a.V);
     T* out = GRAD ? static_cast<T*>(a.grad) + (long long)row * a.grad_ld : nullptr;
     const bool on_grid =
@@ -250,17 +262,9 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
     auto vec = [&](int v) { return STAGED ? staged[v] : r.load(v); };
 
     const Teacher t(smem + a.slice, a.K);
-    if (warp == kRowWarps - 1) {
-        const float q = teacher_softmax(t, a.ids + (long long)row * a.K,
-                                        a.teacher + (long long)row * a.K, a.K, a.V, a.inv_t,
-                                        rank == 0 ? a.err_flag : nullptr);
-        // z at the teacher's tokens: rank 0 needs all of them, the others their own
-        for (int k = lane; k < a.K; k += 32) {
-            const int id = t.id[k];
-            if (id >= 0 && (rank == 0 || (id >= e_lo && id < e_hi))) t.z[k] = to_f32(r.row[id]);
-        }
-        if (lane == 0) warp_q = q;
-    }
+    // rank 0, which makes the loss, needs z at all of the teacher's tokens
+    if (warp == kRowWarps - 1)
+        teacher_load(t, a, row, r.row, rank == 0 ? 0 : e_lo, rank == 0 ? a.V : e_hi, rank == 0);
     if (STAGED) cp_async_wait_all();
 
     // this warp's base and sum
@@ -287,21 +291,30 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
         sum_up(std::false_type{});
     const float2 lanes = halves(add2(sums[0], sums[1]));
     const float s = warp_sum(lanes.x + lanes.y);
-    if (lane == 0) warp_ms[warp] = {m, s};
-    __syncthreads();
-    MaxSum all = join(warp_ms, kRowWarps, a.c);
+    const int me = rank * kRowWarps + warp;
     if (cs > 1) {
         cluster_wait();
-        if (tid < cs)
-            st_cluster_b64(map_cluster(smem_u32(&cta_ms[rank]), tid),
-                           __builtin_bit_cast(uint64_t, all));
+        if (lane < cs)
+            st_cluster_b64(map_cluster(smem_u32(&parts[me]), lane),
+                           __builtin_bit_cast(uint64_t, MaxSum{m, s}));
         __syncwarp();
-        cluster_sync();  // no CTA's shared memory is touched from outside after this
-        all = join(cta_ms, cs, a.c);
+        cluster_arrive();
+    } else if (lane == 0) {
+        parts[me] = {m, s};
     }
+    if (warp == kRowWarps - 1) {
+        const float q = teacher_softmax(t, a.K, a.inv_t);
+        if (lane == 0) has_teacher = q;
+    }
+    if (cs > 1) {
+        __syncwarp();
+        cluster_wait();  // no CTA's shared memory is touched from outside after this
+    }
+    __syncthreads();
+    const MaxSum all = join(parts, cs * kRowWarps, a.c);
     const Power pg(all.max, a.c);
     const float S = all.sum;
-    if (rank == 0 && warp == 0) {
+    if (rank == 0 && warp == kRowWarps - 1) {
         const float ls = log2f(S);
         double loss = 0;
         for (int k = lane; k < a.K; k += 32)
@@ -310,7 +323,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
         loss = warp_sum(loss);
         if (lane == 0) {
             // no logit above -inf: the student gives the teacher's tokens no share
-            if (S == 0.f) loss = warp_q == 0.f ? 0.0 : (double)INFINITY;
+            if (S == 0.f) loss = has_teacher == 0.f ? 0.0 : (double)INFINITY;
             a.loss[row] = (float)(weight * loss);
             a.lse[row] = S == 0.f ? neg_inf() : (float)((double)kLn2 * (pg.base() + ls));
         }
@@ -318,7 +331,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
     if (GRAD) {
         // without a teacher the whole gradient is 0
         const float scale = weight * a.inv_t;
-        const float per_s = S == 0.f || warp_q == 0.f ? 0.f : 1.f / S;
+        const float per_s = S == 0.f || has_teacher == 0.f ? 0.f : 1.f / S;
         const float k = scale * per_s;
         auto write = [&](auto fast) {
 #pragma unroll 2
@@ -337,24 +350,24 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
             write(std::true_type{});
         else
             write(std::false_type{});
-        if (warp_q == 0.f) return;
+        if (has_teacher == 0.f) return;
         __syncthreads();
         fix_tokens<T>(t, a.K, out, e_lo, e_hi, scale,
                       [&](float z) { return pg(z) * per_s; });
     }
 }
 
-// The gradient alone, from lse and the upstream gradient: `cs` CTAs a row, which
-// do not wait on one another.
+// The gradient alone, from lse and the upstream gradient: the CTAs of a row do not
+// wait on one another.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) distill_grad_kernel(DistillArgs a) {
     constexpr int E = VecOf<T>::kElems;
     extern __shared__ __align__(16) char smem[];
-    __shared__ float warp_q;
+    __shared__ float has_teacher;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = blockIdx.x / a.cs, rank = blockIdx.x % a.cs;
+    const int row = blockIdx.x, rank = blockIdx.y;
     const RowView<T> r(a.logits, a.ld, row, a.V);
-    const RowSlice sl(r.nvec, rank, a.cs, warp);
+    const RowSlice sl(r.nvec, a.per, rank, warp);
     const int e_lo = max(sl.lo * E - r.head, 0), e_hi = min(sl.hi * E - r.head, a.V);
     T* out = static_cast<T*>(a.grad) + (long long)row * a.grad_ld;
     const bool on_grid =
@@ -366,36 +379,47 @@ __global__ void __launch_bounds__(kRowThreads) distill_grad_kernel(DistillArgs a
         for (int v = sl.wlo + lane; v < sl.whi; v += 32) store_vec<T>(r, out, on_grid, v, zero);
         return;
     }
+    // batches of kBatch vectors a lane, the next one's loads ahead of this one's stores
+    constexpr int kBatch = 4;
+    uint4 ahead[kBatch];
+    auto load = [&](int v0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (v0 + 32 * i < sl.whi) ahead[i] = r.load(v0 + 32 * i);
+    };
+    load(sl.wlo + lane);
     const Teacher t(smem, a.K);
     if (warp == 0) {
-        const float q = teacher_softmax(t, a.ids + (long long)row * a.K,
-                                        a.teacher + (long long)row * a.K, a.K, a.V, a.inv_t,
-                                        rank == 0 ? a.err_flag : nullptr);
-        for (int k = lane; k < a.K; k += 32) {
-            const int id = t.id[k];
-            if (id >= e_lo && id < e_hi) t.z[k] = to_f32(r.row[id]);
-        }
-        if (lane == 0) warp_q = q;
+        teacher_load(t, a, row, r.row, e_lo, e_hi, rank == 0);
+        const float q = teacher_softmax(t, a.K, a.inv_t);
+        if (lane == 0) has_teacher = q;
     }
     __syncthreads();  // also: z is read before the gradient may take its place
     const float scale = up * weight * a.inv_t;
     const float lse = a.lse[row];
-    const bool none = warp_q == 0.f;
+    const bool none = has_teacher == 0.f;
     auto share = [&](float z) {
         return lse == neg_inf() ? 0.f : ex2(fmaf(z, a.inv_t, -lse) * kLog2e);
     };
     const float k = none || lse == neg_inf() ? 0.f : scale;
     const f32x2 it = pair(a.inv_t, a.inv_t), nl = pair(-lse, -lse), le = pair(kLog2e, kLog2e);
-#pragma unroll 4
-    for (int v = sl.wlo + lane; v < sl.whi; v += 32) {
-        f32x2 f[E / 2];
-        unpack(r.load(v), f);
+    for (int v0 = sl.wlo + lane; v0 < sl.whi; v0 += 32 * kBatch) {
+        uint4 now[kBatch];
 #pragma unroll
-        for (int j = 0; j < E / 2; ++j) {
-            const float2 d = halves(mul2(fma2(f[j], it, nl), le));
-            f[j] = k == 0.f ? 0 : mul2(pair(ex2(d.x), ex2(d.y)), pair(k, k));
+        for (int i = 0; i < kBatch; ++i) now[i] = ahead[i];
+        load(v0 + 32 * kBatch);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (v0 + 32 * i >= sl.whi) break;
+            f32x2 f[E / 2];
+            unpack(now[i], f);
+#pragma unroll
+            for (int j = 0; j < E / 2; ++j) {
+                const float2 d = halves(mul2(fma2(f[j], it, nl), le));
+                f[j] = k == 0.f ? 0 : mul2(pair(ex2(d.x), ex2(d.y)), pair(k, k));
+            }
+            store_vec<T>(r, out, on_grid, v0 + 32 * i, f);
         }
-        store_vec<T>(r, out, on_grid, v, f);
     }
     if (none) return;
     __syncthreads();
@@ -403,21 +427,20 @@ __global__ void __launch_bounds__(kRowThreads) distill_grad_kernel(DistillArgs a
 }
 
 template <typename T, bool GRAD>
-cudaError_t launch_typed(const DistillArgs& a, bool staged, size_t smem, cudaStream_t stream) {
-    return launch_rows(staged ? distill_kernel<T, GRAD, true> : distill_kernel<T, GRAD, false>, a,
-                       a.rows, a.cs, smem, stream);
+cudaError_t launch_typed(const DistillArgs& a, size_t smem, cudaStream_t stream) {
+    return launch_rows(a.slice != 0 ? distill_kernel<T, GRAD, true> : distill_kernel<T, GRAD, false>,
+                       a, a.rows, a.lg, smem, stream);
 }
 
 template <typename T>
 cudaError_t launch_grad(DistillArgs a, size_t smem, cudaStream_t stream, int num_sms) {
-    // The CTAs of a row do not wait on one another, so any number of them will do:
-    // slices of kGradSlice bytes, smaller ones down to kRowSliceMin with few rows.
-    constexpr long long kGradSlice = 32 * 1024;
-    const long long bytes = row_max_vecs(a.V, sizeof(T)) * 16;
-    const long long want = std::min((2LL * num_sms + a.rows - 1) / a.rows, bytes / kRowSliceMin);
-    a.cs = (int)std::min(std::max({1LL, (bytes + kGradSlice - 1) / kGradSlice, want}),
-                         0x7fffffffLL / a.rows);
-    distill_grad_kernel<T><<<(unsigned)((long long)a.rows * a.cs), kRowThreads, smem, stream>>>(a);
+    // Slices of kGradSlice bytes, smaller ones down to kRowSliceMin with few rows.
+    constexpr long long kGradSlice = 64 * 1024;
+    const long long vecs = row_max_vecs(a.V, sizeof(T)), bytes = vecs * 16;
+    const long long want = std::min((4LL * num_sms + a.rows - 1) / a.rows, bytes / kRowSliceMin);
+    const long long n = std::max({1LL, (bytes + kGradSlice - 1) / kGradSlice, want});
+    a.per = (int)((vecs + n - 1) / n);
+    distill_grad_kernel<T><<<dim3(a.rows, (unsigned)n), kRowThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -429,15 +452,16 @@ cudaError_t launch_distill(DistillArgs a, int bf16, cudaStream_t stream, int num
     if (a.grad_loss != nullptr)
         return bf16 ? launch_grad<__nv_bfloat16>(a, teacher, stream, num_sms)
                     : launch_grad<float>(a, teacher, stream, num_sms);
-    const RowPlan p = plan_rows(a.rows, a.V, bf16 ? 2 : 4, num_sms, max_smem - teacher - 1024);
-    a.cs = p.cs;
-    a.slice = (int)p.slice;
-    const size_t smem = p.slice + teacher;
+    const RowSplit p = split_rows(a.rows, a.V, bf16 ? 2 : 4, num_sms, max_smem - teacher - 2048);
+    a.lg = p.lg;
+    a.per = p.per;
+    a.slice = p.staged;
+    const size_t smem = p.staged + teacher;
     if (bf16)
-        return a.grad != nullptr ? launch_typed<__nv_bfloat16, true>(a, p.staged, smem, stream)
-                                 : launch_typed<__nv_bfloat16, false>(a, p.staged, smem, stream);
-    return a.grad != nullptr ? launch_typed<float, true>(a, p.staged, smem, stream)
-                             : launch_typed<float, false>(a, p.staged, smem, stream);
+        return a.grad != nullptr ? launch_typed<__nv_bfloat16, true>(a, smem, stream)
+                                 : launch_typed<__nv_bfloat16, false>(a, smem, stream);
+    return a.grad != nullptr ? launch_typed<float, true>(a, smem, stream)
+                             : launch_typed<float, false>(a, smem, stream);
 }
 
 }  // namespace df2

@@ -195,13 +195,12 @@ struct RowView {
     }
 };
 
-// Which vectors of a row a CTA (rank of cs) and one of its warps work on: both
-// splits are in index order.  Warp slices start on 128-byte lines.
+// Which vectors of a row a CTA (the rank-th, `per` vectors each) and one of its warps
+// work on: both splits are in index order.  Warp slices start on 128-byte lines.
 struct RowSlice {
     int lo, hi;    // the CTA's vectors
     int wlo, whi;  // this warp's
-    __device__ __forceinline__ RowSlice(int nvec, int rank, int cs, int warp) {
-        const int per = (nvec + cs - 1) / cs;
+    __device__ __forceinline__ RowSlice(int nvec, int per, int rank, int warp) {
         lo = min(rank * per, nvec);
         hi = min(lo + per, nvec);
         const int pw = ((hi - lo + kRowWarps - 1) / kRowWarps + 7) & ~7;
@@ -210,11 +209,11 @@ struct RowSlice {
     }
 };
 
-// How a [rows, V] array is split over clusters (host).
-struct RowPlan {
-    int cs;        // CTAs per row (the cluster's size, a power of two)
-    bool staged;   // a CTA's slice is held in shared memory
-    size_t slice;  // bytes of it (0 when not staged)
+// How a [rows, V] array is split over clusters.
+struct RowSplit {
+    int lg;      // log2 of the CTAs per row (the cluster's size)
+    int per;     // vectors of a row per CTA
+    int staged;  // bytes of a slice held in shared memory, or 0
 };
 
 // 16-byte vectors of a row of V elements of `es` bytes, wherever it starts.
@@ -227,37 +226,38 @@ inline long long row_max_vecs(long long V, size_t es) {
 // with another's arithmetic); with few rows, smaller ones, so that more SMs take part.
 constexpr long long kRowSliceBytes = 40 * 1024;
 constexpr long long kRowSliceMin = 8 * 1024;
-inline RowPlan plan_rows(int rows, int V, size_t es, int num_sms, size_t max_slice) {
+inline RowSplit split_rows(int rows, int V, size_t es, int num_sms, size_t max_slice) {
     const long long vecs = row_max_vecs(V, es), bytes = vecs * 16;
-    int cs = 1;
-    while (cs < kRowMaxCluster && bytes / cs > kRowSliceBytes) cs *= 2;
-    while (cs < kRowMaxCluster && (long long)rows * cs < 2LL * num_sms && bytes / cs > kRowSliceMin)
-        cs *= 2;
-    const long long slice = (vecs + cs - 1) / cs * 16;
-    const bool staged = slice <= (long long)max_slice;
-    return {cs, staged, staged ? (size_t)slice : 0};
+    int lg = 0;
+    while (1 << lg < kRowMaxCluster &&
+           (bytes >> lg > kRowSliceBytes ||
+            ((long long)rows << lg < 2LL * num_sms && bytes >> lg > kRowSliceMin)))
+        ++lg;
+    const long long per = (vecs + (1 << lg) - 1) >> lg;
+    return {lg, (int)per, per * 16 <= (long long)max_slice ? (int)(per * 16) : 0};
 }
 
-// Launches `rows` clusters of cs CTAs.
+// Launches `rows` clusters of 2^lg CTAs.
 template <typename Args>
-cudaError_t launch_rows(void (*kernel)(Args), const Args& a, int rows, int cs, size_t smem,
+cudaError_t launch_rows(void (*kernel)(Args), const Args& a, int rows, int lg, size_t smem,
                         cudaStream_t stream) {
-    if (smem > 32 * 1024) {  // with the static arrays this may pass the default 48 KB
-        const cudaError_t e = cudaFuncSetAttribute(
-            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    cudaError_t e = cudaSuccess;
+    if (smem > 24 * 1024)  // with the static arrays this may pass the default 48 KB
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && 1 << lg > 8)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)rows * cs));
+    cfg.gridDim = dim3((unsigned)((long long)rows << lg));
     cfg.blockDim = dim3(kRowThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)cs;
+    attr.val.clusterDim.x = 1u << lg;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = cs > 1 ? 1 : 0;
+    cfg.numAttrs = lg > 0 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 

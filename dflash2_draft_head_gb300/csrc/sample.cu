@@ -508,10 +508,10 @@ __global__ void __launch_bounds__(kRowThreads) sample_kernel(SampleArgs a) {
     __shared__ Shared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int cs = a.cs, rank = cs > 1 ? (int)cluster_ctarank() : 0;
-    const int rowi = blockIdx.x / cs;
+    const int cs = 1 << a.lg, rank = cs > 1 ? (int)cluster_ctarank() : 0;
+    const int rowi = blockIdx.x >> a.lg;
     const RowView<T> r(a.logits, a.ld, rowi, a.V);
-    const RowSlice sl(r.nvec, rank, cs, warp);
+    const RowSlice sl(r.nvec, a.per, rank, warp);
     const Row<T, STAGED> row{r, sl, reinterpret_cast<const uint4*>(smem) - sl.lo, cs, rank};
     if (cs > 1) cluster_arrive();  // met by cluster_wait below: every CTA has started
     if (STAGED) {
@@ -541,11 +541,13 @@ __global__ void __launch_bounds__(kRowThreads) sample_kernel(SampleArgs a) {
         const float other = __shfl_xor_sync(0xffffffffu, m, o);
         if (o < cs) m = fmaxf(m, other);
     }
-    if (tid % cs == 0) (cs > 1 ? sh.own_max : sh.group_max)[tid / cs] = m;
+    if ((tid & (cs - 1)) == 0) (cs > 1 ? sh.own_max : sh.group_max)[tid >> a.lg] = m;
     __syncthreads();
     if (cs > 1) {
         cluster_wait();
-        const int quads = kGroups / 4 / cs, to = tid / quads, i = tid % quads;
+        // kGroups / 4 of the threads send four maxima each to one of the CTAs
+        const int lq = 6 - a.lg, quads = 1 << lq, to = tid >> lq, i = tid & (quads - 1);
+        static_assert(kGroups / 4 == 1 << 6);
         if (to < cs)
             st_cluster_v4(map_cluster(smem_u32(&sh.group_max[4 * (rank * quads + i)]), to),
                           reinterpret_cast<const float4*>(sh.own_max)[i]);
@@ -776,15 +778,15 @@ __global__ void __launch_bounds__(kRowThreads) sample_kernel(SampleArgs a) {
 
 cudaError_t launch_sample(SampleArgs a, int bf16, cudaStream_t stream, int num_sms,
                           size_t max_smem) {
-    const RowPlan p = plan_rows(a.rows, a.V, bf16 ? 2 : 4, num_sms, max_smem - sizeof(Shared) - 1024);
-    a.cs = p.cs;
-    a.slice = (int)p.slice;
+    const RowSplit p = split_rows(a.rows, a.V, bf16 ? 2 : 4, num_sms, max_smem - sizeof(Shared) - 1024);
+    a.lg = p.lg;
+    a.per = p.per;
     if (bf16)
-        return launch_rows(p.staged ? sample_kernel<__nv_bfloat16, true>
-                                    : sample_kernel<__nv_bfloat16, false>,
-                           a, a.rows, a.cs, p.slice, stream);
-    return launch_rows(p.staged ? sample_kernel<float, true> : sample_kernel<float, false>, a,
-                       a.rows, a.cs, p.slice, stream);
+        return launch_rows(p.staged != 0 ? sample_kernel<__nv_bfloat16, true>
+                                         : sample_kernel<__nv_bfloat16, false>,
+                           a, a.rows, a.lg, p.staged, stream);
+    return launch_rows(p.staged != 0 ? sample_kernel<float, true> : sample_kernel<float, false>, a,
+                       a.rows, a.lg, p.staged, stream);
 }
 
 }  // namespace df2
