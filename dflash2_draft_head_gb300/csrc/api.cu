@@ -264,8 +264,7 @@ int run_distill(const char* what, bool backward, df2::DistillArgs a, float tempe
     if (a.V > df2::kDistillMaxV)
         return fail(DF2_ERR_UNSUPPORTED, "%s: V=%d > %d", what, a.V, df2::kDistillMaxV);
     cudaError_t e = df2::launch_distill(a, dtype == DF2_BF16, static_cast<cudaStream_t>(stream),
-                                        num_sms_of_current_device(),
-                                        max_smem_optin_of_current_device());
+                                        num_sms_of_current_device());
     if (e != cudaSuccess) return cuda_fail(e, what);
     return DF2_OK;
 }
@@ -650,8 +649,7 @@ int dflash2_sample(const void* logits, long long ld, const float* uniform,
     df2::SampleArgs a{logits, ld, uniform, temperature, top_k, top_p, min_p, temperature_all,
                       top_k_all, top_p_all, min_p_all, rows, V, tokens, probs};
     cudaError_t e = df2::launch_sample(a, in_dtype == DF2_BF16, static_cast<cudaStream_t>(stream),
-                                       num_sms_of_current_device(),
-                                       max_smem_optin_of_current_device());
+                                       num_sms_of_current_device());
     if (e != cudaSuccess) return cuda_fail(e, "sample launch");
     return DF2_OK;
 }

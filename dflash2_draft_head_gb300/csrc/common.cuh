@@ -178,12 +178,11 @@ struct DistillArgs {
     void* grad;            // [rows, V], rows `grad_ld` elements apart
     long long grad_ld;
     int32_t* err_flag;
-    int lg = 0, per = 0, slice = 0;  // the split of a row, set by the launcher
+    int lg = 0, per = 0, ring = 0;  // the split of a row, set by the launcher
 };
 constexpr int kDistillMaxK = 1024;
 constexpr int kDistillMaxV = 1 << 28;
-cudaError_t launch_distill(DistillArgs a, int bf16, cudaStream_t stream, int num_sms,
-                           size_t max_smem);
+cudaError_t launch_distill(DistillArgs a, int bf16, cudaStream_t stream, int num_sms);
 
 // One token of every row by temperature, top-k, top-p and min-p (sample.cu).  A
 // setting's pointer, when not nullptr, has a value for every row.
@@ -201,13 +200,12 @@ struct SampleArgs {
     int rows, V;
     int32_t* tokens;
     float* probs;        // [rows] or nullptr
-    int lg = 0, per = 0;  // the split of a row, set by the launcher
+    int lg = 0, per = 0, ring = 0;  // the split of a row, set by the launcher
 };
 // Largest V: the fixed-point sums of a row stay inside 62 bits, and those of a
 // CTA's histogram inside their words.
 constexpr int kSampleMaxV = 1 << 21;
-cudaError_t launch_sample(SampleArgs a, int bf16, cudaStream_t stream, int num_sms,
-                          size_t max_smem);
+cudaError_t launch_sample(SampleArgs a, int bf16, cudaStream_t stream, int num_sms);
 
 // Measurement aid: random-row gather (probe.cu).  out[i] = XOR of the 32-bit
 // words of row ids[i] (ids clamped into [0, rows)); row_bytes a power of two

@@ -6,10 +6,9 @@
 //   loss  = weight * sum_k q_k (log q_k - z[id_k] / T + lse)
 //   dz_j  = weight * g * (exp(z_j / T - lse) - sum_{k: id_k = j} q_k) / T
 //
-// Bound by HBM: the logits are read once and the gradient is written once.  A
-// row is split over the CTAs of a cluster, each holding its slice in shared
-// memory between the two uses (the sum of exponentials, then the gradient),
-// which only a (max, sum) pair per CTA crosses.
+// Bound by HBM: the logits are read once and the gradient is written once.  A CTA,
+// or the CTAs of a cluster, take a row through the two uses of it (the sum of
+// exponentials, then the gradient), which only a (max, sum) pair per warp crosses.
 //
 // All exponentials are powers of two with c = log2(e)/T folded in: a slice's
 // sum is taken against its own rounded base b = c * max, 2^(c*z - b) being one
@@ -21,7 +20,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "common.cuh"
 #include "dflash2.h"
@@ -120,11 +118,14 @@ struct Power {
     __device__ __forceinline__ float operator()(float z) const {
         return ex2(fast ? fmaf(z, c, nb) : (z - m) * c);
     }
-    template <bool FAST>
-    __device__ __forceinline__ float2 of(f32x2 z) const {
-        const float2 d = halves(FAST ? fma2(z, pair(c, c), pair(nb, nb))
-                                     : mul2(add2(z, pair(-m, -m)), pair(c, c)));
-        return make_float2(ex2(d.x), ex2(d.y));
+    // the powers of a vector's logits, in their place (fast)
+    template <int N>
+    __device__ __forceinline__ void of(f32x2 (&z)[N]) const {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float2 d = halves(fma2(z[j], pair(c, c), pair(nb, nb)));
+            z[j] = pair(ex2(d.x), ex2(d.y));
+        }
     }
     // 2^(another's base - base)
     __device__ __forceinline__ float against(const Power& o) const {
@@ -137,11 +138,32 @@ struct Power {
     }
 };
 
-// A slice's largest logit and the sum of its powers against that (0, or NaN, where
-// nothing is above -inf).
+// The powers of a vector's logits where the base is not fast, times k: their sum, or
+// themselves as a vector.  Calls, so that the fast path stays free of them.
+template <typename T>
+__device__ __noinline__ float slow_sum(uint4 v, float m, float c) {
+    constexpr int E = VecOf<T>::kElems;
+    float f[E], s = 0.f;
+    unpack(v, f);
+    for (int j = 0; j < E; ++j) s += ex2((f[j] - m) * c);
+    return s;
+}
+template <typename T>
+__device__ __noinline__ uint4 slow_grad(uint4 v, float m, float c, float k) {
+    constexpr int E = VecOf<T>::kElems;
+    float f[E];
+    unpack(v, f);
+#pragma unroll
+    for (int j = 0; j < E; ++j) f[j] = ex2((f[j] - m) * c) * k;
+    return pack(f);
+}
+
+// A part of a row: a logit as base (the largest, or one that is not 2^kSlack times
+// below it; -inf where nothing is above that) and the sum of the powers against it.
 struct alignas(8) MaxSum {  // goes to other CTAs as one 64-bit store
     float max, sum;
 };
+constexpr float kSlack = 60.f;
 
 template <typename T>
 __device__ __forceinline__ T from_f32(float x);
@@ -152,27 +174,24 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
     return __float2bfloat16_rn(x);
 }
 
-// Writes vector v of a gradient row: one 16-byte store where the gradient's row
-// lies on the logits' grid, else (and at the row's edges) element by element.
+// Writes vector v of a gradient row: one 16-byte store where it is whole and the
+// gradient's row lies on the logits' grid, else element by element.
 template <typename T>
-__device__ __forceinline__ void store_vec(const RowView<T>& r, T* out, bool on_grid, int v,
-                                          const f32x2 (&p)[VecOf<T>::kElems / 2]) {
+__device__ __noinline__ void store_edge(const RowView<T> r, T* out, int v, const uint4 vec) {
     constexpr int E = VecOf<T>::kElems;
-    const int e0 = v * E - r.head;
-    float f[E];
-#pragma unroll
-    for (int j = 0; j < E / 2; ++j) {
-        const float2 h = halves(p[j]);
-        f[2 * j] = h.x;
-        f[2 * j + 1] = h.y;
+    const T* f = reinterpret_cast<const T*>(&vec);
+    for (int j = 0; j < E; ++j) {
+        const int e = v * E - r.head + j;
+        if (e >= 0 && e < r.V) out[e] = f[j];
     }
-    if (on_grid && r.inner(v)) {
-        __stcs(reinterpret_cast<uint4*>(out + e0), pack(f));
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < E; ++j)
-        if (e0 + j >= 0 && e0 + j < r.V) out[e0 + j] = from_f32<T>(f[j]);
+}
+template <typename T>
+__device__ __forceinline__ void store_vec(const RowView<T>& r, T* out, bool wide, int v, int v_hi,
+                                          const uint4& vec) {
+    if (wide)
+        __stcs(reinterpret_cast<uint4*>(out + ((long long)v * VecOf<T>::kElems - r.head)), vec);
+    else if (v < v_hi)
+        store_edge(r, out, v, vec);
 }
 
 // Rewrites the gradient at the teacher's tokens among elements [e_lo, e_hi):
@@ -206,27 +225,19 @@ __device__ __forceinline__ void fix_tokens(const Teacher& t, int K, T* out, int 
 
 // Joins n slices' (maximum, sum); every lane gets the result.
 __device__ __forceinline__ MaxSum join(const MaxSum* ms, int n, float c) {
-    constexpr int kPer = kRowMaxCluster * kRowWarps / 32;
     const int lane = threadIdx.x & 31;
-    MaxSum one[kPer];
     float m = neg_inf(), s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        one[i] = lane + 32 * i < n ? ms[lane + 32 * i] : MaxSum{neg_inf(), 0.f};
-        m = fmaxf(m, one[i].max);
-    }
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, ms[i].max);
     m = warp_max(m);
     const Power p(m, c);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        s += one[i].max == neg_inf() ? one[i].sum
-                                     : one[i].sum * p.against(Power(one[i].max, c));
+    for (int i = lane; i < n; i += 32)
+        s += ms[i].max == neg_inf() ? ms[i].sum : ms[i].sum * p.against(Power(ms[i].max, c));
     return {m, warp_sum(s)};
 }
 
 // One cluster per row: lse and loss, and the gradient when GRAD.
-template <typename T, bool GRAD, bool STAGED>
-__global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
+template <typename T, bool GRAD>
+__global__ void __launch_bounds__(kRowThreads, kRowCtasPerSm) distill_kernel(DistillArgs a) {
     constexpr int E = VecOf<T>::kElems;
     extern __shared__ __align__(16) char smem[];
     __shared__ MaxSum parts[kRowMaxCluster * kRowWarps];  // every warp of the row
@@ -236,7 +247,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
     const int rank = cs > 1 ? (int)cluster_ctarank() : 0;
     const int row = blockIdx.x >> a.lg;
     const RowView<T> r(a.logits, a.ld, row, a.V);
-    const RowSlice sl(r.nvec, a.per, rank, warp);
+    RowSlice sl(r, a.per, a.ring, rank, warp, smem + (size_t)a.K * 16);
     const int e_lo = max(sl.lo * E - r.head, 0), e_hi = min(sl.hi * E - r.head, a.V);
     T* out = GRAD ? static_cast<T*>(a.grad) + (long long)row * a.grad_ld : nullptr;
     const bool on_grid =
@@ -244,8 +255,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
     const float weight = a.weight != nullptr ? a.weight[row] : 1.f;
     if (weight == 0.f) {  // the whole cluster leaves: the row's logits are not read
         if (GRAD) {
-            const f32x2 zero[E / 2] = {};
-            for (int v = sl.wlo + lane; v < sl.whi; v += 32) store_vec<T>(r, out, on_grid, v, zero);
+            for (int v = sl.wlo + lane; v < sl.whi; v += 32) store_vec<T>(r, out, on_grid && r.inner(v), v, sl.whi, make_uint4(0, 0, 0, 0));
         }
         if (rank == 0 && tid == 0) {
             a.loss[row] = 0.f;
@@ -255,42 +265,45 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
     }
     if (cs > 1) cluster_arrive();  // met by cluster_wait below: every CTA has started
 
-    const uint4* staged = reinterpret_cast<const uint4*>(smem) - sl.lo;
-    if (STAGED) {
-        for (int v = sl.wlo + lane; v < sl.whi; v += 32) r.stage(v, smem_u32(staged + v));
-    }
-    auto vec = [&](int v) { return STAGED ? staged[v] : r.load(v); };
-
-    const Teacher t(smem + a.slice, a.K);
+    sl.start(r);
+    const Teacher t(smem, a.K);
     // rank 0, which makes the loss, needs z at all of the teacher's tokens
     if (warp == kRowWarps - 1)
         teacher_load(t, a, row, r.row, rank == 0 ? 0 : e_lo, rank == 0 ? a.V : e_hi, rank == 0);
-    if (STAGED) cp_async_wait_all();
-
-    // this warp's base and sum
-    float m = neg_inf();
-    for (int v = sl.wlo + lane; v < sl.whi; v += 32) m = fmaxf(m, vec_max<T>(vec(v)));
-    m = warp_max(m);
-    const Power pw(m, a.c);
+    // each lane's base, changed only for a logit 2^kSlack times above it, and the sum of
+    // the powers against it (in halves); then the warp's
+    Power pw(neg_inf(), a.c);
+    float m = neg_inf(), m_most = neg_inf(), slow = 0.f;
+    const float slack = kSlack / a.c;
     f32x2 sums[2] = {};
-    auto sum_up = [&](auto fast) {
-#pragma unroll 2
-        for (int v = sl.wlo + lane; v < sl.whi; v += 32) {
-            f32x2 f[E / 2];
-            unpack(vec(v), f);
-#pragma unroll
-            for (int j = 0; j < E / 2; ++j) {
-                const float2 e = pw.template of<fast.value>(f[j]);
-                sums[j & 1] = add2(sums[j & 1], pair(e.x, e.y));
-            }
+    sl.pass(r, [&](int, const uint4& v, bool) {
+        const float most = vec_max<T>(v);
+        if (most > m_most) {
+            const Power up(most, a.c);
+            const float by = m == neg_inf() ? 1.f : up.against(pw);
+            sums[0] = mul2(sums[0], pair(by, by));
+            sums[1] = mul2(sums[1], pair(by, by));
+            slow *= by;
+            m = most;
+            m_most = m + slack;
+            pw = up;
         }
-    };
-    if (pw.fast)
-        sum_up(std::true_type{});
-    else
-        sum_up(std::false_type{});
+        if (!pw.fast) {
+            slow += slow_sum<T>(v, pw.m, a.c);
+            return;
+        }
+        f32x2 f[E / 2];
+        unpack(v, f);
+        pw.of(f);
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) sums[j & 1] = add2(sums[j & 1], f[j]);
+    });
     const float2 lanes = halves(add2(sums[0], sums[1]));
-    const float s = warp_sum(lanes.x + lanes.y);
+    float s = lanes.x + lanes.y + slow;
+    const float lane_m = m;
+    m = warp_max(m);
+    if (lane_m != neg_inf()) s *= Power(m, a.c).against(pw);
+    s = warp_sum(s);
     const int me = rank * kRowWarps + warp;
     if (cs > 1) {
         cluster_wait();
@@ -333,23 +346,19 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
         const float scale = weight * a.inv_t;
         const float per_s = S == 0.f || has_teacher == 0.f ? 0.f : 1.f / S;
         const float k = scale * per_s;
-        auto write = [&](auto fast) {
-#pragma unroll 2
-            for (int v = sl.wlo + lane; v < sl.whi; v += 32) {
-                f32x2 f[E / 2];
-                unpack(vec(v), f);
-#pragma unroll
-                for (int j = 0; j < E / 2; ++j) {
-                    const float2 e = pg.template of<fast.value>(f[j]);
-                    f[j] = mul2(pair(e.x, e.y), pair(k, k));
-                }
-                store_vec<T>(r, out, on_grid, v, f);
+        sl.pass(r, [&](int v, const uint4& vec, bool whole) {
+            if (!pg.fast) {
+                store_vec<T>(r, out, whole && on_grid, v, sl.whi,
+                             slow_grad<T>(vec, pg.m, a.c, k));
+                return;
             }
-        };
-        if (pg.fast)
-            write(std::true_type{});
-        else
-            write(std::false_type{});
+            f32x2 f[E / 2];
+            unpack(vec, f);
+            pg.of(f);
+#pragma unroll
+            for (int j = 0; j < E / 2; ++j) f[j] = mul2(f[j], pair(k, k));
+            store_vec<T>(r, out, whole && on_grid, v, sl.whi, pack_pairs(f));
+        });
         if (has_teacher == 0.f) return;
         __syncthreads();
         fix_tokens<T>(t, a.K, out, e_lo, e_hi, scale,
@@ -360,14 +369,14 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a) {
 // The gradient alone, from lse and the upstream gradient: the CTAs of a row do not
 // wait on one another.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) distill_grad_kernel(DistillArgs a) {
+__global__ void __launch_bounds__(kRowThreads, kRowCtasPerSm) distill_grad_kernel(DistillArgs a) {
     constexpr int E = VecOf<T>::kElems;
     extern __shared__ __align__(16) char smem[];
     __shared__ float has_teacher;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x, rank = blockIdx.y;
     const RowView<T> r(a.logits, a.ld, row, a.V);
-    const RowSlice sl(r.nvec, a.per, rank, warp);
+    RowSlice sl(r, a.per, a.ring, rank, warp, smem + (size_t)a.K * 16);
     const int e_lo = max(sl.lo * E - r.head, 0), e_hi = min(sl.hi * E - r.head, a.V);
     T* out = static_cast<T*>(a.grad) + (long long)row * a.grad_ld;
     const bool on_grid =
@@ -375,19 +384,10 @@ __global__ void __launch_bounds__(kRowThreads) distill_grad_kernel(DistillArgs a
     const float weight = a.weight != nullptr ? a.weight[row] : 1.f;
     const float up = a.grad_loss[row];
     if (weight == 0.f || up == 0.f) {
-        const f32x2 zero[E / 2] = {};
-        for (int v = sl.wlo + lane; v < sl.whi; v += 32) store_vec<T>(r, out, on_grid, v, zero);
+        for (int v = sl.wlo + lane; v < sl.whi; v += 32) store_vec<T>(r, out, on_grid && r.inner(v), v, sl.whi, make_uint4(0, 0, 0, 0));
         return;
     }
-    // batches of kBatch vectors a lane, the next one's loads ahead of this one's stores
-    constexpr int kBatch = 4;
-    uint4 ahead[kBatch];
-    auto load = [&](int v0) {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            if (v0 + 32 * i < sl.whi) ahead[i] = r.load(v0 + 32 * i);
-    };
-    load(sl.wlo + lane);
+    sl.start(r);
     const Teacher t(smem, a.K);
     if (warp == 0) {
         teacher_load(t, a, row, r.row, e_lo, e_hi, rank == 0);
@@ -403,65 +403,51 @@ __global__ void __launch_bounds__(kRowThreads) distill_grad_kernel(DistillArgs a
     };
     const float k = none || lse == neg_inf() ? 0.f : scale;
     const f32x2 it = pair(a.inv_t, a.inv_t), nl = pair(-lse, -lse), le = pair(kLog2e, kLog2e);
-    for (int v0 = sl.wlo + lane; v0 < sl.whi; v0 += 32 * kBatch) {
-        uint4 now[kBatch];
+    sl.pass(r, [&](int v, const uint4& vec, bool whole) {
+        f32x2 f[E / 2];
+        unpack(vec, f);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) now[i] = ahead[i];
-        load(v0 + 32 * kBatch);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (v0 + 32 * i >= sl.whi) break;
-            f32x2 f[E / 2];
-            unpack(now[i], f);
-#pragma unroll
-            for (int j = 0; j < E / 2; ++j) {
-                const float2 d = halves(mul2(fma2(f[j], it, nl), le));
-                f[j] = k == 0.f ? 0 : mul2(pair(ex2(d.x), ex2(d.y)), pair(k, k));
-            }
-            store_vec<T>(r, out, on_grid, v0 + 32 * i, f);
+        for (int j = 0; j < E / 2; ++j) {
+            const float2 d = halves(mul2(fma2(f[j], it, nl), le));
+            f[j] = mul2(pair(ex2(d.x), ex2(d.y)), pair(k, k));
         }
-    }
+        store_vec<T>(r, out, whole && on_grid, v, sl.whi,
+                     k == 0.f ? make_uint4(0, 0, 0, 0) : pack_pairs(f));
+    });
     if (none) return;
     __syncthreads();
     fix_tokens<T>(t, a.K, out, e_lo, e_hi, scale, share);
 }
 
-template <typename T, bool GRAD>
-cudaError_t launch_typed(const DistillArgs& a, size_t smem, cudaStream_t stream) {
-    return launch_rows(a.slice != 0 ? distill_kernel<T, GRAD, true> : distill_kernel<T, GRAD, false>,
-                       a, a.rows, a.lg, smem, stream);
-}
-
 template <typename T>
 cudaError_t launch_grad(DistillArgs a, size_t smem, cudaStream_t stream, int num_sms) {
-    // Slices of kGradSlice bytes, smaller ones down to kRowSliceMin with few rows.
-    constexpr long long kGradSlice = 64 * 1024;
-    const long long vecs = row_max_vecs(a.V, sizeof(T)), bytes = vecs * 16;
-    const long long want = std::min((4LL * num_sms + a.rows - 1) / a.rows, bytes / kRowSliceMin);
-    const long long n = std::max({1LL, (bytes + kGradSlice - 1) / kGradSlice, want});
-    a.per = (int)((vecs + n - 1) / n);
-    distill_grad_kernel<T><<<dim3(a.rows, (unsigned)n), kRowThreads, smem, stream>>>(a);
+    const RowSplit p = split_rows(a.rows, a.V, sizeof(T), num_sms);
+    a.per = p.per;
+    a.ring = p.ring;
+    smem += (size_t)a.ring * kRingStepBytes;
+    const cudaError_t e = cudaFuncSetAttribute(
+        distill_grad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    distill_grad_kernel<T><<<dim3(a.rows, 1u << p.lg), kRowThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_distill(DistillArgs a, int bf16, cudaStream_t stream, int num_sms,
-                           size_t max_smem) {
+cudaError_t launch_distill(DistillArgs a, int bf16, cudaStream_t stream, int num_sms) {
     const size_t teacher = (size_t)a.K * 16;
     if (a.grad_loss != nullptr)
         return bf16 ? launch_grad<__nv_bfloat16>(a, teacher, stream, num_sms)
                     : launch_grad<float>(a, teacher, stream, num_sms);
-    const RowSplit p = split_rows(a.rows, a.V, bf16 ? 2 : 4, num_sms, max_smem - teacher - 2048);
+    const RowSplit p = split_rows(a.rows, a.V, bf16 ? 2 : 4, num_sms);
     a.lg = p.lg;
     a.per = p.per;
-    a.slice = p.staged;
-    const size_t smem = p.staged + teacher;
-    if (bf16)
-        return a.grad != nullptr ? launch_typed<__nv_bfloat16, true>(a, smem, stream)
-                                 : launch_typed<__nv_bfloat16, false>(a, smem, stream);
-    return a.grad != nullptr ? launch_typed<float, true>(a, smem, stream)
-                             : launch_typed<float, false>(a, smem, stream);
+    a.ring = p.ring;
+    const auto kernel = bf16 ? (a.grad != nullptr ? distill_kernel<__nv_bfloat16, true>
+                                                  : distill_kernel<__nv_bfloat16, false>)
+                             : (a.grad != nullptr ? distill_kernel<float, true>
+                                                  : distill_kernel<float, false>);
+    return launch_rows(kernel, a, a.rows, a.lg, p.smem + teacher, stream);
 }
 
 }  // namespace df2

@@ -118,6 +118,15 @@ __device__ __forceinline__ void cp_async_wait_all() {
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// cp.async groups of this thread: closes one, waits until at most N are under way.
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Bulk copy from this CTA's shared memory to another CTA of the cluster
 // (dst and bar are shared::cluster addresses from mapa), completing `bytes`
 // of transaction count on the destination CTA's mbarrier.

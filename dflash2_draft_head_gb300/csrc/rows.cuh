@@ -1,26 +1,34 @@
 // Shared by the operators that work on whole vocabulary rows (sampling and
-// distillation): a row of V elements as 16-byte vectors, split over the CTAs of
-// a thread-block cluster and, inside a CTA, over its warps in index order.
+// distillation): a row of V elements as 16-byte vectors, held by one CTA or split over
+// the CTAs of a thread-block cluster and, inside a CTA, over its warps in index order.
 //
 // A row may start at any element: the vectors lie on the 16-byte grid of memory,
 // so the first and the last one may hold places that are not the row's.  Those
 // are never read; they get the fill value -inf, which no operator counts.
-// Each thread copies the vectors that it works on itself (cp.async into shared
-// memory), so a row's slice needs no barrier before it is read.
+//
+// A row is passed over one or more times and read from HBM once: every warp streams its
+// part through a ring in shared memory (cp.async, each lane the vectors that it works on
+// itself, so there is no barrier), and every other pass runs backwards, so that it
+// starts on what the ring still holds; the rest comes again from L2.  Two CTAs share an
+// SM, so that one's loads run under the other's arithmetic and barriers.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "ptx.cuh"
 
 namespace df2 {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 512;
+constexpr int kRowCtasPerSm = 2;
+constexpr int kRingSteps = 5;  // steps of kStepVecs vectors a warp that the ring holds
+constexpr int kStepVecs = 64;
 constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kRowMaxCluster = 8;
+constexpr int kRowMaxCluster = 16;
 
 template <typename T>
 struct VecOf;
@@ -146,6 +154,18 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+template <int N>
+__device__ __forceinline__ uint4 pack_pairs(const f32x2 (&p)[N]) {
+    float f[2 * N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const float2 h = halves(p[j]);
+        f[2 * j] = h.x;
+        f[2 * j + 1] = h.y;
+    }
+    return pack(f);
+}
+
 // 2^x, flushing results below 2^-126 to 0 (relative error about 2^-22).
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -186,34 +206,111 @@ struct RowView {
     __device__ __forceinline__ uint4 load(int v) const {
         return inner(v) ? *reinterpret_cast<const uint4*>(grid + (long long)v * E) : edge(v);
     }
-    // Vector v into shared memory at dst: asynchronous but for the row's two edges.
-    __device__ __forceinline__ void stage(int v, uint32_t dst) const {
-        if (inner(v))
-            cp_async16(dst, grid + (long long)v * E);
-        else
-            st_shared_v4(dst, edge(v));
-    }
 };
 
 // Which vectors of a row a CTA (the rank-th, `per` vectors each) and one of its warps
-// work on: both splits are in index order.  Warp slices start on 128-byte lines.
+// work on, and the warp's ring of `ring` steps in shared memory.  Both splits are in
+// index order, warps' parts start on 128-byte lines.
 struct RowSlice {
-    int lo, hi;    // the CTA's vectors
-    int wlo, whi;  // this warp's
-    __device__ __forceinline__ RowSlice(int nvec, int per, int rank, int warp) {
-        lo = min(rank * per, nvec);
-        hi = min(lo + per, nvec);
+    static constexpr uint32_t kStepBytes = kStepVecs * 16;
+    int lo, hi;      // the CTA's vectors
+    int wlo, whi;    // this warp's
+    int steps;       // the last one may be short
+    int clean_lo, clean_hi;  // steps of nothing but whole vectors of the row
+    uint32_t slots;  // this lane's place in the ring
+    bool up = true;  // the direction of the next pass
+
+    template <typename T>
+    __device__ __forceinline__ RowSlice(const RowView<T>& r, int per, int ring, int rank, int warp,
+                                        const char* smem) {
+        lo = min(rank * per, r.nvec);
+        hi = min(lo + per, r.nvec);
         const int pw = ((hi - lo + kRowWarps - 1) / kRowWarps + 7) & ~7;
         wlo = min(lo + warp * pw, hi);
         whi = min(wlo + pw, hi);
+        steps = (whi - wlo + kStepVecs - 1) / kStepVecs;
+        clean_lo = wlo < r.ilo ? 1 : 0;
+        clean_hi = max(min(whi, r.ihi) - wlo, 0) / kStepVecs;
+        slots = smem_u32(smem) + (uint32_t)(warp * ring * kStepVecs + (threadIdx.x & 31)) * 16u;
+    }
+    __device__ __forceinline__ bool clean(int step) const {
+        return step >= clean_lo && step < clean_hi;
+    }
+    // A step that is not clean, from vector v on: -inf in the places beyond the warp's.
+    template <typename T>
+    static __device__ __noinline__ void load_edge(const RowView<T> r, int v, int whi, uint32_t at) {
+        for (int i = 0; i < kStepVecs; i += 32, v += 32) {
+            if (v < whi && r.inner(v))
+                cp_async16(at + 16u * i, r.grid + (long long)v * RowView<T>::E);
+            else
+                st_shared_v4(at + 16u * i, r.edge(v < whi ? v : r.nvec));
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void load(const RowView<T>& r, int step, const char* src,
+                                         uint32_t at) const {
+        if (clean(step)) {
+#pragma unroll
+            for (int i = 0; i < kStepVecs; i += 32) cp_async16(at + 16u * i, src + 16 * i);
+        } else if ((unsigned)step < (unsigned)steps) {
+            load_edge(r, wlo + step * kStepVecs + (int)(threadIdx.x & 31), whi, at);
+        }
+    }
+    // This lane's first vector of a step.
+    template <typename T>
+    __device__ __forceinline__ const char* source(const RowView<T>& r, int step) const {
+        return reinterpret_cast<const char*>(r.grid) +
+               ((long long)wlo + (long long)step * kStepVecs + (threadIdx.x & 31)) * 16;
+    }
+    // Fills the ring for a first pass.  A step's copies are a group of their own, and
+    // kRingSteps groups are always under way or done.
+    template <typename T>
+    __device__ __forceinline__ void start(const RowView<T>& r) const {
+        const char* src = source(r, 0);
+#pragma unroll 1
+        for (int i = 0; i < kRingSteps; ++i) {
+            load(r, i, src, slots + i * kStepBytes);
+            cp_async_commit();
+            src += kStepBytes;
+        }
+    }
+    // f(vector's number, vector, whether it is whole) for this lane's vectors, and for
+    // some of nothing but -inf beyond the warp's
+    template <typename T, typename F>
+    __device__ __forceinline__ void pass(const RowView<T>& r, F f) {
+        const int by = up ? 1 : -1;
+        int i = up ? 0 : steps - 1;
+        uint32_t at = slots + (up ? 0 : max(i, 0) % kRingSteps) * kStepBytes;
+        const char* src = source(r, i + by * kRingSteps);
+        const uint32_t end = slots + kRingSteps * kStepBytes;
+#pragma unroll 1
+        for (int n = steps; n > 0; --n) {
+            cp_async_wait_group<kRingSteps - 1>();
+            const int v = wlo + i * kStepVecs + (int)(threadIdx.x & 31);
+            const bool whole = clean(i);
+            uint4 now[kStepVecs / 32];
+#pragma unroll
+            for (int h = 0; h < kStepVecs / 32; ++h) now[h] = lds_v4(at + h * 512);
+#pragma unroll
+            for (int h = 0; h < kStepVecs / 32; ++h) f(v + 32 * h, now[h], whole);
+            load(r, i + by * kRingSteps, src, at);
+            cp_async_commit();
+            i += by;
+            src += by * (int)kStepBytes;
+            at += by * (int)kStepBytes;
+            if (at == end) at = slots;
+            if (at < slots) at = end - kStepBytes;
+        }
+        up = !up;
     }
 };
 
 // How a [rows, V] array is split over clusters.
 struct RowSplit {
-    int lg;      // log2 of the CTAs per row (the cluster's size)
-    int per;     // vectors of a row per CTA
-    int staged;  // bytes of a slice held in shared memory, or 0
+    int lg;    // log2 of the CTAs per row (the cluster's size)
+    int per;   // vectors of a row per CTA
+    int ring;  // steps of a warp's ring
+    int smem;  // bytes of a CTA's rings
 };
 
 // 16-byte vectors of a row of V elements of `es` bytes, wherever it starts.
@@ -222,19 +319,27 @@ inline long long row_max_vecs(long long V, size_t es) {
     return (V + 2 * (E - 1)) / E;
 }
 
-// Slices of at most kRowSliceBytes (several CTAs of an SM then overlap one's loads
-// with another's arithmetic); with few rows, smaller ones, so that more SMs take part.
-constexpr long long kRowSliceBytes = 40 * 1024;
-constexpr long long kRowSliceMin = 8 * 1024;
-inline RowSplit split_rows(int rows, int V, size_t es, int num_sms, size_t max_slice) {
+inline int ring_steps(long long per) {
+    const long long warp = ((per + kRowWarps - 1) / kRowWarps + 7) & ~7LL;
+    return (int)std::min((long long)kRingSteps, (warp + kStepVecs - 1) / kStepVecs);
+}
+constexpr int kRingStepBytes = kRowWarps * kStepVecs * 16;  // of a CTA
+
+// Slices of at most kRowSliceBytes, so that what is read again comes from L2; with few
+// rows, smaller ones, so that every SM takes part.
+constexpr long long kRowSliceBytes = 320 * 1024;
+constexpr long long kRowSliceMin = 16 * 1024;
+inline RowSplit split_rows(int rows, int V, size_t es, int num_sms) {
     const long long vecs = row_max_vecs(V, es), bytes = vecs * 16;
     int lg = 0;
     while (1 << lg < kRowMaxCluster &&
            (bytes >> lg > kRowSliceBytes ||
-            ((long long)rows << lg < 2LL * num_sms && bytes >> lg > kRowSliceMin)))
+            ((long long)rows << lg < (long long)kRowCtasPerSm * num_sms &&
+             bytes >> lg > kRowSliceMin)))
         ++lg;
     const long long per = (vecs + (1 << lg) - 1) >> lg;
-    return {lg, (int)per, per * 16 <= (long long)max_slice ? (int)(per * 16) : 0};
+    const int ring = ring_steps(per);
+    return {lg, (int)per, ring, ring * kRingStepBytes};
 }
 
 // Launches `rows` clusters of 2^lg CTAs.
@@ -242,7 +347,7 @@ template <typename Args>
 cudaError_t launch_rows(void (*kernel)(Args), const Args& a, int rows, int lg, size_t smem,
                         cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
-    if (smem > 24 * 1024)  // with the static arrays this may pass the default 48 KB
+    if (smem > 16 * 1024)  // with the static arrays this may pass the default 48 KB
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess && 1 << lg > 8)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
