@@ -28,6 +28,9 @@
 namespace df2 {
 namespace {
 
+using Geo = RowGeometry<256, 4, 6, 160>;
+constexpr int kRowThreads = Geo::kThreads, kRowWarps = Geo::kWarps;
+
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.44269504088896341f;
 
@@ -138,32 +141,32 @@ struct Power {
     }
 };
 
-// The powers of a vector's logits where the base is not fast, times k: their sum, or
-// themselves as a vector.  Calls, so that the fast path stays free of them.
+// The powers of a vector's logits against any base: their sum, or themselves times k as
+// a vector.  Calls, so that the fast path stays free of them.
 template <typename T>
-__device__ __noinline__ float slow_sum(uint4 v, float m, float c) {
+__device__ __noinline__ float slow_sum(uint4 v, const Power p) {
     constexpr int E = VecOf<T>::kElems;
     float f[E], s = 0.f;
     unpack(v, f);
-    for (int j = 0; j < E; ++j) s += ex2((f[j] - m) * c);
+#pragma unroll
+    for (int j = 0; j < E; ++j) s += p(f[j]);
     return s;
 }
 template <typename T>
-__device__ __noinline__ uint4 slow_grad(uint4 v, float m, float c, float k) {
+__device__ __noinline__ uint4 slow_grad(uint4 v, const Power p, float k) {
     constexpr int E = VecOf<T>::kElems;
     float f[E];
     unpack(v, f);
 #pragma unroll
-    for (int j = 0; j < E; ++j) f[j] = ex2((f[j] - m) * c) * k;
+    for (int j = 0; j < E; ++j) f[j] = p(f[j]) * k;
     return pack(f);
 }
 
-// A part of a row: a logit as base (the largest, or one that is not 2^kSlack times
-// below it; -inf where nothing is above that) and the sum of the powers against it.
+// A part of a row: a logit as base (not far below the largest; -inf where nothing is
+// above that) and the sum of the powers against it.
 struct alignas(8) MaxSum {  // goes to other CTAs as one 64-bit store
     float max, sum;
 };
-constexpr float kSlack = 60.f;
 
 template <typename T>
 __device__ __forceinline__ T from_f32(float x);
@@ -189,7 +192,7 @@ template <typename T>
 __device__ __forceinline__ void store_vec(const RowView<T>& r, T* out, bool wide, int v, int v_hi,
                                           const uint4& vec) {
     if (wide)
-        __stcs(reinterpret_cast<uint4*>(out + ((long long)v * VecOf<T>::kElems - r.head)), vec);
+        __stcs(reinterpret_cast<uint4*>(out - r.head) + v, vec);
     else if (v < v_hi)
         store_edge(r, out, v, vec);
 }
@@ -237,7 +240,7 @@ __device__ __forceinline__ MaxSum join(const MaxSum* ms, int n, float c) {
 
 // One cluster per row: lse and loss, and the gradient when GRAD.
 template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kRowThreads, kRowCtasPerSm) distill_kernel(DistillArgs a) {
+__global__ void __launch_bounds__(kRowThreads, Geo::kCtas) distill_kernel(DistillArgs a) {
     constexpr int E = VecOf<T>::kElems;
     extern __shared__ __align__(16) char smem[];
     __shared__ MaxSum parts[kRowMaxCluster * kRowWarps];  // every warp of the row
@@ -247,7 +250,8 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtasPerSm) distill_kernel(Dis
     const int rank = cs > 1 ? (int)cluster_ctarank() : 0;
     const int row = blockIdx.x >> a.lg;
     const RowView<T> r(a.logits, a.ld, row, a.V);
-    RowSlice sl(r, a.per, a.ring, rank, warp, smem + (size_t)a.K * 16);
+    RowSlice<Geo> sl(r, a.per, a.ring, rank, warp, smem + (size_t)a.K * 16,
+                GRAD ? l2_policy_evict_last() : l2_policy_evict_first());
     const int e_lo = max(sl.lo * E - r.head, 0), e_hi = min(sl.hi * E - r.head, a.V);
     T* out = GRAD ? static_cast<T*>(a.grad) + (long long)row * a.grad_ld : nullptr;
     const bool on_grid =
@@ -270,40 +274,38 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtasPerSm) distill_kernel(Dis
     // rank 0, which makes the loss, needs z at all of the teacher's tokens
     if (warp == kRowWarps - 1)
         teacher_load(t, a, row, r.row, rank == 0 ? 0 : e_lo, rank == 0 ? a.V : e_hi, rank == 0);
-    // each lane's base, changed only for a logit 2^kSlack times above it, and the sum of
-    // the powers against it (in halves); then the warp's
-    Power pw(neg_inf(), a.c);
-    float m = neg_inf(), m_most = neg_inf(), slow = 0.f;
-    const float slack = kSlack / a.c;
-    f32x2 sums[2] = {};
-    sl.pass(r, [&](int, const uint4& v, bool) {
-        const float most = vec_max<T>(v);
-        if (most > m_most) {
-            const Power up(most, a.c);
-            const float by = m == neg_inf() ? 1.f : up.against(pw);
-            sums[0] = mul2(sums[0], pair(by, by));
-            sums[1] = mul2(sums[1], pair(by, by));
-            slow *= by;
-            m = most;
-            m_most = m + slack;
-            pw = up;
-        }
-        if (!pw.fast) {
-            slow += slow_sum<T>(v, pw.m, a.c);
-            return;
-        }
-        f32x2 f[E / 2];
-        unpack(v, f);
-        pw.of(f);
+    // The warp's sum of powers against the largest logit of its first vectors: fp32 has
+    // room for sums 2^66 times above that.  Where one was larger (or the base was -inf,
+    // or a NaN is among them), once more against the largest of all.
+    float m = neg_inf(), s;
+    {
+        bool first = true;
+        Power pw(m, a.c);
+        f32x2 sums[2] = {};
+        sl.pass(r, [&](int, const uint4& v, bool) {
+            if (first) {
+                m = warp_max(vec_max<T>(v));
+                pw = Power(m, a.c);
+                first = false;
+            }
+            f32x2 f[E / 2];
+            unpack(v, f);
+            pw.of(f);
 #pragma unroll
-        for (int j = 0; j < E / 2; ++j) sums[j & 1] = add2(sums[j & 1], f[j]);
-    });
-    const float2 lanes = halves(add2(sums[0], sums[1]));
-    float s = lanes.x + lanes.y + slow;
-    const float lane_m = m;
-    m = warp_max(m);
-    if (lane_m != neg_inf()) s *= Power(m, a.c).against(pw);
-    s = warp_sum(s);
+            for (int j = 0; j < E / 2; ++j) sums[j & 1] = add2(sums[j & 1], f[j]);
+        });
+        const float2 lanes = halves(add2(sums[0], sums[1]));
+        s = warp_sum(lanes.x + lanes.y);
+        if (!(m > neg_inf() && pw.fast && s < 1e20f) && sl.steps > 0) {
+            m = neg_inf();
+            sl.pass(r, [&](int, const uint4& v, bool) { m = fmaxf(m, vec_max<T>(v)); });
+            m = warp_max(m);
+            const Power slow(m, a.c);
+            s = 0.f;
+            sl.pass(r, [&](int, const uint4& v, bool) { s += slow_sum<T>(v, slow); });
+            s = warp_sum(s);
+        }
+    }
     const int me = rank * kRowWarps + warp;
     if (cs > 1) {
         cluster_wait();
@@ -346,19 +348,25 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtasPerSm) distill_kernel(Dis
         const float scale = weight * a.inv_t;
         const float per_s = S == 0.f || has_teacher == 0.f ? 0.f : 1.f / S;
         const float k = scale * per_s;
-        sl.pass(r, [&](int v, const uint4& vec, bool whole) {
-            if (!pg.fast) {
-                store_vec<T>(r, out, whole && on_grid, v, sl.whi,
-                             slow_grad<T>(vec, pg.m, a.c, k));
-                return;
-            }
-            f32x2 f[E / 2];
-            unpack(vec, f);
-            pg.of(f);
+        sl.hint = l2_policy_evict_first();
+        if (pg.fast && on_grid) {
+            uint4* const at = reinterpret_cast<uint4*>(out - r.head);
+            sl.pass(r, [&](int v, const uint4& vec, bool whole) {
+                f32x2 f[E / 2];
+                unpack(vec, f);
+                pg.of(f);
 #pragma unroll
-            for (int j = 0; j < E / 2; ++j) f[j] = mul2(f[j], pair(k, k));
-            store_vec<T>(r, out, whole && on_grid, v, sl.whi, pack_pairs(f));
-        });
+                for (int j = 0; j < E / 2; ++j) f[j] = mul2(f[j], pair(k, k));
+                if (whole)
+                    __stcs(at + v, pack_pairs(f));
+                else if (v < sl.whi)
+                    store_edge(r, out, v, pack_pairs(f));
+            });
+        } else {
+            sl.pass(r, [&](int v, const uint4& vec, bool whole) {
+                store_vec<T>(r, out, whole && on_grid, v, sl.whi, slow_grad<T>(vec, pg, k));
+            });
+        }
         if (has_teacher == 0.f) return;
         __syncthreads();
         fix_tokens<T>(t, a.K, out, e_lo, e_hi, scale,
@@ -369,14 +377,15 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtasPerSm) distill_kernel(Dis
 // The gradient alone, from lse and the upstream gradient: the CTAs of a row do not
 // wait on one another.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, kRowCtasPerSm) distill_grad_kernel(DistillArgs a) {
+__global__ void __launch_bounds__(kRowThreads, Geo::kCtas) distill_grad_kernel(DistillArgs a) {
     constexpr int E = VecOf<T>::kElems;
     extern __shared__ __align__(16) char smem[];
     __shared__ float has_teacher;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x, rank = blockIdx.y;
     const RowView<T> r(a.logits, a.ld, row, a.V);
-    RowSlice sl(r, a.per, a.ring, rank, warp, smem + (size_t)a.K * 16);
+    RowSlice<Geo> sl(r, a.per, a.ring, rank, warp, smem + (size_t)a.K * 16,
+                l2_policy_evict_first());
     const int e_lo = max(sl.lo * E - r.head, 0), e_hi = min(sl.hi * E - r.head, a.V);
     T* out = static_cast<T*>(a.grad) + (long long)row * a.grad_ld;
     const bool on_grid =
@@ -421,10 +430,10 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtasPerSm) distill_grad_kerne
 
 template <typename T>
 cudaError_t launch_grad(DistillArgs a, size_t smem, cudaStream_t stream, int num_sms) {
-    const RowSplit p = split_rows(a.rows, a.V, sizeof(T), num_sms);
+    const RowSplit p = split_rows<Geo>(a.rows, a.V, sizeof(T), num_sms);
     a.per = p.per;
     a.ring = p.ring;
-    smem += (size_t)a.ring * kRingStepBytes;
+    smem += (size_t)a.ring * Geo::kStepBytes;
     const cudaError_t e = cudaFuncSetAttribute(
         distill_grad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -439,7 +448,7 @@ cudaError_t launch_distill(DistillArgs a, int bf16, cudaStream_t stream, int num
     if (a.grad_loss != nullptr)
         return bf16 ? launch_grad<__nv_bfloat16>(a, teacher, stream, num_sms)
                     : launch_grad<float>(a, teacher, stream, num_sms);
-    const RowSplit p = split_rows(a.rows, a.V, bf16 ? 2 : 4, num_sms);
+    const RowSplit p = split_rows<Geo>(a.rows, a.V, bf16 ? 2 : 4, num_sms);
     a.lg = p.lg;
     a.per = p.per;
     a.ring = p.ring;
@@ -447,7 +456,7 @@ cudaError_t launch_distill(DistillArgs a, int bf16, cudaStream_t stream, int num
                                                   : distill_kernel<__nv_bfloat16, false>)
                              : (a.grad != nullptr ? distill_kernel<float, true>
                                                   : distill_kernel<float, false>);
-    return launch_rows(kernel, a, a.rows, a.lg, p.smem + teacher, stream);
+    return launch_rows<Geo>(kernel, a, a.rows, a.lg, p.smem + teacher, stream);
 }
 
 }  // namespace df2

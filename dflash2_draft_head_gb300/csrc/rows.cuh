@@ -9,8 +9,8 @@
 // A row is passed over one or more times and read from HBM once: every warp streams its
 // part through a ring in shared memory (cp.async, each lane the vectors that it works on
 // itself, so there is no barrier), and every other pass runs backwards, so that it
-// starts on what the ring still holds; the rest comes again from L2.  Two CTAs share an
-// SM, so that one's loads run under the other's arithmetic and barriers.
+// starts on what the ring still holds; the rest comes again from L2.  Several CTAs share
+// an SM, so that one's loads run under another's arithmetic and barriers.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -23,12 +23,27 @@
 
 namespace df2 {
 
-constexpr int kRowThreads = 512;
-constexpr int kRowCtasPerSm = 2;
-constexpr int kRingSteps = 5;  // steps of kStepVecs vectors a warp that the ring holds
-constexpr int kStepVecs = 64;
-constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kRowMaxCluster = 16;
+constexpr int kStepVecs = 64;  // vectors that a warp handles between two waits
+
+// How a kernel takes rows: threads of a CTA, CTAs that share an SM, steps that a warp's
+// ring holds, and the largest part of a row that a CTA takes.
+template <int THREADS, int CTAS, int RING, int SLICE_KB>
+struct RowGeometry {
+    static constexpr int kThreads = THREADS, kWarps = THREADS / 32, kCtas = CTAS, kRing = RING;
+    static constexpr long long kSliceBytes = SLICE_KB * 1024;
+    static constexpr int kStepBytes = kWarps * kStepVecs * 16;  // a CTA's part of the ring, a step
+    // A warp's part of n vectors: whole steps where it has several (a short one costs as
+    // much as a whole one), else lines of 128 bytes.
+    static __host__ __device__ constexpr int warp_vecs(int n) {
+        const int even = (n + kWarps - 1) / kWarps;
+        return even > 4 * kStepVecs ? (even + kStepVecs - 1) / kStepVecs * kStepVecs
+                                    : (even + 7) & ~7;
+    }
+    static int ring_steps(int n) {
+        return std::min(kRing, (warp_vecs(n) + kStepVecs - 1) / kStepVecs);
+    }
+};
 
 template <typename T>
 struct VecOf;
@@ -203,6 +218,11 @@ struct RowView {
         }
         return pack(f);
     }
+    // A vector of -inf alone.
+    __device__ __forceinline__ uint4 nothing() const {
+        const uint32_t w = E == 8 ? 0xff80ff80u : 0xff800000u;
+        return make_uint4(w, w, w, w);
+    }
     __device__ __forceinline__ uint4 load(int v) const {
         return inner(v) ? *reinterpret_cast<const uint4*>(grid + (long long)v * E) : edge(v);
     }
@@ -211,6 +231,7 @@ struct RowView {
 // Which vectors of a row a CTA (the rank-th, `per` vectors each) and one of its warps
 // work on, and the warp's ring of `ring` steps in shared memory.  Both splits are in
 // index order, warps' parts start on 128-byte lines.
+template <typename G>
 struct RowSlice {
     static constexpr uint32_t kStepBytes = kStepVecs * 16;
     int lo, hi;      // the CTA's vectors
@@ -219,13 +240,15 @@ struct RowSlice {
     int clean_lo, clean_hi;  // steps of nothing but whole vectors of the row
     uint32_t slots;  // this lane's place in the ring
     bool up = true;  // the direction of the next pass
+    uint64_t hint;   // L2 policy of the loads
 
     template <typename T>
     __device__ __forceinline__ RowSlice(const RowView<T>& r, int per, int ring, int rank, int warp,
-                                        const char* smem) {
+                                        const char* smem, uint64_t hint_)
+        : hint(hint_) {
         lo = min(rank * per, r.nvec);
         hi = min(lo + per, r.nvec);
-        const int pw = ((hi - lo + kRowWarps - 1) / kRowWarps + 7) & ~7;
+        const int pw = G::warp_vecs(hi - lo);
         wlo = min(lo + warp * pw, hi);
         whi = min(wlo + pw, hi);
         steps = (whi - wlo + kStepVecs - 1) / kStepVecs;
@@ -242,8 +265,10 @@ struct RowSlice {
         for (int i = 0; i < kStepVecs; i += 32, v += 32) {
             if (v < whi && r.inner(v))
                 cp_async16(at + 16u * i, r.grid + (long long)v * RowView<T>::E);
+            else if (v < whi)
+                st_shared_v4(at + 16u * i, r.edge(v));
             else
-                st_shared_v4(at + 16u * i, r.edge(v < whi ? v : r.nvec));
+                st_shared_v4(at + 16u * i, r.nothing());
         }
     }
     template <typename T>
@@ -251,7 +276,7 @@ struct RowSlice {
                                          uint32_t at) const {
         if (clean(step)) {
 #pragma unroll
-            for (int i = 0; i < kStepVecs; i += 32) cp_async16(at + 16u * i, src + 16 * i);
+            for (int i = 0; i < kStepVecs; i += 32) cp_async16_hint(at + 16u * i, src + 16 * i, hint);
         } else if ((unsigned)step < (unsigned)steps) {
             load_edge(r, wlo + step * kStepVecs + (int)(threadIdx.x & 31), whi, at);
         }
@@ -263,12 +288,12 @@ struct RowSlice {
                ((long long)wlo + (long long)step * kStepVecs + (threadIdx.x & 31)) * 16;
     }
     // Fills the ring for a first pass.  A step's copies are a group of their own, and
-    // kRingSteps groups are always under way or done.
+    // G::kRing groups are always under way or done.
     template <typename T>
     __device__ __forceinline__ void start(const RowView<T>& r) const {
         const char* src = source(r, 0);
 #pragma unroll 1
-        for (int i = 0; i < kRingSteps; ++i) {
+        for (int i = 0; i < G::kRing; ++i) {
             load(r, i, src, slots + i * kStepBytes);
             cp_async_commit();
             src += kStepBytes;
@@ -280,12 +305,12 @@ struct RowSlice {
     __device__ __forceinline__ void pass(const RowView<T>& r, F f) {
         const int by = up ? 1 : -1;
         int i = up ? 0 : steps - 1;
-        uint32_t at = slots + (up ? 0 : max(i, 0) % kRingSteps) * kStepBytes;
-        const char* src = source(r, i + by * kRingSteps);
-        const uint32_t end = slots + kRingSteps * kStepBytes;
+        uint32_t at = slots + (up ? 0 : max(i, 0) % G::kRing) * kStepBytes;
+        const char* src = source(r, i + by * G::kRing);
+        const uint32_t end = slots + G::kRing * kStepBytes;
 #pragma unroll 1
         for (int n = steps; n > 0; --n) {
-            cp_async_wait_group<kRingSteps - 1>();
+            cp_async_wait_group<G::kRing - 1>();
             const int v = wlo + i * kStepVecs + (int)(threadIdx.x & 31);
             const bool whole = clean(i);
             uint4 now[kStepVecs / 32];
@@ -293,7 +318,7 @@ struct RowSlice {
             for (int h = 0; h < kStepVecs / 32; ++h) now[h] = lds_v4(at + h * 512);
 #pragma unroll
             for (int h = 0; h < kStepVecs / 32; ++h) f(v + 32 * h, now[h], whole);
-            load(r, i + by * kRingSteps, src, at);
+            load(r, i + by * G::kRing, src, at);
             cp_async_commit();
             i += by;
             src += by * (int)kStepBytes;
@@ -319,31 +344,23 @@ inline long long row_max_vecs(long long V, size_t es) {
     return (V + 2 * (E - 1)) / E;
 }
 
-inline int ring_steps(long long per) {
-    const long long warp = ((per + kRowWarps - 1) / kRowWarps + 7) & ~7LL;
-    return (int)std::min((long long)kRingSteps, (warp + kStepVecs - 1) / kStepVecs);
-}
-constexpr int kRingStepBytes = kRowWarps * kStepVecs * 16;  // of a CTA
-
-// Slices of at most kRowSliceBytes, so that what is read again comes from L2; with few
-// rows, smaller ones, so that every SM takes part.
-constexpr long long kRowSliceBytes = 320 * 1024;
+// Slices of at most G::kSliceBytes; with few rows smaller ones, so that every SM takes
+// part.
 constexpr long long kRowSliceMin = 16 * 1024;
-inline RowSplit split_rows(int rows, int V, size_t es, int num_sms) {
+template <typename G>
+RowSplit split_rows(int rows, int V, size_t es, int num_sms) {
     const long long vecs = row_max_vecs(V, es), bytes = vecs * 16;
     int lg = 0;
     while (1 << lg < kRowMaxCluster &&
-           (bytes >> lg > kRowSliceBytes ||
-            ((long long)rows << lg < (long long)kRowCtasPerSm * num_sms &&
-             bytes >> lg > kRowSliceMin)))
+           (bytes >> lg > G::kSliceBytes ||
+            ((long long)rows << lg < (long long)G::kCtas * num_sms && bytes >> lg > kRowSliceMin)))
         ++lg;
-    const long long per = (vecs + (1 << lg) - 1) >> lg;
-    const int ring = ring_steps(per);
-    return {lg, (int)per, ring, ring * kRingStepBytes};
+    const int per = (int)((vecs + (1 << lg) - 1) >> lg), ring = G::ring_steps(per);
+    return {lg, per, ring, ring * G::kStepBytes};
 }
 
 // Launches `rows` clusters of 2^lg CTAs.
-template <typename Args>
+template <typename G, typename Args>
 cudaError_t launch_rows(void (*kernel)(Args), const Args& a, int rows, int lg, size_t smem,
                         cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
@@ -354,7 +371,7 @@ cudaError_t launch_rows(void (*kernel)(Args), const Args& a, int rows, int lg, s
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)rows << lg));
-    cfg.blockDim = dim3(kRowThreads);
+    cfg.blockDim = dim3(G::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};

@@ -40,6 +40,9 @@ namespace {
 using u32 = uint32_t;
 using u64 = unsigned long long;
 
+using Geo = RowGeometry<512, 2, 5, 320>;
+constexpr int kRowThreads = Geo::kThreads, kRowWarps = Geo::kWarps;
+
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kOne = 1099511627776.f;  // 2^40, the largest entry's weight
 constexpr float kDepth = 41.f;           // entries 2^-kDepth below the largest weigh nothing
@@ -185,7 +188,7 @@ template <typename T>
 struct Row {
     static constexpr int E = VecOf<T>::kElems;
     RowView<T> r;
-    RowSlice sl;
+    RowSlice<Geo> sl;
     int cs, rank;
 
     template <typename F>
@@ -613,7 +616,7 @@ __device__ __forceinline__ float group_bound(const Shared& sh, int n) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, kRowCtasPerSm) sample_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleArgs a) {
     constexpr int E = VecOf<T>::kElems;
     extern __shared__ __align__(16) char smem[];
     __shared__ Shared sh;
@@ -622,8 +625,8 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtasPerSm) sample_kernel(Samp
     const int cs = 1 << a.lg, rank = cs > 1 ? (int)cluster_ctarank() : 0;
     const int rowi = blockIdx.x >> a.lg;
     const RowView<T> r(a.logits, a.ld, rowi, a.V);
-    Row<T> row{r, RowSlice(r, a.per, a.ring, rank, warp, smem), cs, rank};
-    const RowSlice& sl = row.sl;
+    Row<T> row{r, RowSlice<Geo>(r, a.per, a.ring, rank, warp, smem, l2_policy_evict_last()), cs, rank};
+    const RowSlice<Geo>& sl = row.sl;
     if (cs > 1) cluster_arrive();  // met by cluster_wait below: every CTA has started
     row.sl.start(r);
     float T0 = a.temperature != nullptr ? a.temperature[rowi] : a.temperature0;
@@ -638,7 +641,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtasPerSm) sample_kernel(Samp
 
     // the largest entries of the groups (kLanes * cs lanes each) and of the row
     constexpr int kLanes = kRowThreads / kGroups;
-    static_assert(kLanes * kRowMaxCluster <= 32);
+    static_assert(kLanes >= 1 && kLanes * kRowMaxCluster <= 32);
     float m = neg_inf();
     row.each_vec([&](int, const uint4& v) { m = max_or_nan(m, vec_max_or_nan<T>(v)); });
     const bool has_nan = __any_sync(0xffffffffu, m != m);
@@ -855,7 +858,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtasPerSm) sample_kernel(Samp
     ties = __shfl_sync(0xffffffffu, ties, from);
 
     // that warp's steps, by all warps of its CTA; then the warp of the step that holds it
-    const RowSlice own(r, a.per, a.ring, rank, holder % kRowWarps, smem);
+    const RowSlice<Geo> own(r, a.per, a.ring, rank, holder % kRowWarps, smem, 0);
     for (int step = warp; step < own.steps; step += kRowWarps) {
         u64 w = 0;
         u32 t = 0;
@@ -922,11 +925,11 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtasPerSm) sample_kernel(Samp
 cudaError_t launch_sample(SampleArgs a, int bf16, cudaStream_t stream, int num_sms) {
     // the widest row: kSampleMaxV fp32 entries over the largest cluster
     static_assert(kSampleMaxV / 4 / kRowMaxCluster / kRowWarps / kStepVecs < kMaxSteps);
-    const RowSplit p = split_rows(a.rows, a.V, bf16 ? 2 : 4, num_sms);
+    const RowSplit p = split_rows<Geo>(a.rows, a.V, bf16 ? 2 : 4, num_sms);
     a.lg = p.lg;
     a.per = p.per;
     a.ring = p.ring;
-    return launch_rows(bf16 ? sample_kernel<__nv_bfloat16> : sample_kernel<float>, a, a.rows, a.lg,
+    return launch_rows<Geo>(bf16 ? sample_kernel<__nv_bfloat16> : sample_kernel<float>, a, a.rows, a.lg,
                        p.smem, stream);
 }
 
