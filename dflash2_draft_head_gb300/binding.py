@@ -33,6 +33,8 @@ class Dflash2Error(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -104,6 +106,10 @@ def _ptr(t):
 
 def _stream(dev) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+
+
+# The current stream's handle without a Stream object around it (2 us a call).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _code(dt: torch.dtype) -> int:
@@ -326,34 +332,51 @@ def _logit_rows(t, name):
     spacing of the rows, but one, and elements that lie side by side."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    shape, V = t.shape[:-1], t.shape[-1]
-    if t.is_contiguous():
-        return shape, t.numel() // V if V else 0, V, V
+    shape = t.shape
+    V = shape[-1]
+    if len(shape) == 2:
+        ld, unit = t.stride()
+        if (unit == 1 or V <= 1) and ld >= V:
+            return shape[:1], shape[0], V, ld
     strides = t.stride()
     if V > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must have its last dimension contiguous")
     rows, ld = 1, None
-    for n, st in zip(reversed(shape), reversed(strides[:-1])):
+    for n, st in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if n != 1:
             if ld is None:
                 ld = st
             elif st != ld * rows:
                 raise ValueError(f"the rows of {name} must be evenly spaced")
         rows *= n
-    return shape, rows, V, max(V, 1) if ld is None else ld
+    return shape[:-1], rows, V, max(V, 1) if ld is None else ld
 
 
 def _need_rows(t, name, dtype, shape):
+    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     _need(t, name, dtype)
-    if t is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _out_rows(t, name, dtype, shape, dev, like=None):
+    """(tensor, pointer) of an output with a value for every row, allocated for None
+    (from `like`, another such fp32 tensor, where there is one: that takes less time)."""
+    if t is None:
+        if like is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        elif dtype is torch.float32:
+            t = torch.empty_like(like)
+        else:
+            t = torch.empty_like(like, dtype=dtype)
+        return t, t.data_ptr()
+    return t, _need_rows(t, name, dtype, shape)
 
 
 def _setting(v, name, dtype, shape):
     """(pointer, scalar) of a setting given for every row or once for all."""
     if isinstance(v, torch.Tensor):
-        _need_rows(v, name, dtype, shape)
-        return v.data_ptr(), 0
+        return _need_rows(v, name, dtype, shape), 0
     return None, v
 
 
@@ -365,42 +388,43 @@ def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, toke
     Each setting is a number or a tensor [...] with one per row (top_k int32, the
     others fp32).  The same row and number give the same token in any batch."""
     shape, rows, V, ld = _logit_rows(logits, "logits")
-    _need_rows(uniform, "uniform", torch.float32, shape)
+    up = _need_rows(uniform, "uniform", torch.float32, shape)
     tp, t0 = _setting(temperature, "temperature", torch.float32, shape)
     kp, k0 = _setting(top_k, "top_k", torch.int32, shape)
     pp, p0 = _setting(top_p, "top_p", torch.float32, shape)
     mp, m0 = _setting(min_p, "min_p", torch.float32, shape)
-    if tokens is None:
-        tokens = torch.empty(shape, dtype=torch.int32, device=logits.device)
-    else:
-        _need_rows(tokens, "tokens", torch.int32, shape)
-    if probs is None:
-        probs = torch.empty(shape, dtype=torch.float32, device=logits.device)
-    else:
-        _need_rows(probs, "probs", torch.float32, shape)
-    _check(lib().dflash2_sample(logits.data_ptr(), ld, uniform.data_ptr(), tp, kp, pp, mp, t0, k0,
-                                p0, m0, rows, V, _code(logits.dtype), tokens.data_ptr(),
-                                probs.data_ptr(), _stream(logits.device)))
+    dev = logits.device
+    tokens, tokens_ptr = _out_rows(tokens, "tokens", torch.int32, shape, dev, uniform)
+    probs, probs_ptr = _out_rows(probs, "probs", torch.float32, shape, dev, uniform)
+    st = lib().dflash2_sample(logits.data_ptr(), ld, up, tp, kp, pp, mp, t0, k0, p0, m0, rows, V,
+                              _code(logits.dtype), tokens_ptr, probs_ptr, _raw_stream(dev.index))
+    if st != DF2_OK:
+        _check(st)
     return tokens, probs
 
 
 def _teacher(teacher_ids, teacher_logits, weight, shape):
+    """K and the pointers of the teacher's entries and the weights."""
     K = teacher_ids.shape[-1]
-    _need_rows(teacher_ids, "teacher_ids", torch.int32, shape + (K,))
-    _need_rows(teacher_logits, "teacher_logits", torch.float32, shape + (K,))
-    _need_rows(weight, "weight", torch.float32, shape)
-    return K
+    each = shape + (K,)
+    return (K, _need_rows(teacher_ids, "teacher_ids", torch.int32, each),
+            _need_rows(teacher_logits, "teacher_logits", torch.float32, each),
+            None if weight is None else _need_rows(weight, "weight", torch.float32, shape))
 
 
-def _grad_rows(grad, logits):
-    """The gradient tensor (allocated with the logits' strides when it is True) and the
-    elements between two of its rows."""
+def _grad_rows(grad, logits, ld):
+    """The gradient tensor (allocated with the logits' strides when it is True), its
+    pointer and the elements between two of its rows."""
     if grad is True:
-        grad = torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype,
-                                   device=logits.device)
+        if logits.is_contiguous():
+            grad = torch.empty_like(logits)
+        else:
+            grad = torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype,
+                                       device=logits.device)
+        return grad, grad.data_ptr(), ld
     if grad.shape != logits.shape or grad.dtype != logits.dtype:
         raise ValueError("grad must have the shape and dtype of logits")
-    return grad, _logit_rows(grad, "grad")[3]
+    return grad, grad.data_ptr(), _logit_rows(grad, "grad")[3]
 
 
 def distill(logits, teacher_ids, teacher_logits, temperature=1.0, weight=None, grad=False,
@@ -413,25 +437,21 @@ def distill(logits, teacher_ids, teacher_logits, temperature=1.0, weight=None, g
     a tensor to write, which may be logits) the gradient of the sum of the losses;
     else None."""
     shape, rows, V, ld = _logit_rows(logits, "logits")
-    K = _teacher(teacher_ids, teacher_logits, weight, shape)
-    if loss is None:
-        loss = torch.empty(shape, dtype=torch.float32, device=logits.device)
-    else:
-        _need_rows(loss, "loss", torch.float32, shape)
-    if lse is None:
-        lse = torch.empty(shape, dtype=torch.float32, device=logits.device)
-    else:
-        _need_rows(lse, "lse", torch.float32, shape)
+    K, ids_ptr, teacher_ptr, weight_ptr = _teacher(teacher_ids, teacher_logits, weight, shape)
+    dev = logits.device
+    loss, loss_ptr = _out_rows(loss, "loss", torch.float32, shape, dev, weight)
+    lse, lse_ptr = _out_rows(lse, "lse", torch.float32, shape, dev, loss)
     _need(err_flag, "err_flag", torch.int32)
-    gld = 0
     if grad is None or grad is False:
-        grad = None
+        grad, grad_ptr, grad_ld = None, None, 0
     else:
-        grad, gld = _grad_rows(grad, logits)
-    _check(lib().dflash2_distill(logits.data_ptr(), ld, teacher_ids.data_ptr(),
-                                 teacher_logits.data_ptr(), _ptr(weight), rows, V, K, temperature,
-                                 _code(logits.dtype), loss.data_ptr(), lse.data_ptr(), _ptr(grad),
-                                 gld, _ptr(err_flag), _stream(logits.device)))
+        grad, grad_ptr, grad_ld = _grad_rows(grad, logits, ld)
+    st = lib().dflash2_distill(logits.data_ptr(), ld, ids_ptr, teacher_ptr, weight_ptr, rows, V, K,
+                               temperature, _code(logits.dtype), loss_ptr, lse_ptr, grad_ptr,
+                               grad_ld, None if err_flag is None else err_flag.data_ptr(),
+                               _raw_stream(dev.index))
+    if st != DF2_OK:
+        _check(st)
     return loss, lse, grad
 
 
@@ -441,16 +461,18 @@ def distill_backward(grad_loss, logits, teacher_ids, teacher_logits, lse, temper
     grad_loss [...] fp32, and the lse [...] that it returned.  grad may be a tensor to
     write (also logits)."""
     shape, rows, V, ld = _logit_rows(logits, "logits")
-    K = _teacher(teacher_ids, teacher_logits, weight, shape)
-    _need_rows(grad_loss, "grad_loss", torch.float32, shape)
-    _need_rows(lse, "lse", torch.float32, shape)
+    K, ids_ptr, teacher_ptr, weight_ptr = _teacher(teacher_ids, teacher_logits, weight, shape)
+    up = _need_rows(grad_loss, "grad_loss", torch.float32, shape)
+    lse_ptr = _need_rows(lse, "lse", torch.float32, shape)
     _need(err_flag, "err_flag", torch.int32)
-    grad, gld = _grad_rows(grad, logits)
-    _check(lib().dflash2_distill_backward(grad_loss.data_ptr(), logits.data_ptr(), ld,
-                                          teacher_ids.data_ptr(), teacher_logits.data_ptr(),
-                                          _ptr(weight), lse.data_ptr(), rows, V, K, temperature,
-                                          _code(logits.dtype), _ptr(grad), gld, _ptr(err_flag),
-                                          _stream(logits.device)))
+    grad, grad_ptr, grad_ld = _grad_rows(grad, logits, ld)
+    st = lib().dflash2_distill_backward(up, logits.data_ptr(), ld, ids_ptr, teacher_ptr,
+                                        weight_ptr, lse_ptr, rows, V, K, temperature,
+                                        _code(logits.dtype), grad_ptr, grad_ld,
+                                        None if err_flag is None else err_flag.data_ptr(),
+                                        _raw_stream(logits.device.index))
+    if st != DF2_OK:
+        _check(st)
     return grad
 
 

@@ -18,7 +18,6 @@
 // over) the power is 2^((z - max) * c).
 #include <cuda_runtime.h>
 
-#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -382,7 +381,7 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) distill_grad_kernel(D
     extern __shared__ __align__(16) char smem[];
     __shared__ float has_teacher;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = blockIdx.x, rank = blockIdx.y;
+    const int row = blockIdx.x >> a.lg, rank = blockIdx.x & ((1 << a.lg) - 1);
     const RowView<T> r(a.logits, a.ld, row, a.V);
     RowSlice<Geo> sl(r, a.per, a.ring, rank, warp, smem + (size_t)a.K * 16,
                 l2_policy_evict_first());
@@ -429,34 +428,24 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) distill_grad_kernel(D
 }
 
 template <typename T>
-cudaError_t launch_grad(DistillArgs a, size_t smem, cudaStream_t stream, int num_sms) {
-    const RowSplit p = split_rows<Geo>(a.rows, a.V, sizeof(T), num_sms);
-    a.per = p.per;
-    a.ring = p.ring;
-    smem += (size_t)a.ring * Geo::kStepBytes;
-    const cudaError_t e = cudaFuncSetAttribute(
-        distill_grad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    distill_grad_kernel<T><<<dim3(a.rows, 1u << p.lg), kRowThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_typed(const DistillArgs& a, const RowSplit& p, cudaStream_t stream) {
+    const size_t smem = p.smem + (size_t)a.K * 16;
+    constexpr size_t kMost = Geo::kRingBytes + (size_t)kDistillMaxK * 16;
+    if (a.grad_loss != nullptr)
+        return launch_rows<Geo, distill_grad_kernel<T>>(a, a.rows, p.lg, smem, kMost, stream);
+    if (a.grad != nullptr)
+        return launch_rows<Geo, distill_kernel<T, true>>(a, a.rows, p.lg, smem, kMost, stream);
+    return launch_rows<Geo, distill_kernel<T, false>>(a, a.rows, p.lg, smem, kMost, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_distill(DistillArgs a, int bf16, cudaStream_t stream, int num_sms) {
-    const size_t teacher = (size_t)a.K * 16;
-    if (a.grad_loss != nullptr)
-        return bf16 ? launch_grad<__nv_bfloat16>(a, teacher, stream, num_sms)
-                    : launch_grad<float>(a, teacher, stream, num_sms);
     const RowSplit p = split_rows<Geo>(a.rows, a.V, bf16 ? 2 : 4, num_sms);
     a.lg = p.lg;
     a.per = p.per;
     a.ring = p.ring;
-    const auto kernel = bf16 ? (a.grad != nullptr ? distill_kernel<__nv_bfloat16, true>
-                                                  : distill_kernel<__nv_bfloat16, false>)
-                             : (a.grad != nullptr ? distill_kernel<float, true>
-                                                  : distill_kernel<float, false>);
-    return launch_rows<Geo>(kernel, a, a.rows, a.lg, p.smem + teacher, stream);
+    return bf16 ? launch_typed<__nv_bfloat16>(a, p, stream) : launch_typed<float>(a, p, stream);
 }
 
 }  // namespace df2

@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -33,6 +34,7 @@ struct RowGeometry {
     static constexpr int kThreads = THREADS, kWarps = THREADS / 32, kCtas = CTAS, kRing = RING;
     static constexpr long long kSliceBytes = SLICE_KB * 1024;
     static constexpr int kStepBytes = kWarps * kStepVecs * 16;  // a CTA's part of the ring, a step
+    static constexpr int kRingBytes = kRing * kStepBytes;
     // A warp's part of n vectors: whole steps where it has several (a short one costs as
     // much as a whole one), else lines of 128 bytes.
     static __host__ __device__ constexpr int warp_vecs(int n) {
@@ -359,16 +361,17 @@ RowSplit split_rows(int rows, int V, size_t es, int num_sms) {
     return {lg, per, ring, ring * G::kStepBytes};
 }
 
-// Launches `rows` clusters of 2^lg CTAs.
-template <typename G, typename Args>
-cudaError_t launch_rows(void (*kernel)(Args), const Args& a, int rows, int lg, size_t smem,
+// Launches a kernel over `rows` clusters of 2^lg CTAs.  Its shared memory and cluster
+// size go beyond the defaults: the attributes that allow this are set on the first
+// launch on a device, and again where they turn out to be gone (a device reset).
+template <typename G, auto KERNEL, typename Args>
+cudaError_t launch_rows(const Args& a, int rows, int lg, size_t smem, size_t most_smem,
                         cudaStream_t stream) {
-    cudaError_t e = cudaSuccess;
-    if (smem > 16 * 1024)  // with the static arrays this may pass the default 48 KB
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && 1 << lg > 8)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    static std::atomic<uint64_t> allowed{0};  // a bit for each device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)rows << lg));
     cfg.blockDim = dim3(G::kThreads);
@@ -380,7 +383,18 @@ cudaError_t launch_rows(void (*kernel)(Args), const Args& a, int rows, int lg, s
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = lg > 0 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    const bool known = dev < 64 && (allowed.load(std::memory_order_relaxed) & bit) != 0;
+    if (known) {
+        e = cudaLaunchKernelEx(&cfg, KERNEL, a);
+        if (e == cudaSuccess) return e;
+        cudaGetLastError();
+    }
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) allowed.fetch_or(bit, std::memory_order_relaxed);
+    return cudaLaunchKernelEx(&cfg, KERNEL, a);
 }
 
 }  // namespace df2

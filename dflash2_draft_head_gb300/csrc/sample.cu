@@ -16,16 +16,16 @@
 // Bound by HBM: a row is read once, by one CTA or by the CTAs of a cluster, and passed
 // over two or more times on the chip.  The largest entries of 256 groups of the row come first: their maximum is the row's, and the n-th largest
 // of them is a bound above which at least n entries lie.
-//   - Neither top_k nor top_p: one pass of weights, summed by warp; one warp of the
-//     row holds the token and looks it up.
+//   - Neither top_k nor top_p: one pass of weights, summed by warp; one warp's part of
+//     the row holds the token and is looked through.
 //   - Up to 256 entries to keep, or a top_p that the entries above such a bound
 //     reach: those entries (some hundreds) are listed, and one CTA finishes the row
 //     from the list alone.
-//   - Else the cut is found by histograms: of counts over the distance from the maximum
-//     first (a bin's weights differ by 1.4%, which leaves a few bins that may hold the
-//     cut), then of the exact weights over the values of those bins, until that is one
-//     value; ties there are kept by index.  The weights of what is kept are then
-//     summed and looked up as in the first case.
+//   - Else counts over the distance from the maximum (a bin's weights differ by 1.4%)
+//     leave a few bins that may hold the cut.  Up to 1024 entries there are listed and
+//     sorted; more of them (ties) are told apart by histograms of their exact weights
+//     over their values, until the cut lies in one value.  What is kept is then summed
+//     by warp and looked through as in the first case.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -47,8 +47,10 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kOne = 1099511627776.f;  // 2^40, the largest entry's weight
 constexpr float kDepth = 41.f;           // entries 2^-kDepth below the largest weigh nothing
 constexpr int kDepthBins = 2048;         // of counts, over the depth
-constexpr int kBins = 512;               // of counts and weights, over keys
-constexpr int kLimb = 14;                // a weight in three words of a histogram: 14, 14, 13 bits
+constexpr int kBins = 512;               // of counts, or of weights in four words, over keys
+constexpr int kLimb = 11;                // bits of a weight in each word: 2^21 of them fit 32 bits
+constexpr int kBinsLog = 9;
+static_assert(kBins == 1 << kBinsLog && kBins == kRowThreads && kDepthBins == 4 * kRowThreads);
 
 // An order-preserving whole number of a value (-0 like +0), and back.
 template <typename T>
@@ -122,7 +124,7 @@ __device__ __forceinline__ S warp_before(S v) {
 }
 
 __device__ __forceinline__ u64 bin_weight(const uint4& b) {
-    return (u64)b.y + ((u64)b.z << kLimb) + ((u64)b.w << (2 * kLimb));
+    return (u64)b.x + ((u64)b.y << kLimb) + ((u64)b.z << (2 * kLimb)) + ((u64)b.w << (3 * kLimb));
 }
 
 // Where the kept entries end: those with a key above `key`, and the first `ties`
@@ -132,55 +134,72 @@ struct Cut {
     u64 weight;  // of one of those ties
 };
 
-// How many of n equal entries of weight W, behind a sum of `before`, are kept:
-// those with less than `limit` before them.
-__device__ __forceinline__ u32 ties_below(u64 before, u64 W, u32 n, double limit) {
-    u32 lo = 0, hi = n;  // the first i in [0, n) at which before + i * W reaches the limit
-    while (lo < hi) {
-        const u32 mid = (lo + hi) >> 1;
-        if ((double)(before + (u64)mid * W) < limit)
-            lo = mid + 1;
-        else
-            hi = mid;
+// "The weight before an entry is below p * total", a comparison in fp64, as one of whole
+// numbers: the least one that is not below the product.  One lane of each warp finds it
+// (the SM's fp64 units are few).
+__device__ __forceinline__ u64 limit_of(float p, u64 total) {
+    u64 first = 0;
+    if ((threadIdx.x & 31) == 0) {
+        const double limit = (double)p * (double)total;
+        first = __double2ull_ru(limit);
+        if (limit >= 9007199254740992.) {  // 2^53: numbers just below it may round up to it
+            u64 low = first - 512;         // spaced at most 2^9 apart below 2^62
+            while (first - low > 1) {
+                const u64 mid = low + (first - low) / 2;
+                if ((double)mid >= limit)
+                    first = mid;
+                else
+                    low = mid;
+            }
+        }
     }
-    return lo;
+    return __shfl_sync(0xffffffffu, first, 0);
+}
+
+// u * total as a whole number below total (u outside [0, 1): the nearer end).
+__device__ __forceinline__ u64 target_of(float u, u64 total) {
+    u64 t = 0;
+    if ((threadIdx.x & 31) == 0)
+        t = min((u64)__double2ull_rz((double)(u > 0.f ? u : 0.f) * (double)total), total - 1);
+    return __shfl_sync(0xffffffffu, t, 0);
 }
 
 constexpr int kGroups = 256;          // groups of a row whose maxima are exchanged
 constexpr int kListMax = 1024;        // entries of a row's list
 constexpr int kParts = kRowMaxCluster * kRowWarps;
-constexpr int kMaxSteps = 64;         // of a warp: see the assertion beside the launch
-
-// What a CTA tells the others of its slice: listed entries, their weight, all weight.
-struct Told {
-    u64 listed, weight, all;
-};
+constexpr int kMaxUnits = 128;        // of a warp: see the assertion beside the launch
 
 struct Shared {
     union {
         u32 count[kDepthBins];
-        uint4 hist[kBins];       // count and the three words of the weight
+        uint4 bins[kBins];
         u64 own_list[kListMax];  // this CTA's listed entries
-        u64 sorted[kListMax];    // the row's, in order (rank 0)
+        u64 weight[kListMax];    // the weights of the row's, by place (rank 0)
     };
-    u64 list[kListMax];          // the row's listed entries (rank 0): key, then ~index
+    union {
+        uint4 total[kBins];  // the cluster's bins
+        u64 list[kListMax];  // the row's listed entries (rank 0): key, then ~index
+    };
     float group_max[kGroups];
     float own_max[kGroups];
-    Told told[kRowMaxCluster];
+    u64 told_n[kRowMaxCluster];  // every CTA's listed entries
+    u64 told_w[kRowMaxCluster];  // and their weight
+    u64 cta_w[kRowMaxCluster];   // sums over the row
+    u64 answer[2];               // a cut's key and ties; the kept weight
+    u64 part_w[kParts];          // kept weight of every warp of the row
+    u32 part_t[kParts];          // and its ties at the cut
+    u64 unit_w[kMaxUnits];       // the same of 32 vectors each of one warp
+    u32 unit_t[kMaxUnits];
+    u64 cta_span[kRowMaxCluster];  // largest and smallest key of a bracket, by CTA
     u32 own_n, list_n, base;
     float bound;
-    u64 part_w[kParts];          // kept weight of every warp of the row
-    u64 part_t[kParts];          // and its ties at the cut
-    u64 cta_span[kRowMaxCluster];  // largest and smallest key of a bracket, by CTA
-    u64 cta_w[kRowMaxCluster];     // and the weight above it
-    u64 step_w[kMaxSteps];       // kept weight of the steps of one warp
-    u32 step_t[kMaxSteps];       // and their ties
     u32 span_hi, span_lo;
     u32 scan_n[kRowWarps];
     u64 scan_w[kRowWarps];
-    // the bins that may hold the cut; for one bin, what stands before it and its weight
+    // the bins that may hold the cut: what stands before them and with them; for one bin
+    // the weights
     int at, at_hi;
-    u32 before_n;
+    u32 before_n, upto_n;
     u64 before_w, in_w;
 };
 
@@ -189,32 +208,32 @@ struct Row {
     static constexpr int E = VecOf<T>::kElems;
     RowView<T> r;
     RowSlice<Geo> sl;
-    int cs, rank;
+    int lg, cs, rank;
 
     template <typename F>
     __device__ __forceinline__ void each_vec(F f) {
         sl.pass(r, [&](int v, const uint4& vec, bool) { f(v, vec); });
     }
-    // f(entries, their depths), two at a time.  `plain`: no NaN among them and a finite
-    // maximum; else a NaN has the depth of -inf
+    // f(index, entries, their depths), two at a time.  `plain`: no NaN among them and a
+    // finite maximum; else a NaN has the depth of -inf
     template <typename F>
     __device__ __forceinline__ void each_pair(const Weigh& g, bool plain, F f) {
         const f32x2 nm = pair(-g.m, -g.m), c = pair(g.c, g.c);
         if (plain) {
-            each_vec([&](int, const uint4& vec) {
+            each_vec([&](int v, const uint4& vec) {
                 f32x2 x[E / 2];
                 unpack(vec, x);
 #pragma unroll
                 for (int j = 0; j < E / 2; ++j)
-                    f(halves(x[j]), halves(mul2(add2(x[j], nm), c)));
+                    f(v * E - r.head + 2 * j, halves(x[j]), halves(mul2(add2(x[j], nm), c)));
             });
         } else {
-            each_vec([&](int, const uint4& vec) {
+            each_vec([&](int v, const uint4& vec) {
                 float x[E];
                 unpack(vec, x);
 #pragma unroll 1
                 for (int j = 0; j < E; j += 2)
-                    f(make_float2(x[j], x[j + 1]),
+                    f(v * E - r.head + j, make_float2(x[j], x[j + 1]),
                       make_float2(fmaxf(g.depth(x[j]), -200.f), fmaxf(g.depth(x[j + 1]), -200.f)));
             });
         }
@@ -261,8 +280,8 @@ __device__ __forceinline__ u64 row_weight(Shared& sh, const R& row, u64 w) {
     return w;
 }
 
-// Running sums over the block's threads: what stands before this one.
-__device__ __forceinline__ void block_before(Shared& sh, u32& n, u64& w) {
+// Running sums over the block's threads: what stands before this one.  Returns all.
+__device__ __forceinline__ u64 block_before(Shared& sh, u32& n, u64& w) {
     const u32 bn = warp_before(n);
     const u64 bw = warp_before(w);
     __syncthreads();
@@ -273,10 +292,45 @@ __device__ __forceinline__ void block_before(Shared& sh, u32& n, u64& w) {
     __syncthreads();
     n = bn;
     w = bw;
-    for (int i = 0; i < (int)threadIdx.x >> 5; ++i) {
-        n += sh.scan_n[i];
-        w += sh.scan_w[i];
+    u64 all = 0;
+#pragma unroll
+    for (int i = 0; i < kRowWarps; ++i) {
+        if (i < (int)threadIdx.x >> 5) {
+            n += sh.scan_n[i];
+            w += sh.scan_w[i];
+        }
+        all += sh.scan_w[i];
     }
+    return all;
+}
+
+// Adds up the cluster's bins (each CTA a share of them, which it then tells the others)
+// and returns this thread's.  What stood in sh.bins may be overwritten afterwards.
+template <typename R>
+__device__ __forceinline__ uint4 merge_bins(Shared& sh, const R& row) {
+    const int tid = threadIdx.x;
+    if (row.cs == 1) {
+        __syncthreads();
+        const uint4 b = sh.bins[tid];
+        __syncthreads();
+        return b;
+    }
+    const int lg = kBinsLog - row.lg, share = 1 << lg, other = tid >> lg;
+    const int mine = row.rank * share + (tid & (share - 1));
+    if (tid < share) sh.total[mine] = make_uint4(0, 0, 0, 0);
+    row.sync();  // every CTA's bins are filled
+    const uint4 b = ld_cluster_v4(map_cluster(smem_u32(&sh.bins[mine]), other));
+    u32* sum = reinterpret_cast<u32*>(&sh.total[mine]);
+    if (b.x != 0) atomicAdd(sum, b.x);
+    if (b.y != 0) atomicAdd(sum + 1, b.y);
+    if (b.z != 0) atomicAdd(sum + 2, b.z);
+    if (b.w != 0) atomicAdd(sum + 3, b.w);
+    __syncthreads();
+    if (other != row.rank)
+        st_cluster_v4(map_cluster(smem_u32(&sh.total[mine]), other),
+                      *reinterpret_cast<const float4*>(&sh.total[mine]));
+    row.sync();
+    return sh.total[tid];
 }
 
 __device__ __forceinline__ int depth_bin(float d) {
@@ -294,152 +348,282 @@ __device__ __forceinline__ u64 bin_least(int bin) {
     return bin == kDepthBins - 1 || w == 0 ? 0 : w - 1;
 }
 
-// Adds up the cluster's counts by depth and finds, from the largest entries down, the
-// bins that may hold the cut: sh.at to sh.at_hi (one bin, with sh.before_n, by count);
-// sh.at is kDepthBins when there is no cut.
+// This lane's part of its warp's weight: all entries.
+template <typename T>
+__device__ __forceinline__ u64 all_weight(Row<T>& row, const Weigh& g, bool plain) {
+    WeightSum ws;
+    int entries = 0;
+    row.each_pair(g, plain, [&](int, float2, float2 d) {
+        ws.add(pair(ex2(d.x), ex2(d.y)));
+        entries += 2;
+    });
+    return ws.total(entries);
+}
+
+// This lane's part of its warp's kept weight, and its ties at the cut.
+template <typename T>
+__device__ __forceinline__ void kept_weight(Row<T>& row, const Weigh& g, bool plain,
+                                            const Cut& cut, float min_p, u64& weight, u32& ties) {
+    const float floor = cut.key != 0 ? Key<T>::value(cut.key) : neg_inf();
+    const float least = min_p > 0.f ? min_p : 0.f;
+    WeightSum ws;
+    int entries = 0;
+    u32 t = 0;
+    row.each_pair(g, plain, [&](int, float2 x, float2 d) {
+        const float wx = ex2(d.x), wy = ex2(d.y);
+        const bool kx = wx >= least, ky = wy >= least;
+        ws.add(pair(kx && x.x > floor ? wx : 0.f, ky && x.y > floor ? wy : 0.f));
+        t += (kx && x.x == floor) + (ky && x.y == floor);
+        entries += 2;
+    });
+    weight = ws.total(entries);
+    ties = cut.ties != 0 ? t : 0;
+}
+
+// A listed entry: larger ones come first in the order of falling values.
+template <typename T>
+__device__ __forceinline__ u64 entry_of(float x, int index) {
+    return (u64)Key<T>::of(x) << 32 | (u32)~index;
+}
+
+// Sorts the row's list of n entries, first ones first: every entry counts those before
+// it.  One CTA.
+__device__ __forceinline__ void sort_list(Shared& sh, int n) {
+    constexpr int kPer = kListMax / kRowThreads;
+    const int tid = threadIdx.x;
+    u64 e[kPer];
+    int before[kPer] = {};
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) e[i] = tid + i * kRowThreads < n ? sh.list[tid + i * kRowThreads] : 0;
+    if (tid < n) {
+        if (n <= kRowThreads) {
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) before[0] += sh.list[j] > e[0];
+        } else {
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) {
+                const u64 o = sh.list[j];
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) before[i] += o > e[i];
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (tid + i * kRowThreads < n) sh.list[before[i]] = e[i];
+    __syncthreads();
+}
+
+// Sends this CTA's listed entries to rank 0's list, behind those that got there first.
+// The caller's next row.sync() completes it.
+template <typename R>
+__device__ __forceinline__ void send_list(Shared& sh, const R& row, u32 n) {
+    const int tid = threadIdx.x;
+    if (row.cs == 1) {
+        for (u32 i = tid; i < min(n, (u32)kListMax); i += kRowThreads) sh.list[i] = sh.own_list[i];
+        return;
+    }
+    if (tid == 0)
+        sh.base = n <= kListMax ? atom_add_cluster(map_cluster(smem_u32(&sh.list_n), 0), n) : kListMax;
+    __syncthreads();
+    for (u32 i = tid; i < n && sh.base + i < kListMax; i += kRowThreads)
+        st_cluster_b64(map_cluster(smem_u32(&sh.list[sh.base + i]), 0), sh.own_list[i]);
+}
+
+// Finds, from the largest entries down, the depth bins that may hold the cut: sh.at to
+// sh.at_hi (one bin by count), with the counts before and up to them; sh.at is
+// kDepthBins when there is no cut.
 template <bool BY_COUNT, typename R>
-__device__ void find_bracket(Shared& sh, const R& row, u32 k, double limit) {
-    constexpr int kPer = kDepthBins / kRowThreads;
-    const int first = (int)threadIdx.x * kPer;
+__device__ __forceinline__ void find_bracket(Shared& sh, const R& row, u32 k, u64 limit) {
+    const uint4 b = merge_bins(sh, row);
+    const u32 n[4] = {b.x, b.y, b.z, b.w};
+    const int first = (int)threadIdx.x * 4;
     if (threadIdx.x == 0) {
         sh.at = kDepthBins;
         sh.at_hi = kDepthBins - 1;
+        sh.before_n = 0;
+        sh.upto_n = 0xffffffffu;
     }
-    row.sync();  // every histogram is filled
-    u32 n[kPer] = {};
-    for (int q = 0; q < row.cs; ++q) {
-#pragma unroll
-        for (int i = 0; i < kPer; i += 4) {
-            const uint4 b = row.cs > 1 ? ld_cluster_v4(map_cluster(smem_u32(&sh.count[first + i]), q))
-                                       : *reinterpret_cast<const uint4*>(&sh.count[first + i]);
-            n[i] += b.x;
-            n[i + 1] += b.y;
-            n[i + 2] += b.z;
-            n[i + 3] += b.w;
-        }
-    }
-    u32 bn = 0;
+    u32 bn = 0, none = 0;
     u64 least = 0, most = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < 4; ++i) {
         bn += n[i];
         if (!BY_COUNT) {
             least += n[i] * bin_least(first + i);
             most += n[i] * bin_most(first + i);
         }
     }
-    u32 none = 0;
     block_before(sh, bn, least);
     if (!BY_COUNT) block_before(sh, none, most);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const u64 l = BY_COUNT ? 0 : n[i] * bin_least(first + i);
         const u64 h = BY_COUNT ? 0 : n[i] * bin_most(first + i);
-        if (BY_COUNT ? bn < k && bn + n[i] >= k
-                     : (double)most < limit && (double)(most + h) >= limit) {
+        const bool may = BY_COUNT ? bn < k && bn + n[i] >= k : most < limit && most + h >= limit;
+        const bool must = BY_COUNT ? may : least < limit && least + l >= limit;
+        if (may) {
             sh.at = first + i;
             sh.before_n = bn;
-            if (BY_COUNT) sh.at_hi = first + i;
         }
-        if (!BY_COUNT && (double)least < limit && (double)(least + l) >= limit)
+        if (must) {
             sh.at_hi = first + i;
+            sh.upto_n = bn + n[i];
+        }
         bn += n[i];
         least += l;
         most += h;
     }
-    row.sync();  // every histogram is read, and the bins are found
+    __syncthreads();
 }
 
-// Adds up the cluster's histograms and finds the first bin at which the running count
-// reaches k or the running weight `limit`; sh.at is kBins when none does.
+// The same over the bins of keys: the one bin at which the running count reaches k or the
+// running weight `limit`; sh.at is kBins when none does.
 template <bool BY_COUNT, typename R>
-__device__ void find_bin(Shared& sh, const R& row, u32 base_n, u64 base_w, u32 k, double limit) {
-    constexpr int kPer = kBins / kRowThreads;
-    const int first = (int)threadIdx.x * kPer;
+__device__ __forceinline__ void find_bin(Shared& sh, const R& row, u32 base_n, u64 base_w, u32 k,
+                                         u64 limit) {
+    const uint4 b = merge_bins(sh, row);
+    const u32 n = BY_COUNT ? b.x : 0;
+    const u64 w = BY_COUNT ? 0 : bin_weight(b);
     if (threadIdx.x == 0) sh.at = kBins;
-    row.sync();  // every histogram is filled
-    u32 n[kPer] = {}, bn = 0;
-    u64 w[kPer] = {}, bw = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        for (int q = 0; q < row.cs; ++q) {
-            const uint4 b = row.cs > 1 ? ld_cluster_v4(map_cluster(smem_u32(&sh.hist[first + i]), q))
-                                       : sh.hist[first + i];
-            n[i] += b.x;
-            w[i] += bin_weight(b);
-        }
-        bn += n[i];
-        bw += w[i];
-    }
+    u32 bn = n;
+    u64 bw = w;
     block_before(sh, bn, bw);
     bn += base_n;
     bw += base_w;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const bool open = BY_COUNT ? bn < k : (double)bw < limit;
-        const bool shut = BY_COUNT ? bn + n[i] >= k : (double)(bw + w[i]) >= limit;
-        if (open && shut) {  // one bin of the row
-            sh.at = first + i;
-            sh.before_n = bn;
-            sh.before_w = bw;
-            sh.in_w = w[i];
-        }
-        bn += n[i];
-        bw += w[i];
+    if (BY_COUNT ? bn < k && bn + n >= k : bw < limit && bw + w >= limit) {
+        sh.at = (int)threadIdx.x;
+        sh.before_n = bn;
+        sh.before_w = bw;
+        sh.in_w = w;
     }
-    row.sync();  // every histogram is read, and the bin is found
+    __syncthreads();
 }
 
 // The cut by count (the first k entries) or by weight (those with less than `limit`
 // before them), among the entries inside `in`; `in` itself when that cuts nothing.
 struct Found {
     Cut cut;
-    u64 kept_w;  // the kept entries' weight (by count: where `weigh` asks for it)
-    bool up;     // the direction of the row's next pass
+    u64 kept_w;   // the kept entries' weight (by count: where `weigh` asks for it)
+    bool summed;  // this warp's kept weight and ties are known too
+    u64 warp_w;
+    u32 warp_t;
+    bool up;      // the direction of the row's next pass
 };
 template <bool BY_COUNT, typename T>
 __device__ __noinline__ Found find_cut(Shared& sh, Row<T> row, const Weigh g, bool plain,
-                                      const Cut in, u32 k, double limit, bool weigh) {
+                                       const Cut in, u32 k, u64 limit, bool weigh) {
+    constexpr int E = VecOf<T>::kElems;
     const int tid = threadIdx.x, lane = tid & 31;
-    auto clear = [&] {  // all of count and of hist
-        for (int i = tid; i < kBins; i += kRowThreads) sh.hist[i] = make_uint4(0, 0, 0, 0);
+    auto clear = [&] {
+        sh.bins[tid] = make_uint4(0, 0, 0, 0);
         if (tid == 0) {
+            sh.own_n = sh.list_n = 0;
             sh.span_hi = 0;
             sh.span_lo = 0xffffffffu;
         }
         __syncthreads();
     };
-    static_assert(sizeof(sh.count) == sizeof(sh.hist));
     const float least = in.key != 0 ? Key<T>::value(in.key) : neg_inf();
     clear();
-    row.each_pair(g, plain, [&](float2 x, float2 d) {
+    row.each_pair(g, plain, [&](int, float2 x, float2 d) {
         if (x.x >= least && d.x >= -kDepth) atomicAdd(&sh.count[depth_bin(d.x)], 1u);
         if (x.y >= least && d.y >= -kDepth) atomicAdd(&sh.count[depth_bin(d.y)], 1u);
     });
     find_bracket<BY_COUNT>(sh, row, k, limit);
     const int at = sh.at, at_hi = sh.at_hi;
     u32 n = sh.before_n;
+    const u32 inside = sh.upto_n - n;
+    const bool listed = at < kDepthBins && inside <= kListMax;
 
-    // the weight above the bracket, and the span of the keys in it
+    // the weight above the bracket; its entries, or the span of their keys
     WeightSum above;
     int entries = 0;
     float hi_x = neg_inf(), lo_x = INFINITY;
-    row.each_pair(g, plain, [&](float2 x, float2 d) {
-        const bool in_x = x.x >= least && d.x >= -kDepth, in_y = x.y >= least && d.y >= -kDepth;
-        const int bx = depth_bin(d.x), by = depth_bin(d.y);
-        above.add(pair(in_x && bx < at ? ex2(d.x) : 0.f, in_y && by < at ? ex2(d.y) : 0.f));
+    row.each_pair(g, plain, [&](int index, float2 x, float2 d) {
+        auto look = [&](int index, float x, float d) {
+            if (!(x >= least && d >= -kDepth)) return 0.f;
+            const int bin = depth_bin(d);
+            if (bin < at) return ex2(d);
+            if (bin > at_hi) return 0.f;
+            if (listed) {
+                sh.own_list[atomicAdd(&sh.own_n, 1u)] = entry_of<T>(x, index);
+            } else {
+                hi_x = fmaxf(hi_x, x);
+                lo_x = fminf(lo_x, x);
+            }
+            return 0.f;
+        };
+        const float wx = look(index, x.x, d.x);
+        above.add(pair(wx, look(index + 1, x.y, d.y)));
         entries += 2;
-        if (in_x && bx >= at && bx <= at_hi) {
-            hi_x = fmaxf(hi_x, x.x);
-            lo_x = fminf(lo_x, x.x);
-        }
-        if (in_y && by >= at && by <= at_hi) {
-            hi_x = fmaxf(hi_x, x.y);
-            lo_x = fminf(lo_x, x.y);
-        }
     });
-    u64 w = BY_COUNT && !weigh ? 0 : row_weight(sh, row, above.total(entries));
-    if (at == kDepthBins) return {in, w, row.sl.up};
+    const u64 lane_w = above.total(entries);
+    u64 w = row_weight(sh, row, lane_w);
+    if (at == kDepthBins) return {in, w, false, 0, 0, row.sl.up};
+    if (listed) {
+        const u32 own = sh.own_n;
+        send_list(sh, row, own);
+        row.sync();
+        if (row.rank == 0) {
+            // the last kept entry's place in the sorted list; its ties before it are kept
+            constexpr int kPer = kListMax / kRowThreads;
+            sort_list(sh, (int)inside);
+            u64 W[kPer], before = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const u32 q = (u32)(tid * kPer + i);
+                W[i] = q < inside
+                           ? Weigh::fixed(Weigh::w(g.depth(Key<T>::value((u32)(sh.list[q] >> 32)))))
+                           : 0;
+                before += W[i];
+            }
+            u32 none = 0;
+            block_before(sh, none, before);
+            before += w;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const u32 q = (u32)(tid * kPer + i);
+                const bool last = BY_COUNT ? n + q + 1 == k
+                                           : q < inside && before < limit && before + W[i] >= limit;
+                before += W[i];
+                if (!last) continue;
+                const u32 key = (u32)(sh.list[q] >> 32);
+                u32 ties = 1;
+                while (ties <= q && (u32)(sh.list[q - ties] >> 32) == key) ++ties;
+                for (int to = 0; to < row.cs; ++to) {
+                    if (row.cs > 1) {
+                        const u32 answer = map_cluster(smem_u32(sh.answer), to);
+                        st_cluster_b64(answer, (u64)key << 32 | ties);
+                        st_cluster_b64(answer + 8, before);
+                    } else {
+                        sh.answer[0] = (u64)key << 32 | ties;
+                        sh.answer[1] = before;
+                    }
+                }
+            }
+        }
+        row.sync();
+        Cut out{(u32)(sh.answer[0] >> 32), (u32)sh.answer[0], 0};
+        out.weight = Weigh::fixed(Weigh::w(g.depth(Key<T>::value(out.key))));
+        if (out.key == in.key) out.ties = min(out.ties, in.ties);
+        // this warp's entries of the list
+        u64 sum = lane_w;
+        u32 ties = 0;
+        for (u32 i = lane; i < own; i += 32) {
+            const u64 e = sh.own_list[i];
+            const int v = ((int)~(u32)e + row.r.head) / E;
+            if (v < row.sl.wlo || v >= row.sl.whi) continue;
+            const u32 key = (u32)(e >> 32);
+            if (key > out.key) sum += Weigh::fixed(Weigh::w(g.depth(Key<T>::value(key))));
+            ties += key == out.key;
+        }
+        const u64 kept_w = sh.answer[1];
+        __syncthreads();
+        return {out, kept_w, true, warp_sum(sum), __reduce_add_sync(0xffffffffu, ties), row.sl.up};
+    }
+
     u32 hi = __reduce_max_sync(0xffffffffu, hi_x >= lo_x ? Key<T>::of(hi_x) : 0);
     u32 lo = __reduce_min_sync(0xffffffffu, hi_x >= lo_x ? Key<T>::of(lo_x) : 0xffffffffu);
     if (lane == 0) {
@@ -467,16 +651,20 @@ __device__ __noinline__ Found find_cut(Shared& sh, Row<T> row, const Weigh g, bo
         const int shift = max(0, 32 - __clz((hi - lo) | 1) - 9);
         const float hi_v = Key<T>::value(hi), lo_v = Key<T>::value(lo);
         clear();
-        row.each_pair(g, plain, [&](float2 x, float2 d) {
+        row.each_pair(g, plain, [&](int, float2 x, float2 d) {
             auto add = [&](float x, float d) {
                 if (!(x >= lo_v && x <= hi_v)) return;
-                u32* h = reinterpret_cast<u32*>(&sh.hist[(hi - Key<T>::of(x)) >> shift]);
+                u32* h = reinterpret_cast<u32*>(&sh.bins[(hi - Key<T>::of(x)) >> shift]);
+                if (BY_COUNT) {
+                    atomicAdd(h, 1u);
+                    return;
+                }
                 const u64 W = Weigh::fixed(Weigh::w(d));
-                if (BY_COUNT) atomicAdd(h, 1u);
-                if (BY_COUNT && !weigh) return;
-                atomicAdd(h + 1, (u32)W & ((1u << kLimb) - 1));
-                atomicAdd(h + 2, (u32)(W >> kLimb) & ((1u << kLimb) - 1));
-                atomicAdd(h + 3, (u32)(W >> (2 * kLimb)));
+                constexpr u32 kMask = (1u << kLimb) - 1;
+                atomicAdd(h, (u32)W & kMask);
+                atomicAdd(h + 1, (u32)(W >> kLimb) & kMask);
+                atomicAdd(h + 2, (u32)(W >> (2 * kLimb)) & kMask);
+                atomicAdd(h + 3, (u32)(W >> (3 * kLimb)));
             };
             add(x.x, d.x);
             add(x.y, d.y);
@@ -484,115 +672,74 @@ __device__ __noinline__ Found find_cut(Shared& sh, Row<T> row, const Weigh g, bo
         find_bin<BY_COUNT>(sh, row, n, w, k, limit);
         if (sh.at == kBins) break;  // not reached: the bracket holds the cut
         n = sh.before_n;
-        w = sh.before_w;
-        in_w = sh.in_w;
+        if (!BY_COUNT) {
+            w = sh.before_w;
+            in_w = sh.in_w;
+        }
         hi -= (u32)sh.at << shift;
         lo = hi - min(hi - lo, (1u << shift) - 1);
         more = more && hi != lo;
     }
     Cut out{hi, 0, Weigh::fixed(Weigh::w(g.depth(Key<T>::value(hi))))};
-    out.ties = BY_COUNT ? k - n : ties_below(w, out.weight, (u32)(in_w / max(out.weight, (u64)1)), limit);
+    if (BY_COUNT) {
+        out.ties = k - n;
+    } else {  // those of the ties with less than `limit` before them
+        const u64 W = max(out.weight, (u64)1);
+        out.ties = (u32)min(in_w / W, (limit - w + W - 1) / W);
+    }
     if (hi == in.key) out.ties = min(out.ties, in.ties);
+    if (BY_COUNT && weigh) {
+        u32 none;
+        kept_weight(row, g, plain, out, 0.f, w, none);
+        w = row_weight(sh, row, w);
+    }
     __syncthreads();
-    return {out, w + out.ties * out.weight, row.sl.up};
-}
-
-// This lane's part of its warp's weight: all entries.
-template <typename T>
-__device__ __forceinline__ u64 all_weight(Row<T>& row, const Weigh& g, bool plain) {
-    WeightSum ws;
-    int entries = 0;
-    row.each_pair(g, plain, [&](float2, float2 d) {
-        ws.add(pair(ex2(d.x), ex2(d.y)));
-        entries += 2;
-    });
-    return ws.total(entries);
-}
-
-// This lane's part of its warp's kept weight, and its ties at the cut.
-template <typename T>
-__device__ __forceinline__ void kept_weight(Row<T>& row, const Weigh& g, bool plain,
-                                            const Cut& cut, float min_p, u64& weight, u32& ties) {
-    const float floor = cut.key != 0 ? Key<T>::value(cut.key) : neg_inf();
-    const float least = min_p > 0.f ? min_p : 0.f;
-    WeightSum ws;
-    int entries = 0;
-    u32 t = 0;
-    row.each_pair(g, plain, [&](float2 x, float2 d) {
-        const float wx = ex2(d.x), wy = ex2(d.y);
-        const bool kx = wx >= least, ky = wy >= least;
-        ws.add(pair(kx && x.x > floor ? wx : 0.f, ky && x.y > floor ? wy : 0.f));
-        t += (kx && x.x == floor) + (ky && x.y == floor);
-        entries += 2;
-    });
-    weight = ws.total(entries);
-    ties = cut.ties != 0 ? t : 0;
-}
-
-// u * total as a whole number below total (u outside [0, 1): the nearer end).
-__device__ __forceinline__ u64 target_of(float u, u64 total) {
-    return min((u64)__double2ull_rz((double)(u > 0.f ? u : 0.f) * (double)total), total - 1);
-}
-
-// A listed entry: larger ones come first in the order of falling values.
-template <typename T>
-__device__ __forceinline__ u64 entry_of(float x, int index) {
-    return (u64)Key<T>::of(x) << 32 | (u32)~index;
+    return {out, w + out.ties * out.weight, false, 0, 0, row.sl.up};
 }
 
 // Finishes a row from its list of n entries, which holds the first k (k > 0) or those
 // that reach p of the row's weight `all` (k == 0).  One CTA.
 template <typename T>
-__device__ __noinline__ void finish_list(const SampleArgs& a, Shared& sh, const Weigh g, int rowi, int n, int k,
-                            float p, float min_p, u64 all) {
+__device__ __noinline__ void finish_list(const SampleArgs& a, Shared& sh, const Weigh g, int rowi,
+                                         int n, int k, float p, float min_p, u64 all) {
     constexpr int kPer = kListMax / kRowThreads;
     const int tid = threadIdx.x;
-    __syncthreads();  // `sorted` takes the place of this CTA's own list
-    for (int i = tid; i < n; i += kRowThreads) {
-        const u64 e = sh.list[i];
-        int before = 0;
-        for (int j = 0; j < n; ++j) before += sh.list[j] > e;
-        sh.sorted[before] = e;
-    }
-    __syncthreads();
+    sort_list(sh, n);
     const int last = k > 0 ? min(k, n) : n;
-    u64 W[kPer], sum = 0;
+    u64 W[kPer], before = 0;
     float w[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int at = tid * kPer + i;
-        w[i] = at < last ? Weigh::w(g.depth(Key<T>::value((u32)(sh.sorted[at] >> 32)))) : 0.f;
+        w[i] = at < last ? Weigh::w(g.depth(Key<T>::value((u32)(sh.list[at] >> 32)))) : 0.f;
         W[i] = Weigh::fixed(w[i]);
-        sum += W[i];
+        sh.weight[at] = W[i];
+        before += W[i];
     }
-    u64 before = warp_before(sum);
-    u32 none = 0;
-    u64 total = sum;
-    block_sum(sh, none, total);
-    for (int i = 0; i < tid >> 5; ++i) before += sh.scan_w[i];
-    const double limit = (double)p * (double)(k > 0 ? total : all);
     u32 kept = 0;
-    u64 kept_w = 0;
+    u64 kept_w = block_before(sh, kept, before);
+    const u64 limit = p < 1.f ? limit_of(p, k > 0 ? kept_w : all) : ~0ull;
+    kept_w = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int at = tid * kPer + i;
-        if (at == 0 || (at < last && (!(p < 1.f) || (double)before < limit) && !(w[i] < min_p))) {
+        if (at == 0 || (at < last && before < limit && !(w[i] < min_p))) {
             ++kept;
             kept_w += W[i];
         }
         before += W[i];
-        sh.list[at] = W[i];  // the list is read: weights by place now
     }
     block_sum(sh, kept, kept_w);
     const u64 target = target_of(a.uniform[rowi], kept_w);
     for (int i = tid; i < (int)kept; i += kRowThreads) {
-        const u32 index = (u32)sh.sorted[i];  // ~index
+        const u32 index = (u32)sh.list[i];  // ~index
         u64 cum = 0;
+#pragma unroll 4
         for (int j = 0; j < (int)kept; ++j)
-            if ((u32)sh.sorted[j] > index) cum += sh.list[j];
-        if (cum <= target && target < cum + sh.list[i]) {
+            if ((u32)sh.list[j] > index) cum += sh.weight[j];
+        if (cum <= target && target < cum + sh.weight[i]) {
             a.tokens[rowi] = (int)~index;
-            if (a.probs != nullptr) a.probs[rowi] = (float)((double)sh.list[i] / (double)kept_w);
+            if (a.probs != nullptr) a.probs[rowi] = (float)((double)sh.weight[i] / (double)kept_w);
         }
     }
 }
@@ -605,12 +752,23 @@ __device__ __forceinline__ float group_bound(const Shared& sh, int n) {
     u32 key[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) key[i] = Key<float>::of(sh.group_max[lane + 32 * i]) >> 16;
-    u32 lo = 0;  // the largest value that n keys reach, bit by bit
-    for (u32 bit = 0x8000; bit != 0; bit >>= 1) {
+    u32 lo = key[0], hi = key[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) {
+        lo = min(lo, key[i]);
+        hi = max(hi, key[i]);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);  // all keys reach it
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    while (lo < hi) {  // the largest value that n keys reach
+        const u32 mid = (lo + hi + 1) >> 1;
         u32 count = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) count += key[i] >= (lo | bit);
-        if (__reduce_add_sync(0xffffffffu, count) >= (u32)n) lo |= bit;
+        for (int i = 0; i < kPer; ++i) count += key[i] >= mid;
+        if (__reduce_add_sync(0xffffffffu, count) >= (u32)n)
+            lo = mid;
+        else
+            hi = mid - 1;
     }
     return Key<float>::value(lo << 16);
 }
@@ -625,7 +783,8 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
     const int cs = 1 << a.lg, rank = cs > 1 ? (int)cluster_ctarank() : 0;
     const int rowi = blockIdx.x >> a.lg;
     const RowView<T> r(a.logits, a.ld, rowi, a.V);
-    Row<T> row{r, RowSlice<Geo>(r, a.per, a.ring, rank, warp, smem, l2_policy_evict_last()), cs, rank};
+    Row<T> row{r, RowSlice<Geo>(r, a.per, a.ring, rank, warp, smem, l2_policy_evict_last()), a.lg, cs,
+               rank};
     const RowSlice<Geo>& sl = row.sl;
     if (cs > 1) cluster_arrive();  // met by cluster_wait below: every CTA has started
     row.sl.start(r);
@@ -682,14 +841,27 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
     const bool plain = !has_nan && m < INFINITY;
 
     Cut cut{0, 0, 0};
+    bool summed = false;
+    u64 sw = 0;
+    u32 st = 0;
     if (k > 0 || p < 1.f) {
-        // Is there a bound with a list short enough?  Without top_k: about as many entries
-        // above it as half the groups; in a row of up to kListMax, all of them.
+        u64 all = 0, limit = ~0ull;  // (without top_k) the row's weight and top_p's part of it
+        // Is a list short enough?  Without top_k: of about as many entries as half the
+        // groups, unless the groups' maxima are far from what top_p asks for; of a row of up
+        // to kListMax entries, all.
         const int want = k > 0 ? k : kGroups / 2;
-        u64 listed_all = 0;  // the row's whole weight (without top_k)
-        if (a.V <= kListMax || want <= kGroups) {
+        bool list = a.V <= kListMax || want <= kGroups;
+        if (k == 0) {
+            all = row_weight(sh, row, all_weight(row, g, plain));
+            limit = limit_of(p, all);
+            u64 most = tid < kGroups ? Weigh::fixed(Weigh::w(g.depth(sh.group_max[tid]))) : 0;
+            u32 none = 0;
+            block_sum(sh, none, most);
+            list = a.V <= kListMax || most >= limit / 4;
+        }
+        if (list) {
             if (warp == 0) {
-                float b = a.V <= kListMax ? -3.402823466e38f : group_bound(sh, want);
+                const float b = a.V <= kListMax ? neg_inf() : group_bound(sh, want);
                 if (lane == 0) sh.bound = b > -3.402823466e38f ? b : -3.402823466e38f;
             }
             __syncthreads();
@@ -707,65 +879,52 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
                     if (k == 0) listed_w += Weigh::fixed(Weigh::w(g.depth(x[j])));
                 }
             });
-            u64 all = k == 0 ? all_weight(row, g, plain) : 0;
             u32 none = 0;
-            if (k == 0) {
-                block_sum(sh, none, listed_w);
-                block_sum(sh, none, all);
-            } else {
-                __syncthreads();
-            }
-            const u32 n = sh.own_n;
+            if (k == 0) block_sum(sh, none, listed_w);
+            __syncthreads();
+            const u32 own = sh.own_n;
+            send_list(sh, row, own);
             if (cs > 1) {
-                // to rank 0's list, behind those that got there first
-                if (tid == 0)
-                    sh.base = n <= kListMax
-                                  ? atom_add_cluster(map_cluster(smem_u32(&sh.list_n), 0), n)
-                                  : kListMax;
-                __syncthreads();
-                for (u32 i = tid; i < n && sh.base + i < kListMax; i += kRowThreads)
-                    st_cluster_b64(map_cluster(smem_u32(&sh.list[sh.base + i]), 0),
-                                   sh.own_list[i]);
                 if (tid < cs) {
-                    const u32 told = map_cluster(smem_u32(&sh.told[rank]), tid);
-                    st_cluster_b64(told, n);
-                    st_cluster_b64(told + 8, listed_w);
-                    st_cluster_b64(told + 16, all);
+                    st_cluster_b64(map_cluster(smem_u32(&sh.told_n[rank]), tid), own);
+                    st_cluster_b64(map_cluster(smem_u32(&sh.told_w[rank]), tid), listed_w);
                 }
-            } else {
-                for (u32 i = tid; i < min(n, (u32)kListMax); i += kRowThreads)
-                    sh.list[i] = sh.own_list[i];
-                if (tid == 0) sh.told[0] = {n, listed_w, all};
+            } else if (tid == 0) {
+                sh.told_n[0] = own;
+                sh.told_w[0] = listed_w;
             }
             row.sync();
-            Told t{0, 0, 0};
+            u64 n = 0;
+            listed_w = 0;
             for (int i = 0; i < cs; ++i) {
-                t.listed += sh.told[i].listed;
-                t.weight += sh.told[i].weight;
-                t.all += sh.told[i].all;
+                n += sh.told_n[i];
+                listed_w += sh.told_w[i];
             }
-            if (t.listed <= kListMax &&
-                (k > 0 || (double)t.weight >= (double)p * (double)t.all)) {
+            if (n <= kListMax && (k > 0 || listed_w >= limit)) {
                 // the other CTAs' shared memory is not touched any more
-                if (rank == 0)
-                    finish_list<T>(a, sh, g, rowi, (int)t.listed, k, p, min_p, t.all);
+                if (rank == 0) finish_list<T>(a, sh, g, rowi, (int)n, k, p, min_p, all);
                 return;
             }
-            listed_all = t.all;
             __syncthreads();
         }
-        u64 kept = listed_all;
+        u64 kept = all;
         if (k > 0) {
             const Found f = find_cut<true>(sh, row, g, plain, cut, (u32)k, 0, p < 1.f);
             cut = f.cut;
             kept = f.kept_w;
             row.sl.up = f.up;
+            summed = f.summed;
+            sw = f.warp_w;
+            st = f.warp_t;
         }
         if (p < 1.f) {
             const Found f =
-                find_cut<false>(sh, row, g, plain, cut, 0, (double)p * (double)kept, true);
+                find_cut<false>(sh, row, g, plain, cut, 0, limit_of(p, kept), true);
             cut = f.cut;
             row.sl.up = f.up;
+            summed = f.summed;
+            sw = f.warp_w;
+            st = f.warp_t;
         }
     }
 
@@ -801,19 +960,19 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
                 ties += Weigh::fixed(wj) != 0;
         }
     };
-    u64 sw = 0;
-    u32 st = 0;
-    if (everything)
-        sw = all_weight(row, g, plain);
-    else
-        kept_weight(row, g, plain, cut, min_p, sw, st);
-    sw = warp_sum(sw);
-    st = __reduce_add_sync(0xffffffffu, st);
+    if (!summed || min_p > 0.f) {
+        if (everything)
+            sw = all_weight(row, g, plain);
+        else
+            kept_weight(row, g, plain, cut, min_p, sw, st);
+        sw = warp_sum(sw);
+        st = __reduce_add_sync(0xffffffffu, st);
+    }
     const int me = rank * kRowWarps + warp;
     if (cs > 1) {
         if (lane < cs) {
             st_cluster_b64(map_cluster(smem_u32(&sh.part_w[me]), lane), sw);
-            st_cluster_b64(map_cluster(smem_u32(&sh.part_t[me]), lane), st);
+            st_cluster_f32(map_cluster(smem_u32(&sh.part_t[me]), lane), __uint_as_float(st));
         }
     } else if (lane == 0) {
         sh.part_w[me] = sw;
@@ -821,116 +980,131 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
     }
     row.sync();  // no CTA's shared memory is touched from outside after this
 
-    // the warp that holds the token (every warp finds it: `per` parts a lane)
+    // The part of the row that holds the token: of the warps' parts, then, by the warps of
+    // that CTA, of their 32 vectors at a time, then of a warp's lanes and their entries.
     auto ties_weight = [&](u32 before, u32 n) {
-        return (u64)(min(cut.ties, before + n) - min(cut.ties, before)) * cut.weight;
+        return cut.ties == 0 ? 0
+                             : (u64)(min(cut.ties, before + n) - min(cut.ties, before)) * cut.weight;
     };
-    const int parts = cs * kRowWarps, per = max(1, parts >> 5);
-    const int p_lo = min(lane * per, parts), p_hi = min(p_lo + per, parts);
-    u32 ties = 0;  // before this lane's parts
-    if (cut.ties != 0) {
-        for (int i = p_lo; i < p_hi; ++i) ties += (u32)sh.part_t[i];
-        ties = warp_before(ties);
-    }
-    u64 lane_w = 0;
-    u32 tie = ties;
-    for (int i = p_lo; i < p_hi; ++i) {
-        lane_w += sh.part_w[i];
-        if (cut.ties == 0) continue;
-        lane_w += ties_weight(tie, (u32)sh.part_t[i]);
-        tie += (u32)sh.part_t[i];
-    }
-    u64 sum = warp_before(lane_w);
-    const u64 total = __shfl_sync(0xffffffffu, sum + lane_w, 31);
-    const u64 target = target_of(a.uniform[rowi], total);
-    const int from =
-        __ffs(__ballot_sync(0xffffffffu, sum <= target && target < sum + lane_w)) - 1;
-    int holder = p_lo;
-    for (; holder < p_hi - 1; ++holder) {
-        const u64 w = sh.part_w[holder] + ties_weight(ties, (u32)sh.part_t[holder]);
-        if (target < sum + w) break;
-        sum += w;
-        ties += (u32)sh.part_t[holder];
-    }
-    holder = __shfl_sync(0xffffffffu, holder, from);
-    if (holder / kRowWarps != rank) return;
-    sum = __shfl_sync(0xffffffffu, sum, from);  // kept weight and ties before this warp
-    ties = __shfl_sync(0xffffffffu, ties, from);
-
-    // that warp's steps, by all warps of its CTA; then the warp of the step that holds it
-    const RowSlice<Geo> own(r, a.per, a.ring, rank, holder % kRowWarps, smem, 0);
-    for (int step = warp; step < own.steps; step += kRowWarps) {
-        u64 w = 0;
-        u32 t = 0;
-#pragma unroll
-        for (int i = 0; i < kStepVecs; i += 32) {
-            const int v = own.wlo + step * kStepVecs + i + lane;
-            if (v < own.whi) kept_of(r.load(v), w, t);
+    struct Place {  // the parts of a lane, [lo, hi), and what stands before them
+        int lo, hi;
+        u64 sum, own;
+        u32 ties;
+    };
+    auto scan = [&](const u64* w, const u32* t, int n, u64 sum, u32 ties) {
+        const int per = (n + 31) >> 5;
+        Place q;
+        q.lo = min(lane * per, n);
+        q.hi = min(q.lo + per, n);
+        u32 own_t = 0;
+        if (cut.ties != 0)
+            for (int i = q.lo; i < q.hi; ++i) own_t += t[i];
+        q.ties = ties + (cut.ties != 0 ? warp_before(own_t) : 0);
+        q.own = 0;
+        u32 tie = q.ties;
+        for (int i = q.lo; i < q.hi; ++i) {
+            q.own += w[i] + ties_weight(tie, t[i]);
+            tie += t[i];
         }
-        w = warp_sum(w);
-        t = __reduce_add_sync(0xffffffffu, t);
-        if (lane == 0) {
-            sh.step_w[step] = w;
-            sh.step_t[step] = t;
+        q.sum = sum + warp_before(q.own);
+        return q;
+    };
+    // the part that holds `target`, for every lane; q: what stands before it
+    auto pick = [&](const u64* w, const u32* t, Place& q, u64 target) {
+        const int from =
+            __ffs(__ballot_sync(0xffffffffu, q.sum <= target && target < q.sum + q.own)) - 1;
+        int i = q.lo;
+        for (; i < q.hi - 1; ++i) {
+            const u64 one = w[i] + ties_weight(q.ties, t[i]);
+            if (target < q.sum + one) break;
+            q.sum += one;
+            q.ties += t[i];
+        }
+        q.sum = __shfl_sync(0xffffffffu, q.sum, from);
+        q.ties = __shfl_sync(0xffffffffu, q.ties, from);
+        return __shfl_sync(0xffffffffu, i, from);
+    };
+    Place q = scan(sh.part_w, sh.part_t, cs * kRowWarps, 0, 0);
+    const u64 total = __shfl_sync(0xffffffffu, q.sum + q.own, 31);
+    const u64 target = target_of(a.uniform[rowi], total);
+    const int holder = pick(sh.part_w, sh.part_t, q, target);
+    if (holder / kRowWarps != rank) return;
+
+    const RowSlice<Geo> own(r, a.per, a.ring, rank, holder % kRowWarps, smem, 0);
+    const int units = (own.whi - own.wlo + 31) >> 5;
+    constexpr int kAhead = 3;  // units of a warp loaded together
+    for (int u0 = warp; u0 < units; u0 += kAhead * kRowWarps) {
+        uint4 vec[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int v = own.wlo + (u0 + i * kRowWarps) * 32 + lane;
+            vec[i] = v < own.whi ? r.load(v) : r.nothing();
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int unit = u0 + i * kRowWarps;
+            if (unit >= units) break;
+            u64 w = 0;
+            u32 t = 0;
+            kept_of(vec[i], w, t);
+            w = warp_sum(w);
+            t = __reduce_add_sync(0xffffffffu, t);
+            if (lane == 0) {
+                sh.unit_w[unit] = w;
+                sh.unit_t[unit] = t;
+            }
         }
     }
     __syncthreads();
-    int step = 0;
-    for (; step < own.steps - 1; ++step) {
-        const u64 w = sh.step_w[step] + ties_weight(ties, sh.step_t[step]);
-        if (target < sum + w) break;
-        sum += w;
-        ties += sh.step_t[step];
-    }
-    if (step % kRowWarps != warp) return;
-    for (int i = 0; i < kStepVecs; i += 32) {  // its vectors 32 at a time: the lane, the entry
-        const int v = own.wlo + step * kStepVecs + i + lane;
-        u64 lw = 0;
-        u32 lt = 0;
-        if (v < own.whi) kept_of(r.load(v), lw, lt);
-        u32 tie = ties + warp_before(lt);
-        ties += __reduce_add_sync(0xffffffffu, lt);
-        lw += ties_weight(tie, lt);
-        u64 at = sum + warp_before(lw);
-        sum = __shfl_sync(0xffffffffu, at + lw, 31);
-        if (at > target || target >= at + lw) continue;
-        float x[E];
-        unpack(r.load(v), x);
-        int token = -1;
-        u64 tw = 0;
+    if (warp > 0) return;
+    q = scan(sh.unit_w, sh.unit_t, units, q.sum, q.ties);
+    const int v = own.wlo + pick(sh.unit_w, sh.unit_t, q, target) * 32 + lane;
+    const uint4 vec = v < own.whi ? r.load(v) : r.nothing();
+    u64 lw = 0;
+    u32 lt = 0;
+    kept_of(vec, lw, lt);
+    u32 tie = q.ties + (cut.ties != 0 ? warp_before(lt) : 0);
+    lw += ties_weight(tie, lt);
+    u64 at = q.sum + warp_before(lw);
+    if (at > target || target >= at + lw) return;
+    float x[E];
+    unpack(vec, x);
+    int token = -1;
+    u64 tw = 0;
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const u32 key = Key<T>::of(x[j]);
-            const float wj = Weigh::w(g.depth(x[j]));
-            u64 w = wj < min_p ? 0 : Weigh::fixed(wj);
-            if (key < cut.key) {
-                w = 0;
-            } else if (key == cut.key && w != 0) {
-                w = ties_weight(tie, 1);
-                ++tie;
-            }
-            at += w;
-            if (token < 0 && target < at) {
-                token = v * E + j - r.head;
-                tw = w;
-            }
+    for (int j = 0; j < E; ++j) {
+        const u32 key = Key<T>::of(x[j]);
+        const float wj = Weigh::w(g.depth(x[j]));
+        u64 w = wj < min_p ? 0 : Weigh::fixed(wj);
+        if (key < cut.key) {
+            w = 0;
+        } else if (key == cut.key && w != 0) {
+            w = ties_weight(tie, 1);
+            ++tie;
         }
-        a.tokens[rowi] = token;
-        if (a.probs != nullptr) a.probs[rowi] = (float)((double)tw / (double)total);
+        at += w;
+        if (token < 0 && target < at) {
+            token = v * E + j - r.head;
+            tw = w;
+        }
     }
+    a.tokens[rowi] = token;
+    if (a.probs != nullptr) a.probs[rowi] = (float)((double)tw / (double)total);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(SampleArgs a, int bf16, cudaStream_t stream, int num_sms) {
     // the widest row: kSampleMaxV fp32 entries over the largest cluster
-    static_assert(kSampleMaxV / 4 / kRowMaxCluster / kRowWarps / kStepVecs < kMaxSteps);
+    static_assert(kSampleMaxV / 4 / kRowMaxCluster / kRowWarps / 32 < kMaxUnits);
     const RowSplit p = split_rows<Geo>(a.rows, a.V, bf16 ? 2 : 4, num_sms);
     a.lg = p.lg;
     a.per = p.per;
     a.ring = p.ring;
-    return launch_rows<Geo>(bf16 ? sample_kernel<__nv_bfloat16> : sample_kernel<float>, a, a.rows, a.lg,
-                       p.smem, stream);
+    if (bf16)
+        return launch_rows<Geo, sample_kernel<__nv_bfloat16>>(a, a.rows, a.lg, p.smem,
+                                                              Geo::kRingBytes, stream);
+    return launch_rows<Geo, sample_kernel<float>>(a, a.rows, a.lg, p.smem, Geo::kRingBytes, stream);
 }
 
 }  // namespace df2
