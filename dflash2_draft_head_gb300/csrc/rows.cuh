@@ -133,28 +133,39 @@ __device__ __forceinline__ float vec_max<__nv_bfloat16>(const uint4& v) {
     return fmaxf(__low2float(c), __high2float(c));
 }
 
-// The same, but NaN where one of the elements is.
+// The largest element of vectors, NaN where one of them is.
 __device__ __forceinline__ float max_or_nan(float a, float b) {
     float m;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
     return m;
 }
 template <typename T>
-__device__ __forceinline__ float vec_max_or_nan(const uint4& v);
+struct RunningMax;
 template <>
-__device__ __forceinline__ float vec_max_or_nan<float>(const uint4& v) {
-    return max_or_nan(max_or_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
-                      max_or_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
-}
+struct RunningMax<float> {
+    float m;
+    __device__ __forceinline__ RunningMax() : m(neg_inf()) {}
+    __device__ __forceinline__ void add(const uint4& v) {
+        m = max_or_nan(m, max_or_nan(max_or_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                                     max_or_nan(__uint_as_float(v.z), __uint_as_float(v.w))));
+    }
+    __device__ __forceinline__ float value() const { return m; }
+};
 template <>
-__device__ __forceinline__ float vec_max_or_nan<__nv_bfloat16>(const uint4& v) {
-    const __nv_bfloat162 a = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v.x),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&v.y));
-    const __nv_bfloat162 b = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v.z),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&v.w));
-    const __nv_bfloat162 c = __hmax2_nan(a, b);
-    return max_or_nan(__low2float(c), __high2float(c));
-}
+struct RunningMax<__nv_bfloat16> {
+    __nv_bfloat162 m;
+    __device__ __forceinline__ RunningMax() : m(__float2bfloat162_rn(neg_inf())) {}
+    __device__ __forceinline__ void add(const uint4& v) {
+        const __nv_bfloat162 a = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v.x),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&v.y));
+        const __nv_bfloat162 b = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v.z),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&v.w));
+        m = __hmax2_nan(m, __hmax2_nan(a, b));
+    }
+    __device__ __forceinline__ float value() const {
+        return max_or_nan(__low2float(m), __high2float(m));
+    }
+};
 
 // Four or eight fp32 values as one vector, rounded to the row's type.
 __device__ __forceinline__ uint4 pack(const float (&f)[4]) {

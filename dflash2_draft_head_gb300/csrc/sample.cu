@@ -22,10 +22,11 @@
 //     reach: those entries (some hundreds) are listed, and one CTA finishes the row
 //     from the list alone.
 //   - Else counts over the distance from the maximum (a bin's weights differ by 1.4%)
-//     leave a few bins that may hold the cut.  Up to 1024 entries there are listed and
-//     sorted; more of them (ties) are told apart by histograms of their exact weights
-//     over their values, until the cut lies in one value.  What is kept is then summed
-//     by warp and looked through as in the first case.
+//     leave a bracket of bins that may hold the cut; the exact weight above it narrows
+//     it to one or two.  Up to 1024 entries there are listed and sorted; more of them
+//     (ties) are told apart by histograms of their exact weights over their values,
+//     until the cut lies in one value.  What is kept is then summed by warp and looked
+//     through as in the first case.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -203,6 +204,12 @@ struct Shared {
     u64 before_w, in_w;
 };
 
+// The CTA's, from any function (known to lie in shared memory, unlike an argument).
+__device__ __forceinline__ Shared& shared_block() {
+    __shared__ Shared sh;
+    return sh;
+}
+
 template <typename T>
 struct Row {
     static constexpr int E = VecOf<T>::kElems;
@@ -333,9 +340,8 @@ __device__ __forceinline__ uint4 merge_bins(Shared& sh, const R& row) {
     return sh.total[tid];
 }
 
-__device__ __forceinline__ int depth_bin(float d) {
-    return min(kDepthBins - 1, (int)(d * -(kDepthBins / kDepth)));
-}
+// The depth in bins: its whole part is the bin.
+__device__ __forceinline__ float depth_bins(float d) { return d * -(kDepthBins / kDepth); }
 
 // The bounds of a weight in that bin, in units of 2^-40: the roundings of the depth,
 // of 2^x and of the weight are far inside 2^-16 of it and 1.
@@ -386,32 +392,65 @@ __device__ __forceinline__ u64 entry_of(float x, int index) {
     return (u64)Key<T>::of(x) << 32 | (u32)~index;
 }
 
-// Sorts the row's list of n entries, first ones first: every entry counts those before
-// it.  One CTA.
+// Sorts the row's list of n entries, first ones first.  One CTA.  Up to kCountSort of
+// them: every entry counts those before it, n^2 steps on all threads.  More: a bitonic
+// network over the next power of two, two entries a thread, through shuffles inside a
+// warp and shared memory beyond (436 entries: 1 us, against 4 us by counting).
+constexpr int kCountSort = 128;
 __device__ __forceinline__ void sort_list(Shared& sh, int n) {
-    constexpr int kPer = kListMax / kRowThreads;
     const int tid = threadIdx.x;
-    u64 e[kPer];
-    int before[kPer] = {};
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) e[i] = tid + i * kRowThreads < n ? sh.list[tid + i * kRowThreads] : 0;
-    if (tid < n) {
-        if (n <= kRowThreads) {
+    if (n <= kCountSort) {
+        u64 e = 0;
+        int before = 0;
+        if (tid < n) {
+            e = sh.list[tid];
 #pragma unroll 8
-            for (int j = 0; j < n; ++j) before[0] += sh.list[j] > e[0];
-        } else {
-#pragma unroll 4
-            for (int j = 0; j < n; ++j) {
-                const u64 o = sh.list[j];
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) before[i] += o > e[i];
-            }
+            for (int j = 0; j < n; ++j) before += sh.list[j] > e;
         }
+        __syncthreads();
+        if (tid < n) sh.list[before] = e;
+        __syncthreads();
+        return;
+    }
+    static_assert(kListMax == 2 * kRowThreads);
+    const int size = 1 << (32 - __clz(n - 1));
+    const bool live = 2 * tid < size;
+    u64 e[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) e[i] = 2 * tid + i < n ? sh.list[2 * tid + i] : 0;
+    auto order = [](u64& a, u64& b, bool falling) {
+        if ((a < b) == falling) {
+            const u64 t = a;
+            a = b;
+            b = t;
+        }
+    };
+    for (int k = 2; k <= size; k <<= 1) {
+        const bool falling = (2 * tid & k) == 0;
+        for (int j = k >> 1; j > 1; j >>= 1) {
+            const bool first = (2 * tid & j) == 0;  // the lower place of the two
+            u64 o[2];
+            if (j < 64) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) o[i] = __shfl_xor_sync(0xffffffffu, e[i], j >> 1);
+            } else {
+                __syncthreads();
+                if (live) *reinterpret_cast<ulonglong2*>(&sh.list[2 * tid]) = make_ulonglong2(e[0], e[1]);
+                __syncthreads();
+                if (live) {
+                    const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(&sh.list[2 * tid ^ j]);
+                    o[0] = p.x;
+                    o[1] = p.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (live && (e[i] < o[i]) == (falling == first)) e[i] = o[i];
+        }
+        order(e[0], e[1], falling);
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        if (tid + i * kRowThreads < n) sh.list[before[i]] = e[i];
+    if (live) *reinterpret_cast<ulonglong2*>(&sh.list[2 * tid]) = make_ulonglong2(e[0], e[1]);
     __syncthreads();
 }
 
@@ -433,22 +472,18 @@ __device__ __forceinline__ void send_list(Shared& sh, const R& row, u32 n) {
 
 // Finds, from the largest entries down, the depth bins that may hold the cut: sh.at to
 // sh.at_hi (one bin by count), with the counts before and up to them; sh.at is
-// kDepthBins when there is no cut.
-template <bool BY_COUNT, typename R>
-__device__ __forceinline__ void find_bracket(Shared& sh, const R& row, u32 k, u64 limit) {
-    const uint4 b = merge_bins(sh, row);
-    const u32 n[4] = {b.x, b.y, b.z, b.w};
+// kDepthBins when there is no cut.  b: this thread's merged counts; the cut is known to
+// lie in the bins from `from` to `to`, behind base_n entries of weight base_w.
+template <bool BY_COUNT>
+__device__ __forceinline__ void find_bracket(Shared& sh, const uint4& b, int from, int to,
+                                             u32 base_n, u64 base_w, u32 k, u64 limit) {
+    u32 n[4] = {b.x, b.y, b.z, b.w};
     const int first = (int)threadIdx.x * 4;
-    if (threadIdx.x == 0) {
-        sh.at = kDepthBins;
-        sh.at_hi = kDepthBins - 1;
-        sh.before_n = 0;
-        sh.upto_n = 0xffffffffu;
-    }
     u32 bn = 0, none = 0;
     u64 least = 0, most = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        if (first + i < from || first + i > to) n[i] = 0;
         bn += n[i];
         if (!BY_COUNT) {
             least += n[i] * bin_least(first + i);
@@ -457,6 +492,16 @@ __device__ __forceinline__ void find_bracket(Shared& sh, const R& row, u32 k, u6
     }
     block_before(sh, bn, least);
     if (!BY_COUNT) block_before(sh, none, most);
+    if (threadIdx.x == 0) {
+        sh.at = kDepthBins;
+        sh.at_hi = to;
+        sh.before_n = 0;
+        sh.upto_n = 0xffffffffu;
+    }
+    __syncthreads();
+    bn += base_n;
+    least += base_w;
+    most += base_w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const u64 l = BY_COUNT ? 0 : n[i] * bin_least(first + i);
@@ -502,7 +547,8 @@ __device__ __forceinline__ void find_bin(Shared& sh, const R& row, u32 base_n, u
 }
 
 // The cut by count (the first k entries) or by weight (those with less than `limit`
-// before them), among the entries inside `in`; `in` itself when that cuts nothing.
+// before them, of `all` of their weight), among the entries inside `in`; `in` itself when
+// that cuts nothing.
 struct Found {
     Cut cut;
     u64 kept_w;   // the kept entries' weight (by count: where `weigh` asks for it)
@@ -512,9 +558,10 @@ struct Found {
     bool up;      // the direction of the row's next pass
 };
 template <bool BY_COUNT, typename T>
-__device__ __noinline__ Found find_cut(Shared& sh, Row<T> row, const Weigh g, bool plain,
-                                       const Cut in, u32 k, u64 limit, bool weigh) {
+__device__ __noinline__ Found find_cut(Row<T> row, const Weigh g, bool plain,
+                                       const Cut in, u32 k, u64 limit, u64 all, bool weigh) {
     constexpr int E = VecOf<T>::kElems;
+    Shared& sh = shared_block();
     const int tid = threadIdx.x, lane = tid & 31;
     auto clear = [&] {
         sh.bins[tid] = make_uint4(0, 0, 0, 0);
@@ -526,41 +573,63 @@ __device__ __noinline__ Found find_cut(Shared& sh, Row<T> row, const Weigh g, bo
         __syncthreads();
     };
     const float least = in.key != 0 ? Key<T>::value(in.key) : neg_inf();
+    // by weight: entries below an even share of what is not kept come behind the cut (less
+    // 1 for their rounding, and 7% for that of the depth)
+    const float share = (float)(all - min(all, limit)) / (float)row.r.V - 1.f;
+    const float deepest = BY_COUNT ? -kDepth : fmaxf(-kDepth, log2f(fmaxf(share, 0.f)) - 40.1f);
     clear();
     row.each_pair(g, plain, [&](int, float2 x, float2 d) {
-        if (x.x >= least && d.x >= -kDepth) atomicAdd(&sh.count[depth_bin(d.x)], 1u);
-        if (x.y >= least && d.y >= -kDepth) atomicAdd(&sh.count[depth_bin(d.y)], 1u);
+        if (x.x >= least && d.x >= deepest)
+            atomicAdd(&sh.count[min(kDepthBins - 1, (int)depth_bins(d.x))], 1u);
+        if (x.y >= least && d.y >= deepest)
+            atomicAdd(&sh.count[min(kDepthBins - 1, (int)depth_bins(d.y))], 1u);
     });
-    find_bracket<BY_COUNT>(sh, row, k, limit);
-    const int at = sh.at, at_hi = sh.at_hi;
+    const uint4 counts = merge_bins(sh, row);
+    find_bracket<BY_COUNT>(sh, counts, 0, kDepthBins - 1, 0, 0, k, limit);
+    int at = sh.at, at_hi = sh.at_hi, summed_to = 0;  // bins whose weight is summed
+    u64 lane_w = 0, w = 0;
+    // adds the exact weight of the bins in [summed_to, at)
+    auto sum_up = [&](auto other) {
+        const float from = (float)summed_to, to = (float)at;
+        WeightSum sum;
+        int entries = 0;
+        row.each_pair(g, plain, [&](int index, float2 x, float2 d) {
+            const float bx = depth_bins(d.x), by = depth_bins(d.y);
+            const bool ix = x.x >= least && bx >= from && bx < to;
+            const bool iy = x.y >= least && by >= from && by < to;
+            const float wx = ex2(d.x), wy = ex2(d.y);
+            sum.add(pair(ix ? wx : 0.f, iy ? wy : 0.f));
+            entries += 2;
+            other(index, x.x, d.x, bx);
+            other(index + 1, x.y, d.y, by);
+        });
+        const u64 more = sum.total(entries);
+        lane_w += more;
+        w += row_weight(sh, row, more);
+        summed_to = at;
+    };
+    if (!BY_COUNT && at < kDepthBins && sh.upto_n - sh.before_n > kListMax) {
+        const u32 before = sh.before_n;
+        sum_up([](int, float, float, float) {});
+        find_bracket<false>(sh, counts, at, at_hi, before, w, k, limit);
+        at = min(sh.at, kDepthBins - 1);
+        at_hi = sh.at_hi;
+    }
     u32 n = sh.before_n;
     const u32 inside = sh.upto_n - n;
     const bool listed = at < kDepthBins && inside <= kListMax;
-
-    // the weight above the bracket; its entries, or the span of their keys
-    WeightSum above;
-    int entries = 0;
+    // the bracket's entries, or the span of their keys
+    const float lo_bin = (float)at, hi_bin = at_hi == kDepthBins - 1 ? INFINITY : at_hi + 1.f;
     float hi_x = neg_inf(), lo_x = INFINITY;
-    row.each_pair(g, plain, [&](int index, float2 x, float2 d) {
-        auto look = [&](int index, float x, float d) {
-            if (!(x >= least && d >= -kDepth)) return 0.f;
-            const int bin = depth_bin(d);
-            if (bin < at) return ex2(d);
-            if (bin > at_hi) return 0.f;
-            if (listed) {
-                sh.own_list[atomicAdd(&sh.own_n, 1u)] = entry_of<T>(x, index);
-            } else {
-                hi_x = fmaxf(hi_x, x);
-                lo_x = fminf(lo_x, x);
-            }
-            return 0.f;
-        };
-        const float wx = look(index, x.x, d.x);
-        above.add(pair(wx, look(index + 1, x.y, d.y)));
-        entries += 2;
+    sum_up([&](int index, float x, float d, float bin) {
+        if (!(bin >= lo_bin && bin < hi_bin && d >= deepest && x >= least)) return;
+        if (listed) {
+            sh.own_list[atomicAdd(&sh.own_n, 1u)] = entry_of<T>(x, index);
+        } else {
+            hi_x = fmaxf(hi_x, x);
+            lo_x = fminf(lo_x, x);
+        }
     });
-    const u64 lane_w = above.total(entries);
-    u64 w = row_weight(sh, row, lane_w);
     if (at == kDepthBins) return {in, w, false, 0, 0, row.sl.up};
     if (listed) {
         const u32 own = sh.own_n;
@@ -700,9 +769,10 @@ __device__ __noinline__ Found find_cut(Shared& sh, Row<T> row, const Weigh g, bo
 // Finishes a row from its list of n entries, which holds the first k (k > 0) or those
 // that reach p of the row's weight `all` (k == 0).  One CTA.
 template <typename T>
-__device__ __noinline__ void finish_list(const SampleArgs& a, Shared& sh, const Weigh g, int rowi,
+__device__ __noinline__ void finish_list(const SampleArgs& a, const Weigh g, int rowi,
                                          int n, int k, float p, float min_p, u64 all) {
     constexpr int kPer = kListMax / kRowThreads;
+    Shared& sh = shared_block();
     const int tid = threadIdx.x;
     sort_list(sh, n);
     const int last = k > 0 ? min(k, n) : n;
@@ -777,7 +847,7 @@ template <typename T>
 __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleArgs a) {
     constexpr int E = VecOf<T>::kElems;
     extern __shared__ __align__(16) char smem[];
-    __shared__ Shared sh;
+    Shared& sh = shared_block();
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cs = 1 << a.lg, rank = cs > 1 ? (int)cluster_ctarank() : 0;
@@ -801,8 +871,9 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
     // the largest entries of the groups (kLanes * cs lanes each) and of the row
     constexpr int kLanes = kRowThreads / kGroups;
     static_assert(kLanes >= 1 && kLanes * kRowMaxCluster <= 32);
-    float m = neg_inf();
-    row.each_vec([&](int, const uint4& v) { m = max_or_nan(m, vec_max_or_nan<T>(v)); });
+    RunningMax<T> most;
+    row.each_vec([&](int, const uint4& v) { most.add(v); });
+    float m = most.value();
     const bool has_nan = __any_sync(0xffffffffu, m != m);
     if (has_nan) {
         m = neg_inf();
@@ -902,14 +973,14 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
             }
             if (n <= kListMax && (k > 0 || listed_w >= limit)) {
                 // the other CTAs' shared memory is not touched any more
-                if (rank == 0) finish_list<T>(a, sh, g, rowi, (int)n, k, p, min_p, all);
+                if (rank == 0) finish_list<T>(a, g, rowi, (int)n, k, p, min_p, all);
                 return;
             }
             __syncthreads();
         }
         u64 kept = all;
         if (k > 0) {
-            const Found f = find_cut<true>(sh, row, g, plain, cut, (u32)k, 0, p < 1.f);
+            const Found f = find_cut<true>(row, g, plain, cut, (u32)k, 0, 0, p < 1.f);
             cut = f.cut;
             kept = f.kept_w;
             row.sl.up = f.up;
@@ -919,7 +990,7 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
         }
         if (p < 1.f) {
             const Found f =
-                find_cut<false>(sh, row, g, plain, cut, 0, limit_of(p, kept), true);
+                find_cut<false>(row, g, plain, cut, 0, limit_of(p, kept), kept, true);
             cut = f.cut;
             row.sl.up = f.up;
             summed = f.summed;
