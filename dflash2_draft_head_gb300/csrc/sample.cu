@@ -340,16 +340,42 @@ __device__ __forceinline__ uint4 merge_bins(Shared& sh, const R& row) {
     return sh.total[tid];
 }
 
-// The depth in bins: its whole part is the bin.
-__device__ __forceinline__ float depth_bins(float d) { return d * -(kDepthBins / kDepth); }
+// The bin of a depth: d in bins, rounded by the addition of 2^23, which leaves it in the
+// low bits.
+constexpr float kBinScale = (kDepthBins - 1) / kDepth;
+constexpr float kRound = 8388608.f;
+__device__ __forceinline__ u32 depth_bin(float d) {
+    return __float_as_uint(__fmaf_rn(d, -kBinScale, kRound)) - __float_as_uint(kRound);
+}
+__device__ __forceinline__ uint2 depth_bins(f32x2 d) {
+    const float2 t = halves(fma2(d, pair(-kBinScale, -kBinScale), pair(kRound, kRound)));
+    return make_uint2(__float_as_uint(t.x) - __float_as_uint(kRound),
+                      __float_as_uint(t.y) - __float_as_uint(kRound));
+}
+
+// The depth such that those above it, and no others, lie in bins before `bin`.
+__device__ __forceinline__ float depth_edge(int bin) {
+    if (bin <= 0) return INFINITY;
+    if (bin >= kDepthBins) return -INFINITY;
+    const u32 near = __float_as_uint((bin - 0.5f) / kBinScale);
+    u32 lo = near - 64, hi = near + 64;  // the least number in (lo, hi] in that bin or behind
+    while (hi - lo > 1) {
+        const u32 mid = (lo + hi) >> 1;
+        if (depth_bin(-__uint_as_float(mid)) >= (u32)bin)
+            hi = mid;
+        else
+            lo = mid;
+    }
+    return -__uint_as_float(hi);
+}
 
 // The bounds of a weight in that bin, in units of 2^-40: the roundings of the depth,
 // of 2^x and of the weight are far inside 2^-16 of it and 1.
 __device__ __forceinline__ u64 bin_most(int bin) {
-    return __float2ull_ru(ex2(bin * -(kDepth / kDepthBins)) * (kOne * (1.f + 1.f / 65536))) + 1;
+    return __float2ull_ru(ex2((bin - 0.5f) * -(1.f / kBinScale)) * (kOne * (1.f + 1.f / 65536))) + 1;
 }
 __device__ __forceinline__ u64 bin_least(int bin) {
-    const u64 w = __float2ull_rd(ex2((bin + 1) * -(kDepth / kDepthBins)) *
+    const u64 w = __float2ull_rd(ex2((bin + 0.5f) * -(1.f / kBinScale)) *
                                  (kOne * (1.f - 1.f / 65536)));
     return bin == kDepthBins - 1 || w == 0 ? 0 : w - 1;
 }
@@ -557,7 +583,7 @@ struct Found {
     u32 warp_t;
     bool up;      // the direction of the row's next pass
 };
-template <bool BY_COUNT, typename T>
+template <bool BY_COUNT, bool INSIDE, typename T>
 __device__ __noinline__ Found find_cut(Row<T> row, const Weigh g, bool plain,
                                        const Cut in, u32 k, u64 limit, u64 all, bool weigh) {
     constexpr int E = VecOf<T>::kElems;
@@ -572,45 +598,33 @@ __device__ __noinline__ Found find_cut(Row<T> row, const Weigh g, bool plain,
         }
         __syncthreads();
     };
-    const float least = in.key != 0 ? Key<T>::value(in.key) : neg_inf();
+    const float least = INSIDE ? Key<T>::value(in.key) : neg_inf();
     // by weight: entries below an even share of what is not kept come behind the cut (less
     // 1 for their rounding, and 7% for that of the depth)
     const float share = (float)(all - min(all, limit)) / (float)row.r.V - 1.f;
     const float deepest = BY_COUNT ? -kDepth : fmaxf(-kDepth, log2f(fmaxf(share, 0.f)) - 40.1f);
     clear();
     row.each_pair(g, plain, [&](int, float2 x, float2 d) {
-        if (x.x >= least && d.x >= deepest)
-            atomicAdd(&sh.count[min(kDepthBins - 1, (int)depth_bins(d.x))], 1u);
-        if (x.y >= least && d.y >= deepest)
-            atomicAdd(&sh.count[min(kDepthBins - 1, (int)depth_bins(d.y))], 1u);
+        const uint2 bin = depth_bins(pair(d.x, d.y));
+        if (d.x >= deepest && (!INSIDE || x.x >= least)) atomicAdd(&sh.count[bin.x], 1u);
+        if (d.y >= deepest && (!INSIDE || x.y >= least)) atomicAdd(&sh.count[bin.y], 1u);
     });
     const uint4 counts = merge_bins(sh, row);
     find_bracket<BY_COUNT>(sh, counts, 0, kDepthBins - 1, 0, 0, k, limit);
-    int at = sh.at, at_hi = sh.at_hi, summed_to = 0;  // bins whose weight is summed
-    u64 lane_w = 0, w = 0;
-    // adds the exact weight of the bins in [summed_to, at)
-    auto sum_up = [&](auto other) {
-        const float from = (float)summed_to, to = (float)at;
-        WeightSum sum;
-        int entries = 0;
-        row.each_pair(g, plain, [&](int index, float2 x, float2 d) {
-            const float bx = depth_bins(d.x), by = depth_bins(d.y);
-            const bool ix = x.x >= least && bx >= from && bx < to;
-            const bool iy = x.y >= least && by >= from && by < to;
-            const float wx = ex2(d.x), wy = ex2(d.y);
-            sum.add(pair(ix ? wx : 0.f, iy ? wy : 0.f));
-            entries += 2;
-            other(index, x.x, d.x, bx);
-            other(index + 1, x.y, d.y, by);
-        });
-        const u64 more = sum.total(entries);
-        lane_w += more;
-        w += row_weight(sh, row, more);
-        summed_to = at;
-    };
+    int at = sh.at, at_hi = sh.at_hi;
+    u64 lane_w = 0, w = 0;  // the weight before bin `at`: this lane's part, the row's
     if (!BY_COUNT && at < kDepthBins && sh.upto_n - sh.before_n > kListMax) {
         const u32 before = sh.before_n;
-        sum_up([](int, float, float, float) {});
+        const float edge = depth_edge(at);
+        WeightSum sum;
+        int entries = 0;
+        row.each_pair(g, plain, [&](int, float2 x, float2 d) {
+            const float wx = ex2(d.x), wy = ex2(d.y);
+            sum.add(pair(d.x > edge && (!INSIDE || x.x >= least) ? wx : 0.f,
+                         d.y > edge && (!INSIDE || x.y >= least) ? wy : 0.f));
+            entries += 2;
+        });
+        w = row_weight(sh, row, sum.total(entries));
         find_bracket<false>(sh, counts, at, at_hi, before, w, k, limit);
         at = min(sh.at, kDepthBins - 1);
         at_hi = sh.at_hi;
@@ -618,18 +632,35 @@ __device__ __noinline__ Found find_cut(Row<T> row, const Weigh g, bool plain,
     u32 n = sh.before_n;
     const u32 inside = sh.upto_n - n;
     const bool listed = at < kDepthBins && inside <= kListMax;
-    // the bracket's entries, or the span of their keys
-    const float lo_bin = (float)at, hi_bin = at_hi == kDepthBins - 1 ? INFINITY : at_hi + 1.f;
+    // and the bracket's entries, or the span of their keys
+    const float edge = depth_edge(at), end = depth_edge(at_hi + 1), low = fmaxf(end, deepest);
     float hi_x = neg_inf(), lo_x = INFINITY;
-    sum_up([&](int index, float x, float d, float bin) {
-        if (!(bin >= lo_bin && bin < hi_bin && d >= deepest && x >= least)) return;
-        if (listed) {
-            sh.own_list[atomicAdd(&sh.own_n, 1u)] = entry_of<T>(x, index);
-        } else {
-            hi_x = fmaxf(hi_x, x);
-            lo_x = fminf(lo_x, x);
-        }
-    });
+    {
+        WeightSum sum;
+        int entries = 0;
+        auto look = [&](int index, float x, float d) {
+            if (d > edge || !(d > end) || (INSIDE && !(x >= least))) return;
+            if (listed) {
+                sh.own_list[atomicAdd(&sh.own_n, 1u)] = entry_of<T>(x, index);
+            } else {
+                hi_x = fmaxf(hi_x, x);
+                lo_x = fminf(lo_x, x);
+            }
+        };
+        row.each_pair(g, plain, [&](int index, float2 x, float2 d) {
+            const float wx = ex2(d.x), wy = ex2(d.y);
+            const bool above_x = d.x > edge, above_y = d.y > edge;
+            sum.add(pair(above_x && (!INSIDE || x.x >= least) ? wx : 0.f,
+                         above_y && (!INSIDE || x.y >= least) ? wy : 0.f));
+            entries += 2;
+            if ((!above_x && d.x >= low) || (!above_y && d.y >= low)) {  // rare
+                if (d.x >= low) look(index, x.x, d.x);
+                if (d.y >= low) look(index + 1, x.y, d.y);
+            }
+        });
+        lane_w = sum.total(entries);
+    }
+    w = row_weight(sh, row, lane_w);
     if (at == kDepthBins) return {in, w, false, 0, 0, row.sl.up};
     if (listed) {
         const u32 own = sh.own_n;
@@ -980,7 +1011,7 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
         }
         u64 kept = all;
         if (k > 0) {
-            const Found f = find_cut<true>(row, g, plain, cut, (u32)k, 0, 0, p < 1.f);
+            const Found f = find_cut<true, false>(row, g, plain, cut, (u32)k, 0, 0, p < 1.f);
             cut = f.cut;
             kept = f.kept_w;
             row.sl.up = f.up;
@@ -989,8 +1020,10 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
             st = f.warp_t;
         }
         if (p < 1.f) {
-            const Found f =
-                find_cut<false>(row, g, plain, cut, 0, limit_of(p, kept), kept, true);
+            limit = limit_of(p, kept);
+            const Found f = cut.key != 0
+                                ? find_cut<false, true>(row, g, plain, cut, 0, limit, kept, true)
+                                : find_cut<false, false>(row, g, plain, cut, 0, limit, kept, true);
             cut = f.cut;
             row.sl.up = f.up;
             summed = f.summed;
