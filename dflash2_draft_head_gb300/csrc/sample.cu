@@ -41,7 +41,7 @@ namespace {
 using u32 = uint32_t;
 using u64 = unsigned long long;
 
-using Geo = RowGeometry<512, 2, 5, 320>;
+using Geo = RowGeometry<512, 2, 4, 640>;
 constexpr int kRowThreads = Geo::kThreads, kRowWarps = Geo::kWarps;
 
 constexpr float kLog2e = 1.44269504088896341f;
@@ -889,6 +889,7 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
     const RowSlice<Geo>& sl = row.sl;
     if (cs > 1) cluster_arrive();  // met by cluster_wait below: every CTA has started
     row.sl.start(r);
+    const float uniform = a.uniform[rowi];
     float T0 = a.temperature != nullptr ? a.temperature[rowi] : a.temperature0;
     int k = a.top_k != nullptr ? a.top_k[rowi] : a.top_k0;
     const float p = a.top_p != nullptr ? a.top_p[rowi] : a.top_p0;
@@ -1130,7 +1131,7 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
     };
     Place q = scan(sh.part_w, sh.part_t, cs * kRowWarps, 0, 0);
     const u64 total = __shfl_sync(0xffffffffu, q.sum + q.own, 31);
-    const u64 target = target_of(a.uniform[rowi], total);
+    const u64 target = target_of(uniform, total);
     const int holder = pick(sh.part_w, sh.part_t, q, target);
     if (holder / kRowWarps != rank) return;
 

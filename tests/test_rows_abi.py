@@ -83,3 +83,17 @@ def test_distill_backward_validation(L, kw, code):
 def test_last_error_names_the_call(L):
     assert _back(L, K=0) == 1
     assert ctypes.string_at(L.dflash2_last_error()).startswith(b"distill_backward")
+
+
+def test_binding_refuses_host_tensors_before_any_call():
+    import torch
+
+    import dflash2_draft_head_gb300 as df2
+    x, u = torch.zeros(2, 8), torch.zeros(2)
+    ids, y = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3)
+    with pytest.raises(ValueError):
+        df2.sample(x, u)
+    with pytest.raises(ValueError):
+        df2.distill(x, ids, y)
+    with pytest.raises(ValueError):
+        df2.distill_backward(u, x, ids, y, u)
