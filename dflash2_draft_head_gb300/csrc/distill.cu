@@ -27,8 +27,10 @@
 namespace df2 {
 namespace {
 
-using Geo = RowGeometry<256, 4, 6, 160>;
-constexpr int kRowThreads = Geo::kThreads, kRowWarps = Geo::kWarps;
+// Rows of up to kNarrowBytes take CTAs of four warps, of which an SM holds eight.
+using Wide = RowGeometry<256, 4, 6, 160>;
+using Narrow = RowGeometry<128, 8, 5, 160>;
+constexpr long long kNarrowBytes = 32 * 1024;
 
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.44269504088896341f;
@@ -200,11 +202,11 @@ __device__ __forceinline__ void store_vec(const RowView<T>& r, T* out, bool wide
 // (share(z) - sum of q over the slots of that token) * scale, by the first slot of
 // each token, whose warp adds up the others in a fixed order.  Call after a barrier
 // behind the plain writes.
-template <typename T, typename F>
+template <typename G, typename T, typename F>
 __device__ __forceinline__ void fix_tokens(const Teacher& t, int K, T* out, int e_lo, int e_hi,
                                            float scale, F share) {
     const int lane = threadIdx.x & 31;
-    for (int k0 = threadIdx.x - lane; k0 < K; k0 += kRowThreads) {
+    for (int k0 = threadIdx.x - lane; k0 < K; k0 += G::kThreads) {
         const int mine = k0 + lane < K ? t.id[k0 + lane] : -1;
         unsigned left = __ballot_sync(0xffffffffu, mine >= e_lo && mine < e_hi);
         while (left != 0) {
@@ -238,18 +240,18 @@ __device__ __forceinline__ MaxSum join(const MaxSum* ms, int n, float c) {
 }
 
 // One cluster per row: lse and loss, and the gradient when GRAD.
-template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kRowThreads, Geo::kCtas) distill_kernel(DistillArgs a) {
+template <typename T, bool GRAD, typename G>
+__global__ void __launch_bounds__(G::kThreads, G::kCtas) distill_kernel(DistillArgs a) {
     constexpr int E = VecOf<T>::kElems;
     extern __shared__ __align__(16) char smem[];
-    __shared__ MaxSum parts[kRowMaxCluster * kRowWarps];  // every warp of the row
+    __shared__ MaxSum parts[kRowMaxCluster * G::kWarps];  // every warp of the row
     __shared__ float has_teacher;                         // 1 or 0
 
     const int cs = 1 << a.lg, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = cs > 1 ? (int)cluster_ctarank() : 0;
     const int row = blockIdx.x >> a.lg;
     const RowView<T> r(a.logits, a.ld, row, a.V);
-    RowSlice<Geo> sl(r, a.per, a.ring, rank, warp, smem + (size_t)a.K * 16,
+    RowSlice<G> sl(r, a.per, a.ring, rank, warp, smem + (size_t)a.K * 16,
                 GRAD ? l2_policy_evict_last() : l2_policy_evict_first());
     const int e_lo = max(sl.lo * E - r.head, 0), e_hi = min(sl.hi * E - r.head, a.V);
     T* out = GRAD ? static_cast<T*>(a.grad) + (long long)row * a.grad_ld : nullptr;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) distill_kernel(Distil
     sl.start(r);
     const Teacher t(smem, a.K);
     // rank 0, which makes the loss, needs z at all of the teacher's tokens
-    if (warp == kRowWarps - 1)
+    if (warp == G::kWarps - 1)
         teacher_load(t, a, row, r.row, rank == 0 ? 0 : e_lo, rank == 0 ? a.V : e_hi, rank == 0);
     // The warp's sum of powers against the largest logit of its first vectors: fp32 has
     // room for sums 2^66 times above that.  Where one was larger (or the base was -inf,
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) distill_kernel(Distil
             s = warp_sum(s);
         }
     }
-    const int me = rank * kRowWarps + warp;
+    const int me = rank * G::kWarps + warp;
     if (cs > 1) {
         cluster_wait();
         if (lane < cs)
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) distill_kernel(Distil
     } else if (lane == 0) {
         parts[me] = {m, s};
     }
-    if (warp == kRowWarps - 1) {
+    if (warp == G::kWarps - 1) {
         const float q = teacher_softmax(t, a.K, a.inv_t);
         if (lane == 0) has_teacher = q;
     }
@@ -325,10 +327,10 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) distill_kernel(Distil
         cluster_wait();  // no CTA's shared memory is touched from outside after this
     }
     __syncthreads();
-    const MaxSum all = join(parts, cs * kRowWarps, a.c);
+    const MaxSum all = join(parts, cs * G::kWarps, a.c);
     const Power pg(all.max, a.c);
     const float S = all.sum;
-    if (rank == 0 && warp == kRowWarps - 1) {
+    if (rank == 0 && warp == G::kWarps - 1) {
         const float ls = log2f(S);
         double loss = 0;
         for (int k = lane; k < a.K; k += 32)
@@ -368,22 +370,22 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) distill_kernel(Distil
         }
         if (has_teacher == 0.f) return;
         __syncthreads();
-        fix_tokens<T>(t, a.K, out, e_lo, e_hi, scale,
+        fix_tokens<G, T>(t, a.K, out, e_lo, e_hi, scale,
                       [&](float z) { return pg(z) * per_s; });
     }
 }
 
 // The gradient alone, from lse and the upstream gradient: the CTAs of a row do not
 // wait on one another.
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads, Geo::kCtas) distill_grad_kernel(DistillArgs a) {
+template <typename T, typename G>
+__global__ void __launch_bounds__(G::kThreads, G::kCtas) distill_grad_kernel(DistillArgs a) {
     constexpr int E = VecOf<T>::kElems;
     extern __shared__ __align__(16) char smem[];
     __shared__ float has_teacher;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x >> a.lg, rank = blockIdx.x & ((1 << a.lg) - 1);
     const RowView<T> r(a.logits, a.ld, row, a.V);
-    RowSlice<Geo> sl(r, a.per, a.ring, rank, warp, smem + (size_t)a.K * 16,
+    RowSlice<G> sl(r, a.per, a.ring, rank, warp, smem + (size_t)a.K * 16,
                 l2_policy_evict_first());
     const int e_lo = max(sl.lo * E - r.head, 0), e_hi = min(sl.hi * E - r.head, a.V);
     T* out = static_cast<T*>(a.grad) + (long long)row * a.grad_ld;
@@ -424,28 +426,33 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) distill_grad_kernel(D
     });
     if (none) return;
     __syncthreads();
-    fix_tokens<T>(t, a.K, out, e_lo, e_hi, scale, share);
+    fix_tokens<G, T>(t, a.K, out, e_lo, e_hi, scale, share);
 }
 
-template <typename T>
-cudaError_t launch_typed(const DistillArgs& a, const RowSplit& p, cudaStream_t stream) {
+template <typename T, typename G>
+cudaError_t launch_typed(DistillArgs a, cudaStream_t stream, int num_sms) {
+    const RowSplit p = split_rows<G>(a.rows, a.V, sizeof(T), num_sms);
+    a.lg = p.lg;
+    a.per = p.per;
+    a.ring = p.ring;
     const size_t smem = p.smem + (size_t)a.K * 16;
-    constexpr size_t kMost = Geo::kRingBytes + (size_t)kDistillMaxK * 16;
+    constexpr size_t kMost = G::kRingBytes + (size_t)kDistillMaxK * 16;
     if (a.grad_loss != nullptr)
-        return launch_rows<Geo, distill_grad_kernel<T>>(a, a.rows, p.lg, smem, kMost, stream);
+        return launch_rows<G, distill_grad_kernel<T, G>>(a, a.rows, p.lg, smem, kMost, stream);
     if (a.grad != nullptr)
-        return launch_rows<Geo, distill_kernel<T, true>>(a, a.rows, p.lg, smem, kMost, stream);
-    return launch_rows<Geo, distill_kernel<T, false>>(a, a.rows, p.lg, smem, kMost, stream);
+        return launch_rows<G, distill_kernel<T, true, G>>(a, a.rows, p.lg, smem, kMost, stream);
+    return launch_rows<G, distill_kernel<T, false, G>>(a, a.rows, p.lg, smem, kMost, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_distill(DistillArgs a, int bf16, cudaStream_t stream, int num_sms) {
-    const RowSplit p = split_rows<Geo>(a.rows, a.V, bf16 ? 2 : 4, num_sms);
-    a.lg = p.lg;
-    a.per = p.per;
-    a.ring = p.ring;
-    return bf16 ? launch_typed<__nv_bfloat16>(a, p, stream) : launch_typed<float>(a, p, stream);
+    const bool narrow = (long long)a.V * (bf16 ? 2 : 4) <= kNarrowBytes;
+    if (bf16)
+        return narrow ? launch_typed<__nv_bfloat16, Narrow>(a, stream, num_sms)
+                      : launch_typed<__nv_bfloat16, Wide>(a, stream, num_sms);
+    return narrow ? launch_typed<float, Narrow>(a, stream, num_sms)
+                  : launch_typed<float, Wide>(a, stream, num_sms);
 }
 
 }  // namespace df2

@@ -41,8 +41,12 @@ namespace {
 using u32 = uint32_t;
 using u64 = unsigned long long;
 
-using Geo = RowGeometry<512, 2, 4, 640>;
-constexpr int kRowThreads = Geo::kThreads, kRowWarps = Geo::kWarps;
+// Rows of up to kNarrowBytes take CTAs of four warps, of which an SM holds seven: such a
+// row's time is the latency of the barriers, not of its bytes (4096 x 1000 bf16: 115 us
+// with sixteen warps).
+using Wide = RowGeometry<512, 2, 4, 640>;
+using Narrow = RowGeometry<128, 7, 4, 640>;
+constexpr long long kNarrowBytes = 32 * 1024;
 
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kOne = 1099511627776.f;  // 2^40, the largest entry's weight
@@ -51,7 +55,7 @@ constexpr int kDepthBins = 2048;         // of counts, over the depth
 constexpr int kBins = 512;               // of counts, or of weights in four words, over keys
 constexpr int kLimb = 11;                // bits of a weight in each word: 2^21 of them fit 32 bits
 constexpr int kBinsLog = 9;
-static_assert(kBins == 1 << kBinsLog && kBins == kRowThreads && kDepthBins == 4 * kRowThreads);
+static_assert(kBins == 1 << kBinsLog && kDepthBins == 4 * kBins);
 
 // An order-preserving whole number of a value (-0 like +0), and back.
 template <typename T>
@@ -165,9 +169,12 @@ __device__ __forceinline__ u64 target_of(float u, u64 total) {
     return __shfl_sync(0xffffffffu, t, 0);
 }
 
-constexpr int kGroups = 256;          // groups of a row whose maxima are exchanged
+// groups of a row whose maxima are exchanged
+template <typename G>
+constexpr int kGroups = G::kThreads < 256 ? G::kThreads : 256;
+constexpr int kMaxGroups = 256, kMaxWarps = 16;
 constexpr int kListMax = 1024;        // entries of a row's list
-constexpr int kParts = kRowMaxCluster * kRowWarps;
+constexpr int kParts = kRowMaxCluster * kMaxWarps;
 constexpr int kMaxUnits = 128;        // of a warp: see the assertion beside the launch
 
 struct Shared {
@@ -181,8 +188,8 @@ struct Shared {
         uint4 total[kBins];  // the cluster's bins
         u64 list[kListMax];  // the row's listed entries (rank 0): key, then ~index
     };
-    float group_max[kGroups];
-    float own_max[kGroups];
+    float group_max[kMaxGroups];
+    float own_max[kMaxGroups];
     u64 told_n[kRowMaxCluster];  // every CTA's listed entries
     u64 told_w[kRowMaxCluster];  // and their weight
     u64 cta_w[kRowMaxCluster];   // sums over the row
@@ -195,8 +202,8 @@ struct Shared {
     u32 own_n, list_n, base;
     float bound;
     u32 span_hi, span_lo;
-    u32 scan_n[kRowWarps];
-    u64 scan_w[kRowWarps];
+    u32 scan_n[kMaxWarps];
+    u64 scan_w[kMaxWarps];
     // the bins that may hold the cut: what stands before them and with them; for one bin
     // the weights
     int at, at_hi;
@@ -210,11 +217,12 @@ __device__ __forceinline__ Shared& shared_block() {
     return sh;
 }
 
-template <typename T>
+template <typename T, typename G>
 struct Row {
+    using Geo = G;
     static constexpr int E = VecOf<T>::kElems;
     RowView<T> r;
-    RowSlice<Geo> sl;
+    RowSlice<G> sl;
     int lg, cs, rank;
 
     template <typename F>
@@ -256,6 +264,7 @@ struct Row {
 };
 
 // Block-wide sums of a count and a weight; every thread gets both.
+template <typename G>
 __device__ __forceinline__ void block_sum(Shared& sh, u32& n, u64& w) {
     n = __reduce_add_sync(0xffffffffu, n);
     w = warp_sum(w);
@@ -267,7 +276,7 @@ __device__ __forceinline__ void block_sum(Shared& sh, u32& n, u64& w) {
     __syncthreads();
     n = 0;
     w = 0;
-    for (int i = 0; i < kRowWarps; ++i) {
+    for (int i = 0; i < G::kWarps; ++i) {
         n += sh.scan_n[i];
         w += sh.scan_w[i];
     }
@@ -277,7 +286,7 @@ __device__ __forceinline__ void block_sum(Shared& sh, u32& n, u64& w) {
 template <typename R>
 __device__ __forceinline__ u64 row_weight(Shared& sh, const R& row, u64 w) {
     u32 none = 0;
-    block_sum(sh, none, w);
+    block_sum<typename R::Geo>(sh, none, w);
     if (row.cs == 1) return w;
     if ((int)threadIdx.x < row.cs)
         st_cluster_b64(map_cluster(smem_u32(&sh.cta_w[row.rank]), threadIdx.x), w);
@@ -288,6 +297,7 @@ __device__ __forceinline__ u64 row_weight(Shared& sh, const R& row, u64 w) {
 }
 
 // Running sums over the block's threads: what stands before this one.  Returns all.
+template <typename G>
 __device__ __forceinline__ u64 block_before(Shared& sh, u32& n, u64& w) {
     const u32 bn = warp_before(n);
     const u64 bw = warp_before(w);
@@ -301,7 +311,7 @@ __device__ __forceinline__ u64 block_before(Shared& sh, u32& n, u64& w) {
     w = bw;
     u64 all = 0;
 #pragma unroll
-    for (int i = 0; i < kRowWarps; ++i) {
+    for (int i = 0; i < G::kWarps; ++i) {
         if (i < (int)threadIdx.x >> 5) {
             n += sh.scan_n[i];
             w += sh.scan_w[i];
@@ -311,33 +321,51 @@ __device__ __forceinline__ u64 block_before(Shared& sh, u32& n, u64& w) {
     return all;
 }
 
+// A thread's bins: kBinsOf<G> neighbours of the table.
+template <typename G>
+constexpr int kBinsOf = kBins / G::kThreads;
+template <typename G>
+struct Bins {
+    uint4 b[kBinsOf<G>];
+};
+
 // Adds up the cluster's bins (each CTA a share of them, which it then tells the others)
 // and returns this thread's.  What stood in sh.bins may be overwritten afterwards.
 template <typename R>
-__device__ __forceinline__ uint4 merge_bins(Shared& sh, const R& row) {
+__device__ __forceinline__ Bins<typename R::Geo> merge_bins(Shared& sh, const R& row) {
+    using G = typename R::Geo;
     const int tid = threadIdx.x;
+    Bins<G> own;
     if (row.cs == 1) {
         __syncthreads();
-        const uint4 b = sh.bins[tid];
+#pragma unroll
+        for (int i = 0; i < kBinsOf<G>; ++i) own.b[i] = sh.bins[tid * kBinsOf<G> + i];
         __syncthreads();
-        return b;
+        return own;
     }
-    const int lg = kBinsLog - row.lg, share = 1 << lg, other = tid >> lg;
-    const int mine = row.rank * share + (tid & (share - 1));
-    if (tid < share) sh.total[mine] = make_uint4(0, 0, 0, 0);
+    const int log = kBinsLog - row.lg, share = 1 << log, first = row.rank * share;
+    for (int i = tid; i < share; i += G::kThreads) sh.total[first + i] = make_uint4(0, 0, 0, 0);
     row.sync();  // every CTA's bins are filled
-    const uint4 b = ld_cluster_v4(map_cluster(smem_u32(&sh.bins[mine]), other));
-    u32* sum = reinterpret_cast<u32*>(&sh.total[mine]);
-    if (b.x != 0) atomicAdd(sum, b.x);
-    if (b.y != 0) atomicAdd(sum + 1, b.y);
-    if (b.z != 0) atomicAdd(sum + 2, b.z);
-    if (b.w != 0) atomicAdd(sum + 3, b.w);
+    for (int i = tid; i < kBins; i += G::kThreads) {
+        const int mine = first + (i & (share - 1));
+        const uint4 b = ld_cluster_v4(map_cluster(smem_u32(&sh.bins[mine]), i >> log));
+        u32* sum = reinterpret_cast<u32*>(&sh.total[mine]);
+        if (b.x != 0) atomicAdd(sum, b.x);
+        if (b.y != 0) atomicAdd(sum + 1, b.y);
+        if (b.z != 0) atomicAdd(sum + 2, b.z);
+        if (b.w != 0) atomicAdd(sum + 3, b.w);
+    }
     __syncthreads();
-    if (other != row.rank)
-        st_cluster_v4(map_cluster(smem_u32(&sh.total[mine]), other),
-                      *reinterpret_cast<const float4*>(&sh.total[mine]));
+    for (int i = tid; i < kBins; i += G::kThreads) {
+        const int mine = first + (i & (share - 1)), to = i >> log;
+        if (to != row.rank)
+            st_cluster_v4(map_cluster(smem_u32(&sh.total[mine]), to),
+                          *reinterpret_cast<const float4*>(&sh.total[mine]));
+    }
     row.sync();
-    return sh.total[tid];
+#pragma unroll
+    for (int i = 0; i < kBinsOf<G>; ++i) own.b[i] = sh.total[tid * kBinsOf<G> + i];
+    return own;
 }
 
 // The bin of a depth: d in bins, rounded by the addition of 2^23, which leaves it in the
@@ -381,8 +409,8 @@ __device__ __forceinline__ u64 bin_least(int bin) {
 }
 
 // This lane's part of its warp's weight: all entries.
-template <typename T>
-__device__ __forceinline__ u64 all_weight(Row<T>& row, const Weigh& g, bool plain) {
+template <typename T, typename G>
+__device__ __forceinline__ u64 all_weight(Row<T, G>& row, const Weigh& g, bool plain) {
     WeightSum ws;
     int entries = 0;
     row.each_pair(g, plain, [&](int, float2, float2 d) {
@@ -393,8 +421,8 @@ __device__ __forceinline__ u64 all_weight(Row<T>& row, const Weigh& g, bool plai
 }
 
 // This lane's part of its warp's kept weight, and its ties at the cut.
-template <typename T>
-__device__ __forceinline__ void kept_weight(Row<T>& row, const Weigh& g, bool plain,
+template <typename T, typename G>
+__device__ __forceinline__ void kept_weight(Row<T, G>& row, const Weigh& g, bool plain,
                                             const Cut& cut, float min_p, u64& weight, u32& ties) {
     const float floor = cut.key != 0 ? Key<T>::value(cut.key) : neg_inf();
     const float least = min_p > 0.f ? min_p : 0.f;
@@ -418,14 +446,18 @@ __device__ __forceinline__ u64 entry_of(float x, int index) {
     return (u64)Key<T>::of(x) << 32 | (u32)~index;
 }
 
-// Sorts the row's list of n entries, first ones first.  One CTA.  Up to kCountSort of
-// them: every entry counts those before it, n^2 steps on all threads.  More: a bitonic
-// network over the next power of two, two entries a thread, through shuffles inside a
-// warp and shared memory beyond (436 entries: 1 us, against 4 us by counting).
+// Sorts the row's list of n entries, first ones first.  One CTA.  As many as it has
+// threads, up to kCountSort: every entry counts those before it, n^2 steps on all
+// threads.  More: a bitonic network over the next power of two, kPer neighbours a
+// thread, through shuffles inside a warp and shared memory beyond (436 entries on 512
+// threads: 1 us, against 4 us by counting).
 constexpr int kCountSort = 128;
+template <typename G>
 __device__ __forceinline__ void sort_list(Shared& sh, int n) {
+    constexpr int kPer = kListMax / G::kThreads;
     const int tid = threadIdx.x;
     if (n <= kCountSort) {
+        static_assert(kCountSort <= G::kThreads);
         u64 e = 0;
         int before = 0;
         if (tid < n) {
@@ -438,45 +470,53 @@ __device__ __forceinline__ void sort_list(Shared& sh, int n) {
         __syncthreads();
         return;
     }
-    static_assert(kListMax == 2 * kRowThreads);
-    const int size = 1 << (32 - __clz(n - 1));
-    const bool live = 2 * tid < size;
-    u64 e[2];
+    const int size = 1 << (32 - __clz(n - 1)), base = tid * kPer;
+    const bool live = base < size;
+    u64 e[kPer];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) e[i] = 2 * tid + i < n ? sh.list[2 * tid + i] : 0;
-    auto order = [](u64& a, u64& b, bool falling) {
-        if ((a < b) == falling) {
-            const u64 t = a;
-            a = b;
-            b = t;
-        }
+    for (int i = 0; i < kPer; ++i) e[i] = base + i < n ? sh.list[base + i] : 0;
+    auto save = [&] {
+        if (!live) return;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sh.list[base + i] = e[i];
     };
     for (int k = 2; k <= size; k <<= 1) {
-        const bool falling = (2 * tid & k) == 0;
-        for (int j = k >> 1; j > 1; j >>= 1) {
-            const bool first = (2 * tid & j) == 0;  // the lower place of the two
-            u64 o[2];
-            if (j < 64) {
+        for (int j = k >> 1; j >= kPer; j >>= 1) {
+            const bool larger = ((base & k) == 0) == ((base & j) == 0);  // which of two stays here
+            u64 o[kPer];
+            if (j < 32 * kPer) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) o[i] = __shfl_xor_sync(0xffffffffu, e[i], j >> 1);
+                for (int i = 0; i < kPer; ++i) o[i] = __shfl_xor_sync(0xffffffffu, e[i], j / kPer);
             } else {
                 __syncthreads();
-                if (live) *reinterpret_cast<ulonglong2*>(&sh.list[2 * tid]) = make_ulonglong2(e[0], e[1]);
+                save();
                 __syncthreads();
                 if (live) {
-                    const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(&sh.list[2 * tid ^ j]);
-                    o[0] = p.x;
-                    o[1] = p.y;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) o[i] = sh.list[(base ^ j) + i];
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (live && (e[i] < o[i]) == (falling == first)) e[i] = o[i];
+            for (int i = 0; i < kPer; ++i)
+                if (live && (e[i] < o[i]) == larger) e[i] = o[i];
         }
-        order(e[0], e[1], falling);
+#pragma unroll
+        for (int j = kPer / 2; j > 0; j >>= 1) {
+            if (j >= k) continue;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                if ((i & j) != 0) continue;
+                const bool falling = ((base + i) & k) == 0;
+                if ((e[i] < e[i + j]) == falling) {
+                    const u64 t = e[i];
+                    e[i] = e[i + j];
+                    e[i + j] = t;
+                }
+            }
+        }
     }
     __syncthreads();
-    if (live) *reinterpret_cast<ulonglong2*>(&sh.list[2 * tid]) = make_ulonglong2(e[0], e[1]);
+    save();
     __syncthreads();
 }
 
@@ -486,13 +526,13 @@ template <typename R>
 __device__ __forceinline__ void send_list(Shared& sh, const R& row, u32 n) {
     const int tid = threadIdx.x;
     if (row.cs == 1) {
-        for (u32 i = tid; i < min(n, (u32)kListMax); i += kRowThreads) sh.list[i] = sh.own_list[i];
+        for (u32 i = tid; i < min(n, (u32)kListMax); i += R::Geo::kThreads) sh.list[i] = sh.own_list[i];
         return;
     }
     if (tid == 0)
         sh.base = n <= kListMax ? atom_add_cluster(map_cluster(smem_u32(&sh.list_n), 0), n) : kListMax;
     __syncthreads();
-    for (u32 i = tid; i < n && sh.base + i < kListMax; i += kRowThreads)
+    for (u32 i = tid; i < n && sh.base + i < kListMax; i += R::Geo::kThreads)
         st_cluster_b64(map_cluster(smem_u32(&sh.list[sh.base + i]), 0), sh.own_list[i]);
 }
 
@@ -500,24 +540,28 @@ __device__ __forceinline__ void send_list(Shared& sh, const R& row, u32 n) {
 // sh.at_hi (one bin by count), with the counts before and up to them; sh.at is
 // kDepthBins when there is no cut.  b: this thread's merged counts; the cut is known to
 // lie in the bins from `from` to `to`, behind base_n entries of weight base_w.
-template <bool BY_COUNT>
-__device__ __forceinline__ void find_bracket(Shared& sh, const uint4& b, int from, int to,
+template <bool BY_COUNT, typename G>
+__device__ __forceinline__ void find_bracket(Shared& sh, const Bins<G>& bins, int from, int to,
                                              u32 base_n, u64 base_w, u32 k, u64 limit) {
-    u32 n[4] = {b.x, b.y, b.z, b.w};
-    const int first = (int)threadIdx.x * 4;
+    constexpr int kPer = 4 * kBinsOf<G>;
+    const int first = (int)threadIdx.x * kPer;
+    auto count = [&](int i) {
+        const uint4& b = bins.b[i / 4];
+        const u32 n = i % 4 == 0 ? b.x : i % 4 == 1 ? b.y : i % 4 == 2 ? b.z : b.w;
+        return first + i < from || first + i > to ? 0 : n;
+    };
     u32 bn = 0, none = 0;
     u64 least = 0, most = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (first + i < from || first + i > to) n[i] = 0;
-        bn += n[i];
+    for (int i = 0; i < kPer; ++i) {
+        bn += count(i);
         if (!BY_COUNT) {
-            least += n[i] * bin_least(first + i);
-            most += n[i] * bin_most(first + i);
+            least += count(i) * bin_least(first + i);
+            most += count(i) * bin_most(first + i);
         }
     }
-    block_before(sh, bn, least);
-    if (!BY_COUNT) block_before(sh, none, most);
+    block_before<G>(sh, bn, least);
+    if (!BY_COUNT) block_before<G>(sh, none, most);
     if (threadIdx.x == 0) {
         sh.at = kDepthBins;
         sh.at_hi = to;
@@ -529,10 +573,11 @@ __device__ __forceinline__ void find_bracket(Shared& sh, const uint4& b, int fro
     least += base_w;
     most += base_w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const u64 l = BY_COUNT ? 0 : n[i] * bin_least(first + i);
-        const u64 h = BY_COUNT ? 0 : n[i] * bin_most(first + i);
-        const bool may = BY_COUNT ? bn < k && bn + n[i] >= k : most < limit && most + h >= limit;
+    for (int i = 0; i < kPer; ++i) {
+        const u32 n = count(i);
+        const u64 l = BY_COUNT ? 0 : n * bin_least(first + i);
+        const u64 h = BY_COUNT ? 0 : n * bin_most(first + i);
+        const bool may = BY_COUNT ? bn < k && bn + n >= k : most < limit && most + h >= limit;
         const bool must = BY_COUNT ? may : least < limit && least + l >= limit;
         if (may) {
             sh.at = first + i;
@@ -540,9 +585,9 @@ __device__ __forceinline__ void find_bracket(Shared& sh, const uint4& b, int fro
         }
         if (must) {
             sh.at_hi = first + i;
-            sh.upto_n = bn + n[i];
+            sh.upto_n = bn + n;
         }
-        bn += n[i];
+        bn += n;
         least += l;
         most += h;
     }
@@ -554,20 +599,31 @@ __device__ __forceinline__ void find_bracket(Shared& sh, const uint4& b, int fro
 template <bool BY_COUNT, typename R>
 __device__ __forceinline__ void find_bin(Shared& sh, const R& row, u32 base_n, u64 base_w, u32 k,
                                          u64 limit) {
-    const uint4 b = merge_bins(sh, row);
-    const u32 n = BY_COUNT ? b.x : 0;
-    const u64 w = BY_COUNT ? 0 : bin_weight(b);
+    using G = typename R::Geo;
+    const Bins<G> bins = merge_bins(sh, row);
     if (threadIdx.x == 0) sh.at = kBins;
-    u32 bn = n;
-    u64 bw = w;
-    block_before(sh, bn, bw);
+    u32 bn = 0;
+    u64 bw = 0;
+#pragma unroll
+    for (int i = 0; i < kBinsOf<G>; ++i) {
+        bn += BY_COUNT ? bins.b[i].x : 0;
+        bw += BY_COUNT ? 0 : bin_weight(bins.b[i]);
+    }
+    block_before<G>(sh, bn, bw);
     bn += base_n;
     bw += base_w;
-    if (BY_COUNT ? bn < k && bn + n >= k : bw < limit && bw + w >= limit) {
-        sh.at = (int)threadIdx.x;
-        sh.before_n = bn;
-        sh.before_w = bw;
-        sh.in_w = w;
+#pragma unroll
+    for (int i = 0; i < kBinsOf<G>; ++i) {
+        const u32 n = BY_COUNT ? bins.b[i].x : 0;
+        const u64 w = BY_COUNT ? 0 : bin_weight(bins.b[i]);
+        if (BY_COUNT ? bn < k && bn + n >= k : bw < limit && bw + w >= limit) {
+            sh.at = (int)threadIdx.x * kBinsOf<G> + i;
+            sh.before_n = bn;
+            sh.before_w = bw;
+            sh.in_w = w;
+        }
+        bn += n;
+        bw += w;
     }
     __syncthreads();
 }
@@ -583,14 +639,14 @@ struct Found {
     u32 warp_t;
     bool up;      // the direction of the row's next pass
 };
-template <bool BY_COUNT, bool INSIDE, typename T>
-__device__ __noinline__ Found find_cut(Row<T> row, const Weigh g, bool plain,
+template <bool BY_COUNT, bool INSIDE, typename T, typename G>
+__device__ __noinline__ Found find_cut(Row<T, G> row, const Weigh g, bool plain,
                                        const Cut in, u32 k, u64 limit, u64 all, bool weigh) {
     constexpr int E = VecOf<T>::kElems;
     Shared& sh = shared_block();
     const int tid = threadIdx.x, lane = tid & 31;
     auto clear = [&] {
-        sh.bins[tid] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < kBins; i += G::kThreads) sh.bins[i] = make_uint4(0, 0, 0, 0);
         if (tid == 0) {
             sh.own_n = sh.list_n = 0;
             sh.span_hi = 0;
@@ -609,8 +665,8 @@ __device__ __noinline__ Found find_cut(Row<T> row, const Weigh g, bool plain,
         if (d.x >= deepest && (!INSIDE || x.x >= least)) atomicAdd(&sh.count[bin.x], 1u);
         if (d.y >= deepest && (!INSIDE || x.y >= least)) atomicAdd(&sh.count[bin.y], 1u);
     });
-    const uint4 counts = merge_bins(sh, row);
-    find_bracket<BY_COUNT>(sh, counts, 0, kDepthBins - 1, 0, 0, k, limit);
+    const Bins<G> counts = merge_bins(sh, row);
+    find_bracket<BY_COUNT, G>(sh, counts, 0, kDepthBins - 1, 0, 0, k, limit);
     int at = sh.at, at_hi = sh.at_hi;
     u64 lane_w = 0, w = 0;  // the weight before bin `at`: this lane's part, the row's
     if (!BY_COUNT && at < kDepthBins && sh.upto_n - sh.before_n > kListMax) {
@@ -625,7 +681,7 @@ __device__ __noinline__ Found find_cut(Row<T> row, const Weigh g, bool plain,
             entries += 2;
         });
         w = row_weight(sh, row, sum.total(entries));
-        find_bracket<false>(sh, counts, at, at_hi, before, w, k, limit);
+        find_bracket<false, G>(sh, counts, at, at_hi, before, w, k, limit);
         at = min(sh.at, kDepthBins - 1);
         at_hi = sh.at_hi;
     }
@@ -668,8 +724,8 @@ __device__ __noinline__ Found find_cut(Row<T> row, const Weigh g, bool plain,
         row.sync();
         if (row.rank == 0) {
             // the last kept entry's place in the sorted list; its ties before it are kept
-            constexpr int kPer = kListMax / kRowThreads;
-            sort_list(sh, (int)inside);
+            constexpr int kPer = kListMax / G::kThreads;
+            sort_list<G>(sh, (int)inside);
             u64 W[kPer], before = 0;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
@@ -680,7 +736,7 @@ __device__ __noinline__ Found find_cut(Row<T> row, const Weigh g, bool plain,
                 before += W[i];
             }
             u32 none = 0;
-            block_before(sh, none, before);
+            block_before<G>(sh, none, before);
             before += w;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
@@ -799,13 +855,13 @@ __device__ __noinline__ Found find_cut(Row<T> row, const Weigh g, bool plain,
 
 // Finishes a row from its list of n entries, which holds the first k (k > 0) or those
 // that reach p of the row's weight `all` (k == 0).  One CTA.
-template <typename T>
+template <typename T, typename G>
 __device__ __noinline__ void finish_list(const SampleArgs& a, const Weigh g, int rowi,
                                          int n, int k, float p, float min_p, u64 all) {
-    constexpr int kPer = kListMax / kRowThreads;
+    constexpr int kPer = kListMax / G::kThreads;
     Shared& sh = shared_block();
     const int tid = threadIdx.x;
-    sort_list(sh, n);
+    sort_list<G>(sh, n);
     const int last = k > 0 ? min(k, n) : n;
     u64 W[kPer], before = 0;
     float w[kPer];
@@ -818,7 +874,7 @@ __device__ __noinline__ void finish_list(const SampleArgs& a, const Weigh g, int
         before += W[i];
     }
     u32 kept = 0;
-    u64 kept_w = block_before(sh, kept, before);
+    u64 kept_w = block_before<G>(sh, kept, before);
     const u64 limit = p < 1.f ? limit_of(p, k > 0 ? kept_w : all) : ~0ull;
     kept_w = 0;
 #pragma unroll
@@ -830,9 +886,9 @@ __device__ __noinline__ void finish_list(const SampleArgs& a, const Weigh g, int
         }
         before += W[i];
     }
-    block_sum(sh, kept, kept_w);
+    block_sum<G>(sh, kept, kept_w);
     const u64 target = target_of(a.uniform[rowi], kept_w);
-    for (int i = tid; i < (int)kept; i += kRowThreads) {
+    for (int i = tid; i < (int)kept; i += G::kThreads) {
         const u32 index = (u32)sh.list[i];  // ~index
         u64 cum = 0;
 #pragma unroll 4
@@ -847,8 +903,9 @@ __device__ __noinline__ void finish_list(const SampleArgs& a, const Weigh g, int
 
 // The n-th largest of the row's group maxima, rounded down to the upper 16 bits of its
 // key: at least n entries are not below it.  One warp.
+template <typename G>
 __device__ __forceinline__ float group_bound(const Shared& sh, int n) {
-    constexpr int kPer = kGroups / 32;
+    constexpr int kPer = kGroups<G> / 32;
     const int lane = threadIdx.x & 31;
     u32 key[kPer];
 #pragma unroll
@@ -874,8 +931,8 @@ __device__ __forceinline__ float group_bound(const Shared& sh, int n) {
     return Key<float>::value(lo << 16);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleArgs a) {
+template <typename T, typename G>
+__global__ void __launch_bounds__(G::kThreads, G::kCtas) sample_kernel(SampleArgs a) {
     constexpr int E = VecOf<T>::kElems;
     extern __shared__ __align__(16) char smem[];
     Shared& sh = shared_block();
@@ -884,9 +941,9 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
     const int cs = 1 << a.lg, rank = cs > 1 ? (int)cluster_ctarank() : 0;
     const int rowi = blockIdx.x >> a.lg;
     const RowView<T> r(a.logits, a.ld, rowi, a.V);
-    Row<T> row{r, RowSlice<Geo>(r, a.per, a.ring, rank, warp, smem, l2_policy_evict_last()), a.lg, cs,
+    Row<T, G> row{r, RowSlice<G>(r, a.per, a.ring, rank, warp, smem, l2_policy_evict_last()), a.lg, cs,
                rank};
-    const RowSlice<Geo>& sl = row.sl;
+    const RowSlice<G>& sl = row.sl;
     if (cs > 1) cluster_arrive();  // met by cluster_wait below: every CTA has started
     row.sl.start(r);
     const float uniform = a.uniform[rowi];
@@ -901,7 +958,7 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
     if (tid == 0) sh.own_n = sh.list_n = 0;
 
     // the largest entries of the groups (kLanes * cs lanes each) and of the row
-    constexpr int kLanes = kRowThreads / kGroups;
+    constexpr int kLanes = G::kThreads / kGroups<G>;
     static_assert(kLanes >= 1 && kLanes * kRowMaxCluster <= 32);
     RunningMax<T> most;
     row.each_vec([&](int, const uint4& v) { most.add(v); });
@@ -922,15 +979,16 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
     if (cs > 1) {
         cluster_wait();
         // kGroups / 4 of the threads send four maxima each to one of the CTAs
-        const int lq = 6 - a.lg, quads = 1 << lq, to = tid >> lq, i = tid & (quads - 1);
-        static_assert(kGroups / 4 == 1 << 6);
+        constexpr int kLog = kGroups<G> == 256 ? 6 : 5;
+        static_assert(kGroups<G> / 4 == 1 << kLog);
+        const int lq = kLog - a.lg, quads = 1 << lq, to = tid >> lq, i = tid & (quads - 1);
         if (to < cs)
             st_cluster_v4(map_cluster(smem_u32(&sh.group_max[4 * (rank * quads + i)]), to),
                           reinterpret_cast<const float4*>(sh.own_max)[i]);
         row.sync();
     }
     m = neg_inf();
-    for (int i = lane; i < kGroups; i += 32) m = fmaxf(m, sh.group_max[i]);
+    for (int i = lane; i < kGroups<G>; i += 32) m = fmaxf(m, sh.group_max[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (m == neg_inf()) {  // nothing to choose from
@@ -950,21 +1008,22 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
     if (k > 0 || p < 1.f) {
         u64 all = 0, limit = ~0ull;  // (without top_k) the row's weight and top_p's part of it
         // Is a list short enough?  Without top_k: of about as many entries as half the
-        // groups, unless the groups' maxima are far from what top_p asks for; of a row of up
-        // to kListMax entries, all.
-        const int want = k > 0 ? k : kGroups / 2;
-        bool list = a.V <= kListMax || want <= kGroups;
+        // groups, unless the groups' maxima are far from what top_p asks for.  Where it is
+        // not, all entries of a row of up to kListMax.
+        const int want = k > 0 ? k : kGroups<G> / 2;
+        const bool small = a.V <= kListMax;
+        bool list = want <= kGroups<G>;
         if (k == 0) {
             all = row_weight(sh, row, all_weight(row, g, plain));
             limit = limit_of(p, all);
-            u64 most = tid < kGroups ? Weigh::fixed(Weigh::w(g.depth(sh.group_max[tid]))) : 0;
+            u64 most = tid < kGroups<G> ? Weigh::fixed(Weigh::w(g.depth(sh.group_max[tid]))) : 0;
             u32 none = 0;
-            block_sum(sh, none, most);
-            list = a.V <= kListMax || most >= limit / 4;
+            block_sum<G>(sh, none, most);
+            list = most >= (small ? limit : limit / 4);
         }
-        if (list) {
+        if (list || small) {
             if (warp == 0) {
-                const float b = a.V <= kListMax ? neg_inf() : group_bound(sh, want);
+                const float b = list ? group_bound<G>(sh, want) : neg_inf();
                 if (lane == 0) sh.bound = b > -3.402823466e38f ? b : -3.402823466e38f;
             }
             __syncthreads();
@@ -983,7 +1042,7 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
                 }
             });
             u32 none = 0;
-            if (k == 0) block_sum(sh, none, listed_w);
+            if (k == 0) block_sum<G>(sh, none, listed_w);
             __syncthreads();
             const u32 own = sh.own_n;
             send_list(sh, row, own);
@@ -1005,7 +1064,7 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
             }
             if (n <= kListMax && (k > 0 || listed_w >= limit)) {
                 // the other CTAs' shared memory is not touched any more
-                if (rank == 0) finish_list<T>(a, g, rowi, (int)n, k, p, min_p, all);
+                if (rank == 0) finish_list<T, G>(a, g, rowi, (int)n, k, p, min_p, all);
                 return;
             }
             __syncthreads();
@@ -1073,7 +1132,7 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
         sw = warp_sum(sw);
         st = __reduce_add_sync(0xffffffffu, st);
     }
-    const int me = rank * kRowWarps + warp;
+    const int me = rank * G::kWarps + warp;
     if (cs > 1) {
         if (lane < cs) {
             st_cluster_b64(map_cluster(smem_u32(&sh.part_w[me]), lane), sw);
@@ -1129,25 +1188,25 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
         q.ties = __shfl_sync(0xffffffffu, q.ties, from);
         return __shfl_sync(0xffffffffu, i, from);
     };
-    Place q = scan(sh.part_w, sh.part_t, cs * kRowWarps, 0, 0);
+    Place q = scan(sh.part_w, sh.part_t, cs * G::kWarps, 0, 0);
     const u64 total = __shfl_sync(0xffffffffu, q.sum + q.own, 31);
     const u64 target = target_of(uniform, total);
     const int holder = pick(sh.part_w, sh.part_t, q, target);
-    if (holder / kRowWarps != rank) return;
+    if (holder / G::kWarps != rank) return;
 
-    const RowSlice<Geo> own(r, a.per, a.ring, rank, holder % kRowWarps, smem, 0);
+    const RowSlice<G> own(r, a.per, a.ring, rank, holder % G::kWarps, smem, 0);
     const int units = (own.whi - own.wlo + 31) >> 5;
     constexpr int kAhead = 3;  // units of a warp loaded together
-    for (int u0 = warp; u0 < units; u0 += kAhead * kRowWarps) {
+    for (int u0 = warp; u0 < units; u0 += kAhead * G::kWarps) {
         uint4 vec[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int v = own.wlo + (u0 + i * kRowWarps) * 32 + lane;
+            const int v = own.wlo + (u0 + i * G::kWarps) * 32 + lane;
             vec[i] = v < own.whi ? r.load(v) : r.nothing();
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int unit = u0 + i * kRowWarps;
+            const int unit = u0 + i * G::kWarps;
             if (unit >= units) break;
             u64 w = 0;
             u32 t = 0;
@@ -1199,17 +1258,29 @@ __global__ void __launch_bounds__(kRowThreads, Geo::kCtas) sample_kernel(SampleA
 
 }  // namespace
 
-cudaError_t launch_sample(SampleArgs a, int bf16, cudaStream_t stream, int num_sms) {
+namespace {
+
+template <typename T, typename G>
+cudaError_t launch_typed(SampleArgs a, cudaStream_t stream, int num_sms) {
     // the widest row: kSampleMaxV fp32 entries over the largest cluster
-    static_assert(kSampleMaxV / 4 / kRowMaxCluster / kRowWarps / 32 < kMaxUnits);
-    const RowSplit p = split_rows<Geo>(a.rows, a.V, bf16 ? 2 : 4, num_sms);
+    static_assert(kSampleMaxV / 4 / kRowMaxCluster / Wide::kWarps / 32 < kMaxUnits);
+    static_assert(kNarrowBytes / 16 / Narrow::kWarps / 32 < kMaxUnits);
+    const RowSplit p = split_rows<G>(a.rows, a.V, sizeof(T), num_sms);
     a.lg = p.lg;
     a.per = p.per;
     a.ring = p.ring;
+    return launch_rows<G, sample_kernel<T, G>>(a, a.rows, a.lg, p.smem, G::kRingBytes, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_sample(SampleArgs a, int bf16, cudaStream_t stream, int num_sms) {
+    const bool narrow = (long long)a.V * (bf16 ? 2 : 4) <= kNarrowBytes;
     if (bf16)
-        return launch_rows<Geo, sample_kernel<__nv_bfloat16>>(a, a.rows, a.lg, p.smem,
-                                                              Geo::kRingBytes, stream);
-    return launch_rows<Geo, sample_kernel<float>>(a, a.rows, a.lg, p.smem, Geo::kRingBytes, stream);
+        return narrow ? launch_typed<__nv_bfloat16, Narrow>(a, stream, num_sms)
+                      : launch_typed<__nv_bfloat16, Wide>(a, stream, num_sms);
+    return narrow ? launch_typed<float, Narrow>(a, stream, num_sms)
+                  : launch_typed<float, Wide>(a, stream, num_sms);
 }
 
 }  // namespace df2
