@@ -30,7 +30,7 @@ namespace {
 // Rows of up to kNarrowBytes take CTAs of four warps, of which an SM holds eight.
 using Wide = RowGeometry<256, 4, 6, 160>;
 using Narrow = RowGeometry<128, 8, 5, 160>;
-constexpr long long kNarrowBytes = 32 * 1024;
+constexpr long long kNarrowBytes = 64 * 1024;
 
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.44269504088896341f;

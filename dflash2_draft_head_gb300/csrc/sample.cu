@@ -46,7 +46,7 @@ using u64 = unsigned long long;
 // with sixteen warps).
 using Wide = RowGeometry<512, 2, 4, 640>;
 using Narrow = RowGeometry<128, 7, 4, 640>;
-constexpr long long kNarrowBytes = 32 * 1024;
+constexpr long long kNarrowBytes = 64 * 1024;
 
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kOne = 1099511627776.f;  // 2^40, the largest entry's weight
