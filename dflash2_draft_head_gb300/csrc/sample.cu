@@ -13,14 +13,19 @@
 // token does not depend on how a row is split.  A weight under 2^-41 of the
 // largest one counts as 0: over 2^21 entries that is less than 2^-20 of the sum.
 //
-// Bound by HBM: a row is read once, by one CTA or by the CTAs of a cluster, and passed
-// over two or more times on the chip.  The largest entries of 256 groups of the row come first: their maximum is the row's, and the n-th largest
-// of them is a bound above which at least n entries lie.
+// The floor is HBM: a row is read once, by one CTA or by the CTAs of a cluster, and passed
+// over two or more times on the chip.  What bounds the kernel is the instructions of
+// those passes: exact weights take 7 an entry.  4096 x 151936 bf16 rows at a temperature
+// take 332 to 360 us (3.5 to 3.75 TB/s), their bytes alone 183 us; 604 us for 512 x 262144
+// fp32 rows cut by top_p inside a flat distribution, which makes five passes.
+//
+// The largest entries of the row's groups (of 256 or 128) come first: the largest of them
+// is the row's, and the n-th largest is a bound above which at least n entries lie.
 //   - Neither top_k nor top_p: one pass of weights, summed by warp; one warp's part of
 //     the row holds the token and is looked through.
-//   - Up to 256 entries to keep, or a top_p that the entries above such a bound
-//     reach: those entries (some hundreds) are listed, and one CTA finishes the row
-//     from the list alone.
+//   - No more entries to keep than groups, or a top_p that the entries above such a
+//     bound reach: those entries (tens to hundreds) are listed, and one CTA finishes
+//     the row from the list alone.
 //   - Else counts over the distance from the maximum (a bin's weights differ by 1.4%)
 //     leave a bracket of bins that may hold the cut; the exact weight above it narrows
 //     it to one or two.  Up to 1024 entries there are listed and sorted; more of them
@@ -41,11 +46,13 @@ namespace {
 using u32 = uint32_t;
 using u64 = unsigned long long;
 
-// Rows of up to kNarrowBytes take CTAs of four warps, of which an SM holds seven: such a
-// row's time is the latency of the barriers, not of its bytes (4096 x 1000 bf16: 115 us
-// with sixteen warps).
-using Wide = RowGeometry<512, 2, 4, 640>;
-using Narrow = RowGeometry<128, 7, 4, 640>;
+// Three CTAs of eight warps an SM: with two of sixteen the compiler has 64 registers a
+// thread instead of 80, and 4096 x 151936 bf16 took 371 us instead of 332.  Rows of up to
+// kNarrowBytes take CTAs of four warps, of which an SM holds seven: such a row's time is
+// the latency of the barriers, not of its bytes (4096 x 1000 bf16, temperature alone: 38
+// us, 115 us with sixteen warps; 4096 x 32000, top-k: 124 us, 192).
+using Wide = RowGeometry<256, 3, 6, 320>;
+using Narrow = RowGeometry<128, 7, 4, 320>;
 constexpr long long kNarrowBytes = 64 * 1024;
 
 constexpr float kLog2e = 1.44269504088896341f;
@@ -172,10 +179,10 @@ __device__ __forceinline__ u64 target_of(float u, u64 total) {
 // groups of a row whose maxima are exchanged
 template <typename G>
 constexpr int kGroups = G::kThreads < 256 ? G::kThreads : 256;
-constexpr int kMaxGroups = 256, kMaxWarps = 16;
-constexpr int kListMax = 1024;        // entries of a row's list
+constexpr int kMaxGroups = 256, kMaxWarps = 8;
+constexpr int kListMax = 1024;  // entries of a row's list
 constexpr int kParts = kRowMaxCluster * kMaxWarps;
-constexpr int kMaxUnits = 128;        // of a warp: see the assertion beside the launch
+constexpr int kMaxUnits = 256;  // of a warp: see the assertion beside the launch
 
 struct Shared {
     union {
@@ -526,11 +533,13 @@ template <typename R>
 __device__ __forceinline__ void send_list(Shared& sh, const R& row, u32 n) {
     const int tid = threadIdx.x;
     if (row.cs == 1) {
-        for (u32 i = tid; i < min(n, (u32)kListMax); i += R::Geo::kThreads) sh.list[i] = sh.own_list[i];
+        for (u32 i = tid; i < min(n, (u32)kListMax); i += R::Geo::kThreads)
+            sh.list[i] = sh.own_list[i];
         return;
     }
     if (tid == 0)
-        sh.base = n <= kListMax ? atom_add_cluster(map_cluster(smem_u32(&sh.list_n), 0), n) : kListMax;
+        sh.base = n <= kListMax ? atom_add_cluster(map_cluster(smem_u32(&sh.list_n), 0), n)
+                                : kListMax;
     __syncthreads();
     for (u32 i = tid; i < n && sh.base + i < kListMax; i += R::Geo::kThreads)
         st_cluster_b64(map_cluster(smem_u32(&sh.list[sh.base + i]), 0), sh.own_list[i]);
@@ -941,8 +950,8 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas) sample_kernel(SampleArg
     const int cs = 1 << a.lg, rank = cs > 1 ? (int)cluster_ctarank() : 0;
     const int rowi = blockIdx.x >> a.lg;
     const RowView<T> r(a.logits, a.ld, rowi, a.V);
-    Row<T, G> row{r, RowSlice<G>(r, a.per, a.ring, rank, warp, smem, l2_policy_evict_last()), a.lg, cs,
-               rank};
+    Row<T, G> row{r, RowSlice<G>(r, a.per, a.ring, rank, warp, smem, l2_policy_evict_last()),
+                  a.lg, cs, rank};
     const RowSlice<G>& sl = row.sl;
     if (cs > 1) cluster_arrive();  // met by cluster_wait below: every CTA has started
     row.sl.start(r);
@@ -1255,10 +1264,6 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas) sample_kernel(SampleArg
     a.tokens[rowi] = token;
     if (a.probs != nullptr) a.probs[rowi] = (float)((double)tw / (double)total);
 }
-
-}  // namespace
-
-namespace {
 
 template <typename T, typename G>
 cudaError_t launch_typed(SampleArgs a, cudaStream_t stream, int num_sms) {
