@@ -289,7 +289,8 @@ struct RowSlice {
                                          uint32_t at) const {
         if (clean(step)) {
 #pragma unroll
-            for (int i = 0; i < kStepVecs; i += 32) cp_async16_hint(at + 16u * i, src + 16 * i, hint);
+            for (int i = 0; i < kStepVecs; i += 32)
+                cp_async16_hint(at + 16u * i, src + 16 * i, hint);
         } else if ((unsigned)step < (unsigned)steps) {
             load_edge(r, wlo + step * kStepVecs + (int)(threadIdx.x & 31), whi, at);
         }
