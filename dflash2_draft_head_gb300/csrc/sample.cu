@@ -16,22 +16,24 @@
 // The floor is HBM: a row is read once, by one CTA or by the CTAs of a cluster, and passed
 // over two or more times on the chip.  What bounds the kernel is the instructions of
 // those passes: exact weights take 7 an entry.  4096 x 151936 bf16 rows at a temperature
-// take 332 to 360 us (3.5 to 3.75 TB/s), their bytes alone 183 us; 604 us for 512 x 262144
-// fp32 rows cut by top_p inside a flat distribution, which makes five passes.
+// take 300 us (4.15 TB/s), their bytes alone 183 us; 483 us for 512 x 262144 fp32 rows cut
+// by top_p inside a flat distribution, which makes three passes and counts every entry.
 //
 // The largest entries of the row's groups (of 256 or 128) come first: the largest of them
 // is the row's, and the n-th largest is a bound above which at least n entries lie.
 //   - Neither top_k nor top_p: one pass of weights, summed by warp; one warp's part of
 //     the row holds the token and is looked through.
-//   - No more entries to keep than groups, or a top_p that the entries above such a
-//     bound reach: those entries (tens to hundreds) are listed, and one CTA finishes
-//     the row from the list alone.
-//   - Else counts over the distance from the maximum (a bin's weights differ by 1.4%)
-//     leave a bracket of bins that may hold the cut; the exact weight above it narrows
-//     it to one or two.  Up to 1024 entries there are listed and sorted; more of them
-//     (ties) are told apart by histograms of their exact weights over their values,
-//     until the cut lies in one value.  What is kept is then summed by warp and looked
-//     through as in the first case.
+//   - No more entries to keep than groups, or a top_p that the groups' largest entries
+//     reach: the entries above such a bound (tens to hundreds) are listed, and one CTA
+//     finishes the row from the list alone.
+//   - Else counts over the distance from the maximum (with top_p alone taken in the pass
+//     that sums all weights) tell which few bins hold the cut, by bounds of the weights in
+//     each or, likely, by the weights of the bins' middles.  The next pass takes the exact
+//     weight above them and lists their entries; a sorted list that does not hold the cut
+//     narrows the bins.  More than 1024 entries in a bin (ties) are told apart by
+//     histograms of their exact weights over their values, until the cut lies in one
+//     value.  What is kept is summed by warp in the pass that lists, and looked through as
+//     in the first case.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -216,6 +218,14 @@ struct Shared {
     int at, at_hi;
     u32 before_n, upto_n;
     u64 before_w, in_w;
+    // the bins of the likely cut, what stands before them and with them
+    int likely, likely_hi;
+    u32 likely_n, likely_upto, likely_at;
+    // what find_cut found: the cut and the kept weight, every warp's part of that and its ties
+    Cut found;
+    u64 found_w;
+    u64 found_warp_w[kMaxWarps];
+    u32 found_warp_t[kMaxWarps];
 };
 
 // The CTA's, from any function (known to lie in shared memory, unlike an argument).
@@ -224,13 +234,24 @@ __device__ __forceinline__ Shared& shared_block() {
     return sh;
 }
 
+__device__ __forceinline__ char* ring_block() {
+    extern __shared__ __align__(16) char smem[];
+    return smem;
+}
+
+// This CTA's row.
 template <typename T, typename G>
 struct Row {
     using Geo = G;
     static constexpr int E = VecOf<T>::kElems;
+    int lg, cs, rank;
     RowView<T> r;
     RowSlice<G> sl;
-    int lg, cs, rank;
+
+    __device__ __forceinline__ explicit Row(const SampleArgs& a)
+        : lg(a.lg), cs(1 << a.lg), rank(a.lg > 0 ? (int)cluster_ctarank() : 0),
+          r(a.logits, a.ld, blockIdx.x >> a.lg, a.V),
+          sl(r, a.per, a.ring, rank, threadIdx.x >> 5, ring_block(), l2_policy_evict_last()) {}
 
     template <typename F>
     __device__ __forceinline__ void each_vec(F f) {
@@ -336,6 +357,12 @@ struct Bins {
     uint4 b[kBinsOf<G>];
 };
 
+template <typename G>
+__device__ __forceinline__ void clear_bins(Shared& sh) {
+    for (int i = threadIdx.x; i < kBins; i += G::kThreads) sh.bins[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+}
+
 // Adds up the cluster's bins (each CTA a share of them, which it then tells the others)
 // and returns this thread's.  What stood in sh.bins may be overwritten afterwards.
 template <typename R>
@@ -375,44 +402,62 @@ __device__ __forceinline__ Bins<typename R::Geo> merge_bins(Shared& sh, const R&
     return own;
 }
 
-// The bin of a depth: d in bins, rounded by the addition of 2^23, which leaves it in the
-// low bits.
-constexpr float kBinScale = (kDepthBins - 1) / kDepth;
-constexpr float kRound = 8388608.f;
-__device__ __forceinline__ u32 depth_bin(float d) {
-    return __float_as_uint(__fmaf_rn(d, -kBinScale, kRound)) - __float_as_uint(kRound);
-}
-__device__ __forceinline__ uint2 depth_bins(f32x2 d) {
-    const float2 t = halves(fma2(d, pair(-kBinScale, -kBinScale), pair(kRound, kRound)));
-    return make_uint2(__float_as_uint(t.x) - __float_as_uint(kRound),
-                      __float_as_uint(t.y) - __float_as_uint(kRound));
-}
+// Bins of equal width over the depths from 0 down to `deepest`.
+struct DepthBins {
+    float deepest, scale;
+    __device__ __forceinline__ explicit DepthBins(float deepest)
+        : deepest(deepest), scale((kDepthBins - 1) / fmaxf(-deepest, 1.f)) {}
 
-// The depth such that those above it, and no others, lie in bins before `bin`.
-__device__ __forceinline__ float depth_edge(int bin) {
-    if (bin <= 0) return INFINITY;
-    if (bin >= kDepthBins) return -INFINITY;
-    const u32 near = __float_as_uint((bin - 0.5f) / kBinScale);
-    u32 lo = near - 64, hi = near + 64;  // the least number in (lo, hi] in that bin or behind
-    while (hi - lo > 1) {
-        const u32 mid = (lo + hi) >> 1;
-        if (depth_bin(-__uint_as_float(mid)) >= (u32)bin)
-            hi = mid;
-        else
-            lo = mid;
+    // The bin of a depth: d in bins, rounded by the addition of 2^23, which leaves it in
+    // the low bits.
+    static constexpr float kRound = 8388608.f;
+    __device__ __forceinline__ u32 of(float d) const {
+        return __float_as_uint(__fmaf_rn(d, -scale, kRound)) - __float_as_uint(kRound);
     }
-    return -__uint_as_float(hi);
-}
+    // Counts a pair of entries where `x`, `y`.
+    __device__ __forceinline__ void count(u32* counts, float2 d, bool x, bool y) const {
+        const float2 t =
+            halves(fma2(pair(d.x, d.y), pair(-scale, -scale), pair(kRound, kRound)));
+        if (x) atomicAdd(&counts[__float_as_uint(t.x) - __float_as_uint(kRound)], 1u);
+        if (y) atomicAdd(&counts[__float_as_uint(t.y) - __float_as_uint(kRound)], 1u);
+    }
+    // The depth such that those above it, and no others, lie in bins before `bin`.
+    __device__ __forceinline__ float edge(int bin) const {
+        if (bin <= 0) return INFINITY;
+        if (bin >= kDepthBins) return -INFINITY;
+        const u32 near = __float_as_uint((bin - 0.5f) / scale);
+        u32 lo = near - 64, hi = near + 64;  // the least number in (lo, hi] in that bin or behind
+        while (hi - lo > 1) {
+            const u32 mid = (lo + hi) >> 1;
+            if (of(-__uint_as_float(mid)) >= (u32)bin)
+                hi = mid;
+            else
+                lo = mid;
+        }
+        return -__uint_as_float(hi);
+    }
+    // The bounds of a weight in that bin, in units of 2^-40 (the roundings of the depth, of
+    // 2^x and of the weight are far inside 2^-16 of it and 1), and that of its middle.
+    __device__ __forceinline__ u64 most(int bin) const {
+        return __float2ull_ru(ex2(-__fdividef(bin - 0.5f, scale)) * (kOne * (1.f + 1.f / 65536))) +
+               1;
+    }
+    __device__ __forceinline__ u64 least(int bin) const {
+        const u64 w = __float2ull_rd(ex2(-__fdividef(bin + 0.5f, scale)) *
+                                     (kOne * (1.f - 1.f / 65536)));
+        return bin == kDepthBins - 1 || w == 0 ? 0 : w - 1;
+    }
+    __device__ __forceinline__ u64 middle(int bin) const {
+        return __float2ull_rn(ex2(-__fdividef((float)bin, scale)) * kOne);
+    }
+};
 
-// The bounds of a weight in that bin, in units of 2^-40: the roundings of the depth,
-// of 2^x and of the weight are far inside 2^-16 of it and 1.
-__device__ __forceinline__ u64 bin_most(int bin) {
-    return __float2ull_ru(ex2((bin - 0.5f) * -(1.f / kBinScale)) * (kOne * (1.f + 1.f / 65536))) + 1;
-}
-__device__ __forceinline__ u64 bin_least(int bin) {
-    const u64 w = __float2ull_rd(ex2((bin + 0.5f) * -(1.f / kBinScale)) *
-                                 (kOne * (1.f - 1.f / 65536)));
-    return bin == kDepthBins - 1 || w == 0 ? 0 : w - 1;
+// The depth below which no entry is before a cut by weight that leaves out `rest`: entries
+// of less than an even share of that come behind it (less 1 for their rounding, and 7% for
+// that of the depth).
+__device__ __forceinline__ float deepest_cut(float rest, int V) {
+    const float share = rest / (float)V - 1.f;
+    return fmaxf(-kDepth, log2f(fmaxf(share, 0.f)) - 40.1f);
 }
 
 // This lane's part of its warp's weight: all entries.
@@ -548,46 +593,70 @@ __device__ __forceinline__ void send_list(Shared& sh, const R& row, u32 n) {
 // Finds, from the largest entries down, the depth bins that may hold the cut: sh.at to
 // sh.at_hi (one bin by count), with the counts before and up to them; sh.at is
 // kDepthBins when there is no cut.  b: this thread's merged counts; the cut is known to
-// lie in the bins from `from` to `to`, behind base_n entries of weight base_w.
+// lie in the bins from `from` to `to`, behind base_n entries; base_w: the weight before
+// bin `from` or, with `at_end`, up to and with bin `to`.
+// By weight and where those bins have more than kListSure entries: sh.likely to
+// sh.likely_hi are the bins within kAside entries of the cut that the weights of the bins'
+// middles give (of normal logits in fp32 and bf16 that held the cut in 97 of 100 rows, with
+// 200 to 500 entries); sh.likely is kDepthBins when there are too many for a list.
+constexpr u32 kListSure = 256;
+constexpr u32 kAside = 64;
 template <bool BY_COUNT, typename G>
-__device__ __forceinline__ void find_bracket(Shared& sh, const Bins<G>& bins, int from, int to,
-                                             u32 base_n, u64 base_w, u32 k, u64 limit) {
+__device__ __forceinline__ void find_bracket(Shared& sh, const DepthBins& depths,
+                                             const Bins<G>& bins, int from, int to, u32 base_n,
+                                             u64 base_w, bool at_end, u32 k, u64 limit) {
+    using i64 = long long;
     constexpr int kPer = 4 * kBinsOf<G>;
-    const int first = (int)threadIdx.x * kPer;
+    int first = (int)threadIdx.x * kPer;
     auto count = [&](int i) {
         const uint4& b = bins.b[i / 4];
         const u32 n = i % 4 == 0 ? b.x : i % 4 == 1 ? b.y : i % 4 == 2 ? b.z : b.w;
         return first + i < from || first + i > to ? 0 : n;
     };
-    u32 bn = 0, none = 0;
-    u64 least = 0, most = 0;
+    u32 before_n = 0, none = 0;
+    u64 least = 0, most = 0, middle = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        bn += count(i);
+        before_n += count(i);
         if (!BY_COUNT) {
-            least += count(i) * bin_least(first + i);
-            most += count(i) * bin_most(first + i);
+            least += count(i) * depths.least(first + i);
+            most += count(i) * depths.most(first + i);
+            middle += count(i) * depths.middle(first + i);
         }
     }
-    block_before<G>(sh, bn, least);
-    if (!BY_COUNT) block_before<G>(sh, none, most);
+    // by weight: bounds of what stands before a bin, and an estimate of it
+    const u64 all_least = block_before<G>(sh, before_n, least);
+    u64 all_most = 0, all_middle = 0;
+    if (!BY_COUNT) {
+        all_most = block_before<G>(sh, none, most);
+        all_middle = block_before<G>(sh, none, middle);
+    }
+    i64 low = (i64)(least + base_w), high = (i64)(most + base_w), mid = (i64)(middle + base_w);
+    if (at_end) {
+        low = (i64)(base_w - all_most + most);
+        high = (i64)(base_w - all_least + least);
+        mid -= (i64)all_middle;
+    }
     if (threadIdx.x == 0) {
-        sh.at = kDepthBins;
+        sh.at = at_end && high >= (i64)limit ? from : kDepthBins;
         sh.at_hi = to;
-        sh.before_n = 0;
+        sh.before_n = base_n;
         sh.upto_n = 0xffffffffu;
+        sh.likely = kDepthBins;
     }
     __syncthreads();
-    bn += base_n;
-    least += base_w;
-    most += base_w;
+    before_n += base_n;
+    u32 bn = before_n;
+    asm volatile("" : "+r"(first));  // the bins' weights again, rather than kept in registers
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const u32 n = count(i);
-        const u64 l = BY_COUNT ? 0 : n * bin_least(first + i);
-        const u64 h = BY_COUNT ? 0 : n * bin_most(first + i);
-        const bool may = BY_COUNT ? bn < k && bn + n >= k : most < limit && most + h >= limit;
-        const bool must = BY_COUNT ? may : least < limit && least + l >= limit;
+        const i64 l = BY_COUNT ? 0 : n * depths.least(first + i);
+        const i64 h = BY_COUNT ? 0 : n * depths.most(first + i);
+        const i64 m = BY_COUNT ? 0 : n * depths.middle(first + i), want = (i64)limit;
+        const i64 to_low = low + (at_end ? h : l), to_high = high + (at_end ? l : h);
+        const bool may = BY_COUNT ? bn < k && bn + n >= k : high < want && to_high >= want;
+        const bool must = BY_COUNT ? may : low < want && to_low >= want;
         if (may) {
             sh.at = first + i;
             sh.before_n = bn;
@@ -596,9 +665,41 @@ __device__ __forceinline__ void find_bracket(Shared& sh, const Bins<G>& bins, in
             sh.at_hi = first + i;
             sh.upto_n = bn + n;
         }
+        if (!BY_COUNT && mid < want && mid + m >= want && n <= kListMax) {
+            sh.likely = sh.likely_hi = first + i;
+            sh.likely_n = bn;
+            sh.likely_upto = bn + n;
+            sh.likely_at = bn + (u32)((float)n * __fdividef((float)(want - mid), (float)m));
+        }
         bn += n;
-        least += l;
-        most += h;
+        low = to_low;
+        high = to_high;
+        mid += m;
+    }
+    __syncthreads();
+    const int bin = sh.likely, at = sh.at, at_hi = sh.at_hi;
+    if (BY_COUNT || bin == kDepthBins || at == kDepthBins || sh.upto_n - sh.before_n <= kListSure)
+        return;
+    // and the bins with the entries next to that place
+    const u32 likely_n = sh.likely_n, likely_upto = sh.likely_upto;
+    const u32 lo = max(sh.likely_at - min(sh.likely_at, kAside), sh.before_n);
+    const u32 hi = min(sh.likely_at + kAside, sh.upto_n - 1);
+    const u32 spare = (kListMax - (likely_upto - likely_n)) / 2;
+    __syncthreads();
+    bn = before_n;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const u32 n = count(i);
+        const int here = first + i;
+        if (here >= at && here < bin && bn <= lo && lo < bn + n && likely_n - bn <= spare) {
+            sh.likely = here;
+            sh.likely_n = bn;
+        }
+        if (here > bin && here <= at_hi && bn <= hi && hi < bn + n && bn + n - likely_upto <= spare) {
+            sh.likely_hi = here;
+            sh.likely_upto = bn + n;
+        }
+        bn += n;
     }
     __syncthreads();
 }
@@ -638,69 +739,68 @@ __device__ __forceinline__ void find_bin(Shared& sh, const R& row, u32 base_n, u
 }
 
 // The cut by count (the first k entries) or by weight (those with less than `limit`
-// before them, of `all` of their weight), among the entries inside `in`; `in` itself when
-// that cuts nothing.
-struct Found {
-    Cut cut;
-    u64 kept_w;   // the kept entries' weight (by count: where `weigh` asks for it)
-    bool summed;  // this warp's kept weight and ties are known too
-    u64 warp_w;
-    u32 warp_t;
+// before them), among the entries inside `in`; `in` itself when that cuts nothing.
+// `counted`: sh.count has the entries of the depths already.  `weigh`: the kept weight is
+// asked for.  The results are left in sh.found and behind it, so that the call needs few
+// registers; `in` is an earlier call's sh.found.
+struct Flags {
     bool up;      // the direction of the row's next pass
+    bool summed;  // the warps' kept weight and ties are known too
 };
 template <bool BY_COUNT, bool INSIDE, typename T, typename G>
-__device__ __noinline__ Found find_cut(Row<T, G> row, const Weigh g, bool plain,
-                                       const Cut in, u32 k, u64 limit, u64 all, bool weigh) {
+__device__ __noinline__ Flags find_cut(const SampleArgs& a, const Weigh g, bool plain, bool up,
+                                       u32 k, u64 limit, float deepest, bool counted,
+                                       bool weigh) {
     constexpr int E = VecOf<T>::kElems;
     Shared& sh = shared_block();
+    Row<T, G> row(a);
+    row.sl.up = up;
+    const DepthBins depths(deepest);
     const int tid = threadIdx.x, lane = tid & 31;
-    auto clear = [&] {
-        for (int i = tid; i < kBins; i += G::kThreads) sh.bins[i] = make_uint4(0, 0, 0, 0);
+    const Cut in = INSIDE ? sh.found : Cut{0, 0, 0};
+    auto leave = [&](const Cut& cut, u64 kept_w, bool summed) {
         if (tid == 0) {
-            sh.own_n = sh.list_n = 0;
-            sh.span_hi = 0;
-            sh.span_lo = 0xffffffffu;
+            sh.found = cut;
+            sh.found_w = kept_w;
         }
         __syncthreads();
+        return Flags{row.sl.up, summed};
     };
     const float least = INSIDE ? Key<T>::value(in.key) : neg_inf();
-    // by weight: entries below an even share of what is not kept come behind the cut (less
-    // 1 for their rounding, and 7% for that of the depth)
-    const float share = (float)(all - min(all, limit)) / (float)row.r.V - 1.f;
-    const float deepest = BY_COUNT ? -kDepth : fmaxf(-kDepth, log2f(fmaxf(share, 0.f)) - 40.1f);
-    clear();
-    row.each_pair(g, plain, [&](int, float2 x, float2 d) {
-        const uint2 bin = depth_bins(pair(d.x, d.y));
-        if (d.x >= deepest && (!INSIDE || x.x >= least)) atomicAdd(&sh.count[bin.x], 1u);
-        if (d.y >= deepest && (!INSIDE || x.y >= least)) atomicAdd(&sh.count[bin.y], 1u);
-    });
-    const Bins<G> counts = merge_bins(sh, row);
-    find_bracket<BY_COUNT, G>(sh, counts, 0, kDepthBins - 1, 0, 0, k, limit);
-    int at = sh.at, at_hi = sh.at_hi;
-    u64 lane_w = 0, w = 0;  // the weight before bin `at`: this lane's part, the row's
-    if (!BY_COUNT && at < kDepthBins && sh.upto_n - sh.before_n > kListMax) {
-        const u32 before = sh.before_n;
-        const float edge = depth_edge(at);
-        WeightSum sum;
-        int entries = 0;
+    if (!counted) {
+        clear_bins<G>(sh);
         row.each_pair(g, plain, [&](int, float2 x, float2 d) {
-            const float wx = ex2(d.x), wy = ex2(d.y);
-            sum.add(pair(d.x > edge && (!INSIDE || x.x >= least) ? wx : 0.f,
-                         d.y > edge && (!INSIDE || x.y >= least) ? wy : 0.f));
-            entries += 2;
+            depths.count(sh.count, d, d.x >= depths.deepest && (!INSIDE || x.x >= least),
+                         d.y >= depths.deepest && (!INSIDE || x.y >= least));
         });
-        w = row_weight(sh, row, sum.total(entries));
-        find_bracket<false, G>(sh, counts, at, at_hi, before, w, k, limit);
-        at = min(sh.at, kDepthBins - 1);
-        at_hi = sh.at_hi;
     }
-    u32 n = sh.before_n;
-    const u32 inside = sh.upto_n - n;
-    const bool listed = at < kDepthBins && inside <= kListMax;
-    // and the bracket's entries, or the span of their keys
-    const float edge = depth_edge(at), end = depth_edge(at_hi + 1), low = fmaxf(end, deepest);
+    const Bins<G> counts = merge_bins(sh, row);
+    find_bracket<BY_COUNT, G>(sh, depths, counts, 0, kDepthBins - 1, 0, 0, false, k, limit);
+    if (tid == 0) {
+        sh.own_n = sh.list_n = 0;
+        sh.span_hi = 0;
+        sh.span_lo = 0xffffffffu;
+    }
+    __syncthreads();
+    u64 w = 0;  // the weight before the bins that are looked at
+    u32 n = 0;  // and the entries
     float hi_x = neg_inf(), lo_x = INFINITY;
-    {
+    for (int turn = 0;; ++turn) {
+        int at = sh.at, at_hi = sh.at_hi;
+        n = sh.before_n;
+        u32 inside = sh.upto_n - n;
+        const bool sure = BY_COUNT || at == kDepthBins || inside <= kListSure || turn == 2 ||
+                          sh.likely == kDepthBins;
+        const bool listed = at < kDepthBins && (!sure || inside <= kListMax);
+        if (!sure) {
+            at = sh.likely;
+            at_hi = sh.likely_hi;
+            n = sh.likely_n;
+            inside = sh.likely_upto - n;
+        }
+        // the weight before them, and their entries or the span of their keys
+        const float edge = depths.edge(at), end = depths.edge(at_hi + 1);
+        const float low = fmaxf(end, depths.deepest);
         WeightSum sum;
         int entries = 0;
         auto look = [&](int index, float x, float d) {
@@ -723,70 +823,91 @@ __device__ __noinline__ Found find_cut(Row<T, G> row, const Weigh g, bool plain,
                 if (d.y >= low) look(index + 1, x.y, d.y);
             }
         });
-        lane_w = sum.total(entries);
-    }
-    w = row_weight(sh, row, lane_w);
-    if (at == kDepthBins) return {in, w, false, 0, 0, row.sl.up};
-    if (listed) {
-        const u32 own = sh.own_n;
-        send_list(sh, row, own);
-        row.sync();
-        if (row.rank == 0) {
-            // the last kept entry's place in the sorted list; its ties before it are kept
-            constexpr int kPer = kListMax / G::kThreads;
-            sort_list<G>(sh, (int)inside);
-            u64 W[kPer], before = 0;
+        const u64 lane_w = sum.total(entries);
+        w = row_weight(sh, row, lane_w);
+        if (at == kDepthBins) return leave(in, w, false);
+        if (!listed) break;
+        const bool before = !sure && w >= limit;  // the cut comes before these bins
+        if (!before) {
+            const u32 own = sh.own_n;
+            send_list(sh, row, own);
+            row.sync();
+            if (row.rank == 0) {
+                // the last kept entry's place in the sorted list; its ties before it are kept
+                constexpr int kPer = kListMax / G::kThreads;
+                sort_list<G>(sh, (int)inside);
+                u64 W[kPer], upto = 0;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const u32 q = (u32)(tid * kPer + i);
-                W[i] = q < inside
-                           ? Weigh::fixed(Weigh::w(g.depth(Key<T>::value((u32)(sh.list[q] >> 32)))))
-                           : 0;
-                before += W[i];
-            }
-            u32 none = 0;
-            block_before<G>(sh, none, before);
-            before += w;
+                for (int i = 0; i < kPer; ++i) {
+                    const u32 q = (u32)(tid * kPer + i);
+                    W[i] = q < inside ? Weigh::fixed(Weigh::w(
+                                            g.depth(Key<T>::value((u32)(sh.list[q] >> 32)))))
+                                      : 0;
+                    upto += W[i];
+                }
+                u32 none = 0;
+                block_before<G>(sh, none, upto);
+                upto += w;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const u32 q = (u32)(tid * kPer + i);
-                const bool last = BY_COUNT ? n + q + 1 == k
-                                           : q < inside && before < limit && before + W[i] >= limit;
-                before += W[i];
-                if (!last) continue;
-                const u32 key = (u32)(sh.list[q] >> 32);
-                u32 ties = 1;
-                while (ties <= q && (u32)(sh.list[q - ties] >> 32) == key) ++ties;
-                for (int to = 0; to < row.cs; ++to) {
-                    if (row.cs > 1) {
-                        const u32 answer = map_cluster(smem_u32(sh.answer), to);
-                        st_cluster_b64(answer, (u64)key << 32 | ties);
-                        st_cluster_b64(answer + 8, before);
-                    } else {
-                        sh.answer[0] = (u64)key << 32 | ties;
-                        sh.answer[1] = before;
+                for (int i = 0; i < kPer; ++i) {
+                    const u32 q = (u32)(tid * kPer + i);
+                    if (q >= inside) break;
+                    const bool last = BY_COUNT ? n + q + 1 == k
+                                               : upto < limit && upto + W[i] >= limit;
+                    upto += W[i];
+                    const bool none_last = !sure && q + 1 == inside && upto < limit;
+                    if (!last && !none_last) continue;
+                    u64 answer = 0;
+                    if (last) {
+                        const u32 key = (u32)(sh.list[q] >> 32);
+                        u32 ties = 1;
+                        while (ties <= q && (u32)(sh.list[q - ties] >> 32) == key) ++ties;
+                        answer = (u64)key << 32 | ties;
+                    }
+                    for (int to = 0; to < row.cs; ++to) {
+                        if (row.cs > 1) {
+                            const u32 there = map_cluster(smem_u32(sh.answer), to);
+                            st_cluster_b64(there, answer);
+                            st_cluster_b64(there + 8, upto);
+                        } else {
+                            sh.answer[0] = answer;
+                            sh.answer[1] = upto;
+                        }
                     }
                 }
             }
+            row.sync();
+            Cut out{(u32)(sh.answer[0] >> 32), (u32)sh.answer[0], 0};
+            w = sh.answer[1];
+            if (sure || out.key != 0) {
+                out.weight = Weigh::fixed(Weigh::w(g.depth(Key<T>::value(out.key))));
+                if (out.key == in.key) out.ties = min(out.ties, in.ties);
+                // this warp's entries of the list
+                u64 warp_w = lane_w;
+                u32 ties = 0;
+                for (u32 i = lane; i < own; i += 32) {
+                    const u64 e = sh.own_list[i];
+                    const int v = ((int)~(u32)e + row.r.head) / E;
+                    if (v < row.sl.wlo || v >= row.sl.whi) continue;
+                    const u32 key = (u32)(e >> 32);
+                    if (key > out.key) warp_w += Weigh::fixed(Weigh::w(g.depth(Key<T>::value(key))));
+                    ties += key == out.key;
+                }
+                warp_w = warp_sum(warp_w);
+                ties = __reduce_add_sync(0xffffffffu, ties);
+                if (lane == 0) {
+                    sh.found_warp_w[tid >> 5] = warp_w;
+                    sh.found_warp_t[tid >> 5] = ties;
+                }
+                return leave(out, w, true);
+            }
         }
-        row.sync();
-        Cut out{(u32)(sh.answer[0] >> 32), (u32)sh.answer[0], 0};
-        out.weight = Weigh::fixed(Weigh::w(g.depth(Key<T>::value(out.key))));
-        if (out.key == in.key) out.ties = min(out.ties, in.ties);
-        // this warp's entries of the list
-        u64 sum = lane_w;
-        u32 ties = 0;
-        for (u32 i = lane; i < own; i += 32) {
-            const u64 e = sh.own_list[i];
-            const int v = ((int)~(u32)e + row.r.head) / E;
-            if (v < row.sl.wlo || v >= row.sl.whi) continue;
-            const u32 key = (u32)(e >> 32);
-            if (key > out.key) sum += Weigh::fixed(Weigh::w(g.depth(Key<T>::value(key))));
-            ties += key == out.key;
-        }
-        const u64 kept_w = sh.answer[1];
+        // what was found narrows the bins
+        const int from = before ? sh.at : at_hi + 1, to = before ? at - 1 : sh.at_hi;
+        const u32 base_n = before ? sh.before_n : n + inside;
         __syncthreads();
-        return {out, kept_w, true, warp_sum(sum), __reduce_add_sync(0xffffffffu, ties), row.sl.up};
+        if (tid == 0) sh.own_n = sh.list_n = 0;
+        find_bracket<BY_COUNT, G>(sh, depths, counts, from, to, base_n, w, before, k, limit);
     }
 
     u32 hi = __reduce_max_sync(0xffffffffu, hi_x >= lo_x ? Key<T>::of(hi_x) : 0);
@@ -815,7 +936,7 @@ __device__ __noinline__ Found find_cut(Row<T, G> row, const Weigh g, bool plain,
         more = hi != lo;
         const int shift = max(0, 32 - __clz((hi - lo) | 1) - 9);
         const float hi_v = Key<T>::value(hi), lo_v = Key<T>::value(lo);
-        clear();
+        clear_bins<G>(sh);
         row.each_pair(g, plain, [&](int, float2 x, float2 d) {
             auto add = [&](float x, float d) {
                 if (!(x >= lo_v && x <= hi_v)) return;
@@ -858,8 +979,7 @@ __device__ __noinline__ Found find_cut(Row<T, G> row, const Weigh g, bool plain,
         kept_weight(row, g, plain, out, 0.f, w, none);
         w = row_weight(sh, row, w);
     }
-    __syncthreads();
-    return {out, w + out.ties * out.weight, false, 0, 0, row.sl.up};
+    return leave(out, w + out.ties * out.weight, false);
 }
 
 // Finishes a row from its list of n entries, which holds the first k (k > 0) or those
@@ -940,186 +1060,39 @@ __device__ __forceinline__ float group_bound(const Shared& sh, int n) {
     return Key<float>::value(lo << 16);
 }
 
-template <typename T, typename G>
-__global__ void __launch_bounds__(G::kThreads, G::kCtas) sample_kernel(SampleArgs a) {
+// Chooses the token among the entries inside the cut that min_p keeps.  `summed`: the
+// warps' kept weight (without min_p) and their ties are left behind sh.found.
+template <bool CUT, typename T, typename G>
+__device__ __forceinline__ void choose(const SampleArgs& a, Row<T, G>& row, const Weigh& g,
+                                       bool plain, const Cut cut, bool summed, float min_p) {
     constexpr int E = VecOf<T>::kElems;
-    extern __shared__ __align__(16) char smem[];
     Shared& sh = shared_block();
-
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int cs = 1 << a.lg, rank = cs > 1 ? (int)cluster_ctarank() : 0;
-    const int rowi = blockIdx.x >> a.lg;
-    const RowView<T> r(a.logits, a.ld, rowi, a.V);
-    Row<T, G> row{r, RowSlice<G>(r, a.per, a.ring, rank, warp, smem, l2_policy_evict_last()),
-                  a.lg, cs, rank};
-    const RowSlice<G>& sl = row.sl;
-    if (cs > 1) cluster_arrive();  // met by cluster_wait below: every CTA has started
-    row.sl.start(r);
+    const RowView<T>& r = row.r;
+    const int cs = row.cs, rank = row.rank, rowi = blockIdx.x >> a.lg;
     const float uniform = a.uniform[rowi];
-    float T0 = a.temperature != nullptr ? a.temperature[rowi] : a.temperature0;
-    int k = a.top_k != nullptr ? a.top_k[rowi] : a.top_k0;
-    const float p = a.top_p != nullptr ? a.top_p[rowi] : a.top_p0;
-    float min_p = a.min_p != nullptr ? a.min_p[rowi] : a.min_p0;
-    if (!(T0 > 0.f)) T0 = 0.f;
-    if (k < 0 || k >= a.V) k = 0;
-    if (T0 == 0.f || p <= 0.f || min_p > 1.f) k = 1;  // the first entry is always kept
-    if (k == 1) min_p = 0.f;
-    if (tid == 0) sh.own_n = sh.list_n = 0;
-
-    // the largest entries of the groups (kLanes * cs lanes each) and of the row
-    constexpr int kLanes = G::kThreads / kGroups<G>;
-    static_assert(kLanes >= 1 && kLanes * kRowMaxCluster <= 32);
-    RunningMax<T> most;
-    row.each_vec([&](int, const uint4& v) { most.add(v); });
-    float m = most.value();
-    const bool has_nan = __any_sync(0xffffffffu, m != m);
-    if (has_nan) {
-        m = neg_inf();
-        row.each_vec([&](int, const uint4& v) { m = fmaxf(m, vec_max<T>(v)); });
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float other = __shfl_xor_sync(0xffffffffu, m, o);
-        if (o < kLanes << a.lg) m = fmaxf(m, other);
-    }
-    if ((tid & ((kLanes << a.lg) - 1)) == 0)
-        (cs > 1 ? sh.own_max : sh.group_max)[tid / kLanes >> a.lg] = m;
-    __syncthreads();
-    if (cs > 1) {
-        cluster_wait();
-        // kGroups / 4 of the threads send four maxima each to one of the CTAs
-        constexpr int kLog = kGroups<G> == 256 ? 6 : 5;
-        static_assert(kGroups<G> / 4 == 1 << kLog);
-        const int lq = kLog - a.lg, quads = 1 << lq, to = tid >> lq, i = tid & (quads - 1);
-        if (to < cs)
-            st_cluster_v4(map_cluster(smem_u32(&sh.group_max[4 * (rank * quads + i)]), to),
-                          reinterpret_cast<const float4*>(sh.own_max)[i]);
-        row.sync();
-    }
-    m = neg_inf();
-    for (int i = lane; i < kGroups<G>; i += 32) m = fmaxf(m, sh.group_max[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m == neg_inf()) {  // nothing to choose from
-        if (rank == 0 && tid == 0) {
-            a.tokens[rowi] = -1;
-            if (a.probs != nullptr) a.probs[rowi] = 0.f;
-        }
-        return;
-    }
-    const Weigh g{m, __fdiv_rn(kLog2e, T0 > 0.f ? T0 : 1.f)};
-    const bool plain = !has_nan && m < INFINITY;
-
-    Cut cut{0, 0, 0};
-    bool summed = false;
-    u64 sw = 0;
-    u32 st = 0;
-    if (k > 0 || p < 1.f) {
-        u64 all = 0, limit = ~0ull;  // (without top_k) the row's weight and top_p's part of it
-        // Is a list short enough?  Without top_k: of about as many entries as half the
-        // groups, unless the groups' maxima are far from what top_p asks for.  Where it is
-        // not, all entries of a row of up to kListMax.
-        const int want = k > 0 ? k : kGroups<G> / 2;
-        const bool small = a.V <= kListMax;
-        bool list = want <= kGroups<G>;
-        if (k == 0) {
-            all = row_weight(sh, row, all_weight(row, g, plain));
-            limit = limit_of(p, all);
-            u64 most = tid < kGroups<G> ? Weigh::fixed(Weigh::w(g.depth(sh.group_max[tid]))) : 0;
-            u32 none = 0;
-            block_sum<G>(sh, none, most);
-            list = most >= (small ? limit : limit / 4);
-        }
-        if (list || small) {
-            if (warp == 0) {
-                const float b = list ? group_bound<G>(sh, want) : neg_inf();
-                if (lane == 0) sh.bound = b > -3.402823466e38f ? b : -3.402823466e38f;
-            }
-            __syncthreads();
-            const float bound = sh.bound;
-            u64 listed_w = 0;
-            row.each_vec([&](int v, const uint4& vec) {
-                if (!(vec_max<T>(vec) >= bound)) return;
-                float x[E];
-                unpack(vec, x);
-#pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    if (!(x[j] >= bound)) continue;
-                    const u32 at = atomicAdd(&sh.own_n, 1u);
-                    if (at < kListMax) sh.own_list[at] = entry_of<T>(x[j], v * E + j - r.head);
-                    if (k == 0) listed_w += Weigh::fixed(Weigh::w(g.depth(x[j])));
-                }
-            });
-            u32 none = 0;
-            if (k == 0) block_sum<G>(sh, none, listed_w);
-            __syncthreads();
-            const u32 own = sh.own_n;
-            send_list(sh, row, own);
-            if (cs > 1) {
-                if (tid < cs) {
-                    st_cluster_b64(map_cluster(smem_u32(&sh.told_n[rank]), tid), own);
-                    st_cluster_b64(map_cluster(smem_u32(&sh.told_w[rank]), tid), listed_w);
-                }
-            } else if (tid == 0) {
-                sh.told_n[0] = own;
-                sh.told_w[0] = listed_w;
-            }
-            row.sync();
-            u64 n = 0;
-            listed_w = 0;
-            for (int i = 0; i < cs; ++i) {
-                n += sh.told_n[i];
-                listed_w += sh.told_w[i];
-            }
-            if (n <= kListMax && (k > 0 || listed_w >= limit)) {
-                // the other CTAs' shared memory is not touched any more
-                if (rank == 0) finish_list<T, G>(a, g, rowi, (int)n, k, p, min_p, all);
-                return;
-            }
-            __syncthreads();
-        }
-        u64 kept = all;
-        if (k > 0) {
-            const Found f = find_cut<true, false>(row, g, plain, cut, (u32)k, 0, 0, p < 1.f);
-            cut = f.cut;
-            kept = f.kept_w;
-            row.sl.up = f.up;
-            summed = f.summed;
-            sw = f.warp_w;
-            st = f.warp_t;
-        }
-        if (p < 1.f) {
-            limit = limit_of(p, kept);
-            const Found f = cut.key != 0
-                                ? find_cut<false, true>(row, g, plain, cut, 0, limit, kept, true)
-                                : find_cut<false, false>(row, g, plain, cut, 0, limit, kept, true);
-            cut = f.cut;
-            row.sl.up = f.up;
-            summed = f.summed;
-            sw = f.warp_w;
-            st = f.warp_t;
-        }
-    }
 
     // every warp's kept weight and its ties at the cut
     const bool everything = cut.key == 0 && !(min_p > 0.f);
     const float floor = cut.key != 0 ? Key<T>::value(cut.key) : neg_inf();
-    const float min_d = min_p > 0.f ? log2f(min_p) - 0.02f : neg_inf();  // w < min_p below it
+    const float least = min_p > 0.f ? min_p : 0.f;
     auto kept_of = [&](const uint4& vec, u64& w, u32& ties) {
-        if (everything && plain) {
+        if (plain) {
             f32x2 x[E / 2];
             unpack(vec, x);
+            const f32x2 nm = pair(-g.m, -g.m), c = pair(g.c, g.c);
             WeightSum ws;
 #pragma unroll
             for (int j = 0; j < E / 2; ++j) {
-                const float2 h = halves(x[j]);
-                ws.add(pair(Weigh::w(g.depth(h.x)), Weigh::w(g.depth(h.y))));
+                const float2 h = halves(x[j]), d = halves(mul2(add2(x[j], nm), c));
+                const float wx = ex2(d.x), wy = ex2(d.y);
+                const bool kx = wx >= least, ky = wy >= least;
+                ws.add(pair(kx && h.x > floor ? wx : 0.f, ky && h.y > floor ? wy : 0.f));
+                ties += (kx && h.x == floor) + (ky && h.y == floor);
             }
             w += ws.total(E);
             return;
         }
-        const float most = vec_max<T>(vec);  // one of the kept entries is rare: look at it first
-        if (!(most >= floor) || !(g.depth(most) >= min_d)) return;
         float x[E];
         unpack(vec, x);
 #pragma unroll
@@ -1133,7 +1106,13 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas) sample_kernel(SampleArg
                 ties += Weigh::fixed(wj) != 0;
         }
     };
-    if (!summed || min_p > 0.f) {
+    u64 sw = 0;
+    u32 st = 0;
+    // (the weights above the cut's are not below it by more than the rounding of 2^x)
+    if (CUT && summed && Weigh::w(g.depth(floor)) >= min_p * (1.f + 1.f / 1048576)) {
+        sw = sh.found_warp_w[warp];
+        st = sh.found_warp_t[warp];
+    } else {
         if (everything)
             sw = all_weight(row, g, plain);
         else
@@ -1203,7 +1182,7 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas) sample_kernel(SampleArg
     const int holder = pick(sh.part_w, sh.part_t, q, target);
     if (holder / G::kWarps != rank) return;
 
-    const RowSlice<G> own(r, a.per, a.ring, rank, holder % G::kWarps, smem, 0);
+    const RowSlice<G> own(r, a.per, a.ring, rank, holder % G::kWarps, ring_block(), 0);
     const int units = (own.whi - own.wlo + 31) >> 5;
     constexpr int kAhead = 3;  // units of a warp loaded together
     for (int u0 = warp; u0 < units; u0 += kAhead * G::kWarps) {
@@ -1265,6 +1244,191 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas) sample_kernel(SampleArg
     if (a.probs != nullptr) a.probs[rowi] = (float)((double)tw / (double)total);
 }
 
+// Finds the cut by top_k, then that by top_p among what it keeps, and chooses.  all, limit:
+// the row's weight and top_p's part of it, where there is no top_k.  A call of its own, the
+// kernel's last: inside it its registers cost the passes before it (2048 x 151936 bf16,
+// top_k 20: 149 us, 176).
+template <typename T, typename G>
+__device__ __noinline__ void choose_cut(const SampleArgs& a, const Weigh g, bool plain, bool up,
+                                        int k, float p, float min_p, u64 all, u64 limit,
+                                        float deepest, bool counted) {
+    Shared& sh = shared_block();
+    Flags f{up, false};
+    const bool cuts = k > 0 || p < 1.f;
+    if (k > 0) {
+        f = find_cut<true, false, T, G>(a, g, plain, f.up, (u32)k, 0, -kDepth, false, p < 1.f);
+        if (p < 1.f) {
+            all = sh.found_w;
+            limit = limit_of(p, all);
+        }
+    }
+    if (p < 1.f) {
+        if (!counted) deepest = deepest_cut((float)(all - min(all, limit)), a.V);
+        if (k > 0 && sh.found.key != 0)
+            f = find_cut<false, true, T, G>(a, g, plain, f.up, 0, limit, deepest, false, true);
+        else
+            f = find_cut<false, false, T, G>(a, g, plain, f.up, 0, limit, deepest, counted,
+                                             true);
+    }
+    Row<T, G> row(a);
+    row.sl.up = f.up;
+    choose<true>(a, row, g, plain, cuts ? sh.found : Cut{0, 0, 0}, f.summed, min_p);
+}
+
+// CUTS: top_k or top_p may be set, or the largest entry may be all that is kept.  Without
+// that code a temperature alone has more registers (4096 x 151936 bf16: 300 us, 360).
+template <typename T, typename G, bool CUTS>
+__global__ void __launch_bounds__(G::kThreads, G::kCtas)
+    sample_kernel(const __grid_constant__ SampleArgs a) {
+    constexpr int E = VecOf<T>::kElems;
+    Shared& sh = shared_block();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Row<T, G> row(a);
+    const RowView<T>& r = row.r;
+    const RowSlice<G>& sl = row.sl;
+    const int cs = row.cs, rank = row.rank, rowi = blockIdx.x >> a.lg;
+    if (cs > 1) cluster_arrive();  // met by cluster_wait below: every CTA has started
+    row.sl.start(r);
+    float T0 = a.temperature != nullptr ? a.temperature[rowi] : a.temperature0;
+    int k = a.top_k != nullptr ? a.top_k[rowi] : a.top_k0;
+    const float p = a.top_p != nullptr ? a.top_p[rowi] : a.top_p0;
+    float min_p = a.min_p != nullptr ? a.min_p[rowi] : a.min_p0;
+    if (!(T0 > 0.f)) T0 = 0.f;
+    if (k < 0 || k >= a.V) k = 0;
+    if (T0 == 0.f || p <= 0.f || min_p > 1.f) k = 1;  // the first entry is always kept
+    if (k == 1) min_p = 0.f;
+    if (tid == 0) sh.own_n = sh.list_n = 0;
+
+    // the largest entries of the groups (kLanes * cs lanes each) and of the row
+    constexpr int kLanes = G::kThreads / kGroups<G>;
+    static_assert(kLanes >= 1 && kLanes * kRowMaxCluster <= 32);
+    RunningMax<T> most;
+    row.each_vec([&](int, const uint4& v) { most.add(v); });
+    float m = most.value();
+    const bool has_nan = __any_sync(0xffffffffu, m != m);
+    if (has_nan) {
+        m = neg_inf();
+        row.each_vec([&](int, const uint4& v) { m = fmaxf(m, vec_max<T>(v)); });
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, m, o);
+        if (o < kLanes << a.lg) m = fmaxf(m, other);
+    }
+    if ((tid & ((kLanes << a.lg) - 1)) == 0)
+        (cs > 1 ? sh.own_max : sh.group_max)[tid / kLanes >> a.lg] = m;
+    __syncthreads();
+    if (cs > 1) {
+        cluster_wait();
+        // kGroups / 4 of the threads send four maxima each to one of the CTAs
+        constexpr int kLog = kGroups<G> == 256 ? 6 : 5;
+        static_assert(kGroups<G> / 4 == 1 << kLog);
+        const int lq = kLog - a.lg, quads = 1 << lq, to = tid >> lq, i = tid & (quads - 1);
+        if (to < cs)
+            st_cluster_v4(map_cluster(smem_u32(&sh.group_max[4 * (rank * quads + i)]), to),
+                          reinterpret_cast<const float4*>(sh.own_max)[i]);
+        row.sync();
+    }
+    m = neg_inf();
+    for (int i = lane; i < kGroups<G>; i += 32) m = fmaxf(m, sh.group_max[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == neg_inf()) {  // nothing to choose from
+        if (rank == 0 && tid == 0) {
+            a.tokens[rowi] = -1;
+            if (a.probs != nullptr) a.probs[rowi] = 0.f;
+        }
+        return;
+    }
+    const Weigh g{m, __fdiv_rn(kLog2e, T0 > 0.f ? T0 : 1.f)};
+    const bool plain = !has_nan && m < INFINITY;
+
+    u64 all = 0, limit = ~0ull;  // (without top_k) the row's weight and top_p's part of it
+    float deepest = -kDepth;     // of the counts
+    bool counted = false;
+    if (CUTS && (k > 0 || p < 1.f)) {
+        // Is a list short enough?  Without top_k: of about as many entries as half the
+        // groups, unless the groups' maxima are far from what top_p asks for.  Where it is
+        // not, all entries of a row of up to kListMax.
+        const int want = k > 0 ? k : kGroups<G> / 2;
+        const bool small = a.V <= kListMax;
+        bool list = want <= kGroups<G>;
+        if (k == 0) {
+            clear_bins<G>(sh);
+            u64 most = tid < kGroups<G> ? Weigh::fixed(Weigh::w(g.depth(sh.group_max[tid]))) : 0;
+            u32 none = 0;
+            block_sum<G>(sh, none, most);
+            // (a part of the weight, whose rest is not above the row's)
+            deepest = deepest_cut((1.f - p) * 0.999f * (float)most, a.V);
+            const DepthBins depths(deepest);
+            WeightSum ws;
+            int entries = 0;
+            row.each_pair(g, plain, [&](int, float2, float2 d) {
+                ws.add(pair(ex2(d.x), ex2(d.y)));
+                entries += 2;
+                depths.count(sh.count, d, d.x >= deepest, d.y >= deepest);
+            });
+            all = row_weight(sh, row, ws.total(entries));
+            limit = limit_of(p, all);
+            list = most >= limit;
+        }
+        counted = k == 0;
+        if (list || small) {
+            counted = false;
+            if (warp == 0) {
+                const float b = list ? group_bound<G>(sh, want) : neg_inf();
+                if (lane == 0) sh.bound = b > -3.402823466e38f ? b : -3.402823466e38f;
+            }
+            __syncthreads();
+            const float bound = sh.bound;
+            u64 listed_w = 0;
+            row.each_vec([&](int v, const uint4& vec) {
+                if (!(vec_max<T>(vec) >= bound)) return;
+                float x[E];
+                unpack(vec, x);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    if (!(x[j] >= bound)) continue;
+                    const u32 at = atomicAdd(&sh.own_n, 1u);
+                    if (at < kListMax) sh.own_list[at] = entry_of<T>(x[j], v * E + j - r.head);
+                    if (k == 0) listed_w += Weigh::fixed(Weigh::w(g.depth(x[j])));
+                }
+            });
+            u32 none = 0;
+            if (k == 0) block_sum<G>(sh, none, listed_w);
+            __syncthreads();
+            const u32 own = sh.own_n;
+            send_list(sh, row, own);
+            if (cs > 1) {
+                if (tid < cs) {
+                    st_cluster_b64(map_cluster(smem_u32(&sh.told_n[rank]), tid), own);
+                    st_cluster_b64(map_cluster(smem_u32(&sh.told_w[rank]), tid), listed_w);
+                }
+            } else if (tid == 0) {
+                sh.told_n[0] = own;
+                sh.told_w[0] = listed_w;
+            }
+            row.sync();
+            u64 n = 0;
+            listed_w = 0;
+            for (int i = 0; i < cs; ++i) {
+                n += sh.told_n[i];
+                listed_w += sh.told_w[i];
+            }
+            if (n <= kListMax && (k > 0 || listed_w >= limit)) {
+                // the other CTAs' shared memory is not touched any more
+                if (rank == 0) finish_list<T, G>(a, g, rowi, (int)n, k, p, min_p, all);
+                return;
+            }
+            __syncthreads();
+        }
+    }
+    if (CUTS)
+        choose_cut<T, G>(a, g, plain, row.sl.up, k, p, min_p, all, limit, deepest, counted);
+    else
+        choose<false>(a, row, g, plain, Cut{0, 0, 0}, false, min_p);
+}
+
 template <typename T, typename G>
 cudaError_t launch_typed(SampleArgs a, cudaStream_t stream, int num_sms) {
     // the widest row: kSampleMaxV fp32 entries over the largest cluster
@@ -1274,7 +1438,13 @@ cudaError_t launch_typed(SampleArgs a, cudaStream_t stream, int num_sms) {
     a.lg = p.lg;
     a.per = p.per;
     a.ring = p.ring;
-    return launch_rows<G, sample_kernel<T, G>>(a, a.rows, a.lg, p.smem, G::kRingBytes, stream);
+    const bool cuts = a.top_k != nullptr || (a.top_k0 > 0 && a.top_k0 < a.V) ||
+                      a.top_p != nullptr || a.top_p0 < 1.f || a.temperature != nullptr ||
+                      !(a.temperature0 > 0.f) || a.min_p != nullptr || a.min_p0 > 1.f;
+    return cuts ? launch_rows<G, sample_kernel<T, G, true>>(a, a.rows, a.lg, p.smem,
+                                                            G::kRingBytes, stream)
+                : launch_rows<G, sample_kernel<T, G, false>>(a, a.rows, a.lg, p.smem,
+                                                             G::kRingBytes, stream);
 }
 
 }  // namespace
