@@ -213,6 +213,7 @@ struct Shared {
     u32 span_hi, span_lo;
     u32 scan_n[kMaxWarps];
     u64 scan_w[kMaxWarps];
+    u64 scan_w3[3][kMaxWarps];
     // the bins that may hold the cut: what stands before them and with them; for one bin
     // the weights
     int at, at_hi;
@@ -349,6 +350,34 @@ __device__ __forceinline__ u64 block_before(Shared& sh, u32& n, u64& w) {
     return all;
 }
 
+// The same of a count and three weights; `all`: the sums of those.
+template <typename G>
+__device__ __forceinline__ void block_before(Shared& sh, u32& n, u64 (&w)[3], u64 (&all)[3]) {
+    const int warp = (int)threadIdx.x >> 5;
+    const u32 bn = warp_before(n);
+    u64 bw[3];
+#pragma unroll
+    for (int q = 0; q < 3; ++q) bw[q] = warp_before(w[q]);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 31) {
+        sh.scan_n[warp] = bn + n;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) sh.scan_w3[q][warp] = bw[q] + w[q];
+    }
+    __syncthreads();
+    n = bn;
+    for (int i = 0; i < warp; ++i) n += sh.scan_n[i];
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+        w[q] = bw[q];
+        all[q] = 0;
+        for (int i = 0; i < G::kWarps; ++i) {
+            if (i == warp) w[q] += all[q];
+            all[q] += sh.scan_w3[q][i];
+        }
+    }
+}
+
 // A thread's bins: kBinsOf<G> neighbours of the table.
 template <typename G>
 constexpr int kBinsOf = kBins / G::kThreads;
@@ -435,20 +464,6 @@ struct DepthBins {
                 lo = mid;
         }
         return -__uint_as_float(hi);
-    }
-    // The bounds of a weight in that bin, in units of 2^-40 (the roundings of the depth, of
-    // 2^x and of the weight are far inside 2^-16 of it and 1), and that of its middle.
-    __device__ __forceinline__ u64 most(int bin) const {
-        return __float2ull_ru(ex2(-__fdividef(bin - 0.5f, scale)) * (kOne * (1.f + 1.f / 65536))) +
-               1;
-    }
-    __device__ __forceinline__ u64 least(int bin) const {
-        const u64 w = __float2ull_rd(ex2(-__fdividef(bin + 0.5f, scale)) *
-                                     (kOne * (1.f - 1.f / 65536)));
-        return bin == kDepthBins - 1 || w == 0 ? 0 : w - 1;
-    }
-    __device__ __forceinline__ u64 middle(int bin) const {
-        return __float2ull_rn(ex2(-__fdividef((float)bin, scale)) * kOne);
     }
 };
 
@@ -613,29 +628,41 @@ __device__ __forceinline__ void find_bracket(Shared& sh, const DepthBins& depths
         const u32 n = i % 4 == 0 ? b.x : i % 4 == 1 ? b.y : i % 4 == 2 ? b.z : b.w;
         return first + i < from || first + i > to ? 0 : n;
     };
-    u32 before_n = 0, none = 0;
-    u64 least = 0, most = 0, middle = 0;
+    // the bounds of the bins' weights, in units of 2^-40 (the roundings of the depth, of 2^x
+    // and of the weight are far inside 2^-16 of it and 1), and those of their middles
+    const float width = 1.f / depths.scale;
+    const float up = ex2(0.5f * width) * (1.f + 1.f / 65536);
+    const float down = ex2(-0.5f * width) * (1.f - 1.f / 65536);
+    auto bounds = [&](int i, u64 (&b)[3]) {
+        const u32 n = count(i);
+        const float w = ex2((float)(first + i) * -width) * kOne;
+        const u64 l = __float2ull_rd(w * down);
+        b[0] = first + i == kDepthBins - 1 || l == 0 ? 0 : n * (l - 1);
+        b[1] = n * (__float2ull_ru(w * up) + 1);
+        b[2] = n * __float2ull_rn(w);
+    };
+    u32 before_n = 0;
+    u64 sum[3] = {}, all[3] = {};
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         before_n += count(i);
         if (!BY_COUNT) {
-            least += count(i) * depths.least(first + i);
-            most += count(i) * depths.most(first + i);
-            middle += count(i) * depths.middle(first + i);
+            u64 b[3];
+            bounds(i, b);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) sum[q] += b[q];
         }
     }
     // by weight: bounds of what stands before a bin, and an estimate of it
-    const u64 all_least = block_before<G>(sh, before_n, least);
-    u64 all_most = 0, all_middle = 0;
-    if (!BY_COUNT) {
-        all_most = block_before<G>(sh, none, most);
-        all_middle = block_before<G>(sh, none, middle);
-    }
-    i64 low = (i64)(least + base_w), high = (i64)(most + base_w), mid = (i64)(middle + base_w);
+    if (BY_COUNT)
+        block_before<G>(sh, before_n, sum[0]);
+    else
+        block_before<G>(sh, before_n, sum, all);
+    i64 low = (i64)(sum[0] + base_w), high = (i64)(sum[1] + base_w), mid = (i64)(sum[2] + base_w);
     if (at_end) {
-        low = (i64)(base_w - all_most + most);
-        high = (i64)(base_w - all_least + least);
-        mid -= (i64)all_middle;
+        low = (i64)(base_w - all[1] + sum[1]);
+        high = (i64)(base_w - all[0] + sum[0]);
+        mid -= (i64)all[2];
     }
     if (threadIdx.x == 0) {
         sh.at = at_end && high >= (i64)limit ? from : kDepthBins;
@@ -651,9 +678,9 @@ __device__ __forceinline__ void find_bracket(Shared& sh, const DepthBins& depths
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const u32 n = count(i);
-        const i64 l = BY_COUNT ? 0 : n * depths.least(first + i);
-        const i64 h = BY_COUNT ? 0 : n * depths.most(first + i);
-        const i64 m = BY_COUNT ? 0 : n * depths.middle(first + i), want = (i64)limit;
+        u64 b[3] = {};
+        if (!BY_COUNT) bounds(i, b);
+        const i64 l = (i64)b[0], h = (i64)b[1], m = (i64)b[2], want = (i64)limit;
         const i64 to_low = low + (at_end ? h : l), to_high = high + (at_end ? l : h);
         const bool may = BY_COUNT ? bn < k && bn + n >= k : high < want && to_high >= want;
         const bool must = BY_COUNT ? may : low < want && to_low >= want;
@@ -695,7 +722,8 @@ __device__ __forceinline__ void find_bracket(Shared& sh, const DepthBins& depths
             sh.likely = here;
             sh.likely_n = bn;
         }
-        if (here > bin && here <= at_hi && bn <= hi && hi < bn + n && bn + n - likely_upto <= spare) {
+        if (here > bin && here <= at_hi && bn <= hi && hi < bn + n &&
+            bn + n - likely_upto <= spare) {
             sh.likely_hi = here;
             sh.likely_upto = bn + n;
         }
@@ -775,17 +803,20 @@ __device__ __noinline__ Flags find_cut(const SampleArgs& a, const Weigh g, bool 
         });
     }
     const Bins<G> counts = merge_bins(sh, row);
-    find_bracket<BY_COUNT, G>(sh, depths, counts, 0, kDepthBins - 1, 0, 0, false, k, limit);
     if (tid == 0) {
-        sh.own_n = sh.list_n = 0;
         sh.span_hi = 0;
         sh.span_lo = 0xffffffffu;
     }
-    __syncthreads();
-    u64 w = 0;  // the weight before the bins that are looked at
-    u32 n = 0;  // and the entries
+    // the cut is in the bins from `from` to `to`: behind base_n entries, and the weight w is
+    // that before them or, with at_end, up to them
+    int from = 0, to = kDepthBins - 1;
+    u32 base_n = 0, n = 0;  // n: the entries before the bins that are looked at
+    u64 w = 0;
+    bool at_end = false;
     float hi_x = neg_inf(), lo_x = INFINITY;
     for (int turn = 0;; ++turn) {
+        if (tid == 0) sh.own_n = sh.list_n = 0;
+        find_bracket<BY_COUNT, G>(sh, depths, counts, from, to, base_n, w, at_end, k, limit);
         int at = sh.at, at_hi = sh.at_hi;
         n = sh.before_n;
         u32 inside = sh.upto_n - n;
@@ -827,8 +858,8 @@ __device__ __noinline__ Flags find_cut(const SampleArgs& a, const Weigh g, bool 
         w = row_weight(sh, row, lane_w);
         if (at == kDepthBins) return leave(in, w, false);
         if (!listed) break;
-        const bool before = !sure && w >= limit;  // the cut comes before these bins
-        if (!before) {
+        at_end = !sure && w >= limit;  // the cut comes before these bins
+        if (!at_end) {
             const u32 own = sh.own_n;
             send_list(sh, row, own);
             row.sync();
@@ -864,9 +895,9 @@ __device__ __noinline__ Flags find_cut(const SampleArgs& a, const Weigh g, bool 
                         while (ties <= q && (u32)(sh.list[q - ties] >> 32) == key) ++ties;
                         answer = (u64)key << 32 | ties;
                     }
-                    for (int to = 0; to < row.cs; ++to) {
+                    for (int cta = 0; cta < row.cs; ++cta) {
                         if (row.cs > 1) {
-                            const u32 there = map_cluster(smem_u32(sh.answer), to);
+                            const u32 there = map_cluster(smem_u32(sh.answer), cta);
                             st_cluster_b64(there, answer);
                             st_cluster_b64(there + 8, upto);
                         } else {
@@ -890,7 +921,8 @@ __device__ __noinline__ Flags find_cut(const SampleArgs& a, const Weigh g, bool 
                     const int v = ((int)~(u32)e + row.r.head) / E;
                     if (v < row.sl.wlo || v >= row.sl.whi) continue;
                     const u32 key = (u32)(e >> 32);
-                    if (key > out.key) warp_w += Weigh::fixed(Weigh::w(g.depth(Key<T>::value(key))));
+                    if (key > out.key)
+                        warp_w += Weigh::fixed(Weigh::w(g.depth(Key<T>::value(key))));
                     ties += key == out.key;
                 }
                 warp_w = warp_sum(warp_w);
@@ -903,11 +935,10 @@ __device__ __noinline__ Flags find_cut(const SampleArgs& a, const Weigh g, bool 
             }
         }
         // what was found narrows the bins
-        const int from = before ? sh.at : at_hi + 1, to = before ? at - 1 : sh.at_hi;
-        const u32 base_n = before ? sh.before_n : n + inside;
+        from = at_end ? sh.at : at_hi + 1;
+        to = at_end ? at - 1 : sh.at_hi;
+        base_n = at_end ? sh.before_n : n + inside;
         __syncthreads();
-        if (tid == 0) sh.own_n = sh.list_n = 0;
-        find_bracket<BY_COUNT, G>(sh, depths, counts, from, to, base_n, w, before, k, limit);
     }
 
     u32 hi = __reduce_max_sync(0xffffffffu, hi_x >= lo_x ? Key<T>::of(hi_x) : 0);
@@ -1135,8 +1166,9 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Row<T, G>& row, cons
     // The part of the row that holds the token: of the warps' parts, then, by the warps of
     // that CTA, of their 32 vectors at a time, then of a warp's lanes and their entries.
     auto ties_weight = [&](u32 before, u32 n) {
-        return cut.ties == 0 ? 0
-                             : (u64)(min(cut.ties, before + n) - min(cut.ties, before)) * cut.weight;
+        return cut.ties == 0
+                   ? 0
+                   : (u64)(min(cut.ties, before + n) - min(cut.ties, before)) * cut.weight;
     };
     struct Place {  // the parts of a lane, [lo, hi), and what stands before them
         int lo, hi;
