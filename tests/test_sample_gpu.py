@@ -212,6 +212,22 @@ def test_ties_are_kept_by_index(dtype):
         _check(x, u, **s)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("levels,copies,span", [(60, 700, 8.0), (200, 220, 3.0), (24, 1500, 6.0)])
+def test_cuts_among_levels(levels, copies, span, dtype):
+    """Few values, each many times: within the bins of a cut by weight the values are not
+    spread evenly, so that what the bins' middles tell of the cut is often wrong."""
+    rows, V = 24, levels * copies
+    g = torch.Generator().manual_seed(levels)
+    lev = torch.rand((rows, levels), generator=g) * -span
+    at = torch.stack([torch.randperm(V, generator=g) for _ in range(rows)])
+    x = torch.empty((rows, V)).scatter_(1, at, lev.repeat_interleave(copies, dim=1))
+    x = _place(x, torch.bfloat16 if dtype == "bf16" else torch.float32)
+    for i, p in enumerate((0.3, 0.7, 0.95)):
+        _check(x, _u(rows, 40 + i), p=p)
+        _check(x, _u(rows, 50 + i), p=p, k=V // 3, mp=0.01)
+
+
 def test_values_that_crowd_round_zero():
     """fp32 values of every exponent: the bin with the cut spans most of the keys."""
     V = 9001
