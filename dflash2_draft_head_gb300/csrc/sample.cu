@@ -16,7 +16,7 @@
 // The floor is HBM: a row is read once, by one CTA or by the CTAs of a cluster, and passed
 // over two or more times on the chip.  What bounds the kernel is the instructions of
 // those passes: exact weights take 7 an entry.  4096 x 151936 bf16 rows at a temperature
-// take 300 us (4.15 TB/s), their bytes alone 183 us; 483 us for 512 x 262144 fp32 rows cut
+// take 298 us (4.2 TB/s), their bytes alone 183 us; 474 us for 512 x 262144 fp32 rows cut
 // by top_p inside a flat distribution, which makes three passes and counts every entry.
 //
 // The largest entries of the row's groups (of 256 or 128) come first: the largest of them
@@ -49,10 +49,10 @@ using u32 = uint32_t;
 using u64 = unsigned long long;
 
 // Three CTAs of eight warps an SM: with two of sixteen the compiler has 64 registers a
-// thread instead of 80, and 4096 x 151936 bf16 took 371 us instead of 332.  Rows of up to
-// kNarrowBytes take CTAs of four warps, of which an SM holds seven: such a row's time is
-// the latency of the barriers, not of its bytes (4096 x 1000 bf16, temperature alone: 38
-// us, 115 us with sixteen warps; 4096 x 32000, top-k: 124 us, 192).
+// thread instead of 80 (4096 x 151936 bf16, all paths in one kernel: 332 us, 371).  Rows of
+// up to kNarrowBytes take CTAs of four warps, of which an SM holds seven: such a row's time
+// is the latency of the barriers, not of its bytes (4096 x 1000 bf16, temperature alone: 38
+// us, 115 us with sixteen warps; 4096 x 32000, top-k: 97 us, 192).
 using Wide = RowGeometry<256, 3, 6, 320>;
 using Narrow = RowGeometry<128, 7, 4, 320>;
 constexpr long long kNarrowBytes = 64 * 1024;
