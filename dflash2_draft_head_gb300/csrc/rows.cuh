@@ -358,18 +358,19 @@ inline long long row_max_vecs(long long V, size_t es) {
     return (V + 2 * (E - 1)) / E;
 }
 
-// Slices of at most G::kSliceBytes; with few rows smaller ones, so that more SMs take
+// Slices of at most `slice` bytes; with few rows smaller ones, so that more SMs take
 // part, but in clusters of 8 at most (16 x 151936 bf16, top-k: 12 us with 8 CTAs a row,
 // 19 us with 16, whose barriers cost more than the shorter passes save).
 constexpr long long kRowSliceMin = 16 * 1024;
 template <typename G>
-RowSplit split_rows(int rows, int V, size_t es, int num_sms) {
+RowSplit split_rows(int rows, int V, size_t es, int num_sms,
+                    long long slice = G::kSliceBytes) {
     const long long vecs = row_max_vecs(V, es), bytes = vecs * 16;
     int lg = 0;
     while (lg < 3 && (long long)rows << lg < (long long)G::kCtas * num_sms &&
            bytes >> lg > kRowSliceMin)
         ++lg;
-    while (1 << lg < kRowMaxCluster && bytes >> lg > G::kSliceBytes) ++lg;
+    while (1 << lg < kRowMaxCluster && bytes >> lg > slice) ++lg;
     const int per = (int)((vecs + (1 << lg) - 1) >> lg), ring = G::ring_steps(per);
     return {lg, per, ring, ring * G::kStepBytes};
 }

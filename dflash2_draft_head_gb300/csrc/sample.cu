@@ -16,7 +16,7 @@
 // The floor is HBM: a row is read once, by one CTA or by the CTAs of a cluster, and passed
 // over two or more times on the chip.  What bounds the kernel is the instructions of
 // those passes: exact weights take 7 an entry.  4096 x 151936 bf16 rows at a temperature
-// take 298 us (4.2 TB/s), their bytes alone 183 us; 474 us for 512 x 262144 fp32 rows cut
+// take 298 us (4.2 TB/s), their bytes alone 183 us; 432 us for 512 x 262144 fp32 rows cut
 // by top_p inside a flat distribution, which makes three passes and counts every entry.
 //
 // The largest entries of the row's groups (of 256 or 128) come first: the largest of them
@@ -56,6 +56,11 @@ using u64 = unsigned long long;
 using Wide = RowGeometry<256, 3, 6, 320>;
 using Narrow = RowGeometry<128, 7, 4, 320>;
 constexpr long long kNarrowBytes = 64 * 1024;
+// Where top_p, or a top_k beyond the groups, may ask for all passes, the instructions bound
+// them and a cluster's barriers stand between: slices of up to 640 KB (512 x 262144 fp32,
+// top_p: 384 us, 428 with 320 KB).  A temperature or a short list is bound by what misses
+// L2 (the same at a temperature: 158 us, 134).
+constexpr long long kCutSliceBytes = 640 * 1024;
 
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kOne = 1099511627776.f;  // 2^40, the largest entry's weight
@@ -1466,13 +1471,17 @@ cudaError_t launch_typed(SampleArgs a, cudaStream_t stream, int num_sms) {
     // the widest row: kSampleMaxV fp32 entries over the largest cluster
     static_assert(kSampleMaxV / 4 / kRowMaxCluster / Wide::kWarps / 32 < kMaxUnits);
     static_assert(kNarrowBytes / 16 / Narrow::kWarps / 32 < kMaxUnits);
-    const RowSplit p = split_rows<G>(a.rows, a.V, sizeof(T), num_sms);
+    static_assert(kCutSliceBytes / 16 / Wide::kWarps / 32 < kMaxUnits);
+    const bool top_k = a.top_k0 > 0 && a.top_k0 < a.V;
+    const bool passes = a.top_k != nullptr || (top_k ? a.top_k0 > kGroups<G>
+                                                     : a.top_p != nullptr || a.top_p0 < 1.f);
+    const RowSplit p = split_rows<G>(a.rows, a.V, sizeof(T), num_sms,
+                                     passes ? kCutSliceBytes : G::kSliceBytes);
     a.lg = p.lg;
     a.per = p.per;
     a.ring = p.ring;
-    const bool cuts = a.top_k != nullptr || (a.top_k0 > 0 && a.top_k0 < a.V) ||
-                      a.top_p != nullptr || a.top_p0 < 1.f || a.temperature != nullptr ||
-                      !(a.temperature0 > 0.f) || a.min_p != nullptr || a.min_p0 > 1.f;
+    const bool cuts = passes || top_k || a.temperature != nullptr || !(a.temperature0 > 0.f) ||
+                      a.min_p != nullptr || a.min_p0 > 1.f;
     return cuts ? launch_rows<G, sample_kernel<T, G, true>>(a, a.rows, a.lg, p.smem,
                                                             G::kRingBytes, stream)
                 : launch_rows<G, sample_kernel<T, G, false>>(a, a.rows, a.lg, p.smem,
