@@ -16,7 +16,7 @@
 // The floor is HBM: a row is read once, by one CTA or by the CTAs of a cluster, and passed
 // over two or more times on the chip.  What bounds the kernel is the instructions of
 // those passes: exact weights take 7 an entry.  4096 x 151936 bf16 rows at a temperature
-// take 298 us (4.2 TB/s), their bytes alone 183 us; 432 us for 512 x 262144 fp32 rows cut
+// take 298 us (4.2 TB/s), their bytes alone 183 us; 425 us for 512 x 262144 fp32 rows cut
 // by top_p inside a flat distribution, which makes three passes and counts every entry.
 //
 // The largest entries of the row's groups (of 256 or 128) come first: the largest of them
@@ -58,7 +58,7 @@ using Narrow = RowGeometry<128, 7, 4, 320>;
 constexpr long long kNarrowBytes = 64 * 1024;
 // Where top_p, or a top_k beyond the groups, may ask for all passes, the instructions bound
 // them and a cluster's barriers stand between: slices of up to 640 KB (512 x 262144 fp32,
-// top_p: 384 us, 428 with 320 KB).  A temperature or a short list is bound by what misses
+// top_p: 383 us, 428 with 320 KB).  A temperature or a short list is bound by what misses
 // L2 (the same at a temperature: 158 us, 134).
 constexpr long long kCutSliceBytes = 640 * 1024;
 
@@ -848,6 +848,8 @@ __device__ __noinline__ Flags find_cut(const SampleArgs& a, const Weigh g, bool 
                 lo_x = fminf(lo_x, x);
             }
         };
+        // the row's last pass, most often (512 x 262144 fp32, top_p and min_p: 425 us, 432)
+        row.sl.hint = l2_policy_evict_first();
         row.each_pair(g, plain, [&](int index, float2 x, float2 d) {
             const float wx = ex2(d.x), wy = ex2(d.y);
             const bool above_x = d.x > edge, above_y = d.y > edge;
