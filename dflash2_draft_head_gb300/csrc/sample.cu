@@ -842,7 +842,8 @@ __device__ __noinline__ Flags find_cut(const SampleArgs& a, const Weigh g, bool 
         auto look = [&](int index, float x, float d) {
             if (d > edge || !(d > end) || (INSIDE && !(x >= least))) return;
             if (listed) {
-                sh.own_list[atomicAdd(&sh.own_n, 1u)] = entry_of<T>(x, index);
+                const u32 place = atomicAdd(&sh.own_n, 1u);  // below `inside`, by the counts
+                if (place < kListMax) sh.own_list[place] = entry_of<T>(x, index);
             } else {
                 hi_x = fmaxf(hi_x, x);
                 lo_x = fminf(lo_x, x);
@@ -867,7 +868,7 @@ __device__ __noinline__ Flags find_cut(const SampleArgs& a, const Weigh g, bool 
         if (!listed) break;
         at_end = !sure && w >= limit;  // the cut comes before these bins
         if (!at_end) {
-            const u32 own = sh.own_n;
+            const u32 own = min(sh.own_n, (u32)kListMax);
             send_list(sh, row, own);
             row.sync();
             if (row.rank == 0) {
