@@ -316,7 +316,9 @@ __device__ __forceinline__ void block_sum(Shared& sh, u32& n, u64& w) {
     }
 }
 
-// Sums of weights over the whole row; every thread gets them.
+// Sums of weights over the whole row; every thread gets them.  Between two calls a
+// row.sync() has to stand, behind this one's reads: the next one's stores into the other
+// CTAs' cta_w come before its own.
 template <typename R>
 __device__ __forceinline__ u64 row_weight(Shared& sh, const R& row, u64 w) {
     u32 none = 0;
@@ -946,7 +948,10 @@ __device__ __noinline__ Flags find_cut(const SampleArgs& a, const Weigh g, bool 
         from = at_end ? sh.at : at_hi + 1;
         to = at_end ? at - 1 : sh.at_hi;
         base_n = at_end ? sh.before_n : n + inside;
-        __syncthreads();
+        if (at_end)
+            row.sync();  // of this turn's sums: no list has been sent, whose syncs stand behind them
+        else
+            __syncthreads();
     }
 
     u32 hi = __reduce_max_sync(0xffffffffu, hi_x >= lo_x ? Key<T>::of(hi_x) : 0);
