@@ -263,8 +263,9 @@ struct Row {
     __device__ __forceinline__ void each_vec(F f) {
         sl.pass(r, [&](int v, const uint4& vec, bool) { f(v, vec); });
     }
-    // f(index, entries, their depths), two at a time.  `plain`: no NaN among them and a
-    // finite maximum; else a NaN has the depth of -inf
+    // f(index, entries, their depths), two at a time.  `plain`: no NaN among them, a finite
+    // maximum and a factor that is neither 0 nor infinite, so that no product is a NaN; else
+    // a NaN has the depth of -inf
     template <typename F>
     __device__ __forceinline__ void each_pair(const Weigh& g, bool plain, F f) {
         const f32x2 nm = pair(-g.m, -g.m), c = pair(g.c, g.c);
@@ -1147,7 +1148,7 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Row<T, G>& row, cons
             if (key > cut.key)
                 w += Weigh::fixed(wj);
             else
-                ties += Weigh::fixed(wj) != 0;
+                ++ties;
         }
     };
     u64 sw = 0;
@@ -1272,10 +1273,10 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Row<T, G>& row, cons
     for (int j = 0; j < E; ++j) {
         const u32 key = Key<T>::of(x[j]);
         const float wj = Weigh::w(g.depth(x[j]));
-        u64 w = wj < min_p ? 0 : Weigh::fixed(wj);
-        if (key < cut.key) {
+        u64 w = Weigh::fixed(wj);
+        if (key < cut.key || wj < min_p) {
             w = 0;
-        } else if (key == cut.key && w != 0) {
+        } else if (key == cut.key) {
             w = ties_weight(tie, 1);
             ++tie;
         }
@@ -1385,8 +1386,11 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
         }
         return;
     }
-    const Weigh g{m, __fdiv_rn(kLog2e, T0 > 0.f ? T0 : 1.f)};
-    const bool plain = !has_nan && m < INFINITY;
+    // c is +inf below T = 4.3e-39, and 0 at T = +inf: there 0 stands for a finite maximum, so
+    // that no x - m leaves fp32's range and all finite entries have the depth 0
+    const float c = __fdiv_rn(kLog2e, T0 > 0.f ? T0 : 1.f);
+    const Weigh g{c == 0.f && m < INFINITY ? 0.f : m, c};
+    const bool plain = !has_nan && m < INFINITY && g.c > 0.f && g.c < INFINITY;
 
     u64 all = 0, limit = ~0ull;  // (without top_k) the row's weight and top_p's part of it
     float deepest = -kDepth;     // of the counts

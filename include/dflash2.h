@@ -330,11 +330,11 @@ int dflash2_chain(const int32_t* cand_ids, const float* unary, const float* edge
  *   prob  = W_token / S
  * Sums of whole numbers are exact, so the token does not depend on the number of
  * rows or on how a row is split over the GPU.  T <= 0 (or NaN): the largest entry
- * (lowest index).  top_k <= 0 or >= V, top_p >= 1 (or NaN), min_p <= 0 (or NaN): no
- * such limit; top_p <= 0 or min_p > 1: the first entry alone.  A row whose maximum is
- * +inf samples among its +inf entries.  A row with no entry above -inf gives token -1
- * and prob 0.  uniform is in [0, 1); a value outside is taken to the nearer end, NaN
- * to 0.
+ * (lowest index).  T = +inf: every finite entry weighs the same.  top_k <= 0 or
+ * >= V, top_p >= 1 (or NaN), min_p <= 0 (or NaN): no such limit; top_p <= 0 or
+ * min_p > 1: the first entry alone.  A row whose maximum is +inf samples among its +inf
+ * entries.  A row with no entry above -inf gives token -1 and prob 0.  uniform is in
+ * [0, 1); a value outside is taken to the nearer end, NaN to 0.
  *   logits  [rows,V] in_dtype, element (r, j) at r * ld + j, ld >= V; any start
  *           aligned to an element
  *   uniform [rows] fp32
