@@ -17,8 +17,8 @@
 // sum is taken against its own rounded base b = c * max, 2^(c*z - b) being one
 // fused multiply-add and one ex2, and the same b goes into lse, so the rounding
 // of b cancels.  The loss takes c * z - b the same way (in 64 bits, K terms).
-// Where c * max leaves fp32's range (a row masked by the type's lowest value all
-// over) the power is 2^((z - max) * c).
+// Where c * max is 2^24 or more (a row masked by a large number or the type's lowest value
+// all over) the power is 2^((z - max) * c).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -117,8 +117,10 @@ __device__ __forceinline__ float teacher_softmax(const Teacher& t, int K, float 
 }
 
 // 2^(c * z - base), base = c * max: rounded to fp32 and by a fused multiply-add, or
-// with the maximum taken off first where the base is too large for that.
-constexpr float kFastBase = 1e38f;
+// with the maximum taken off first where the base is too large for that: the multiply-add
+// leaves the base's rounding error in all exponents, which is half at most below 2^24, but
+// leaves fp32's range for bases from 2^31 on (a row masked by -1e10 all over).
+constexpr float kFastBase = 16777216.f;
 struct Power {
     bool fast;
     float c, m, nb;  // the maximum (0 for -inf: every z is), -base
@@ -138,9 +140,10 @@ struct Power {
             z[j] = pair(ex2(d.x), ex2(d.y));
         }
     }
-    // 2^(another's base - base)
+    // 2^(another's base - base); a base that is not fast is the product itself, not rounded
     __device__ __forceinline__ float against(const Power& o) const {
-        return ex2(fast ? nb - o.nb : (o.m - m) * c);
+        if (fast) return ex2(o.fast ? nb - o.nb : fmaf(o.m, c, nb));
+        return ex2(o.fast ? -fmaf(m, c, o.nb) : (o.m - m) * c);
     }
     __device__ __forceinline__ double base() const { return fast ? -(double)nb : (double)m * c; }
     // c * z - base in 64 bits
