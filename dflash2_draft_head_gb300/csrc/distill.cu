@@ -257,41 +257,25 @@ __device__ __forceinline__ MaxSum join(const MaxSum* ms, int n, float c) {
     return {m, warp_sum(s)};
 }
 
-// One cluster per row: lse and loss, and the gradient when GRAD.
-template <typename T, bool GRAD, typename G>
-__global__ void __launch_bounds__(G::kThreads, G::kCtas) distill_kernel(DistillArgs a) {
+// A row by its cluster: lse and loss when LOSS, and the gradient, times `up`, when GRAD.
+template <typename T, bool LOSS, bool GRAD, typename G>
+__device__ __forceinline__ void whole_row(const DistillArgs& a, const RowView<T>& r,
+                                          RowSlice<G>& sl, char* smem, int row, int rank, T* out,
+                                          bool on_grid, float weight, float up) {
     constexpr int E = VecOf<T>::kElems;
-    extern __shared__ __align__(16) char smem[];
     __shared__ MaxSum parts[kRowMaxCluster * G::kWarps];  // every warp of the row
     __shared__ float has_teacher;                         // 1 or 0
 
     const int cs = 1 << a.lg, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = cs > 1 ? (int)cluster_ctarank() : 0;
-    const int row = blockIdx.x >> a.lg;
-    const RowView<T> r(a.logits, a.ld, row, a.V);
-    RowSlice<G> sl(r, a.per, a.ring, rank, warp, smem + (size_t)a.K * 16,
-                   GRAD ? l2_policy_evict_last() : l2_policy_evict_first());
     const int e_lo = max(sl.lo * E - r.head, 0), e_hi = min(sl.hi * E - r.head, a.V);
-    T* out = GRAD ? static_cast<T*>(a.grad) + (long long)row * a.grad_ld : nullptr;
-    const bool on_grid =
-        GRAD &&
-        ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(r.row)) & 15u) == 0;
-    const float weight = a.weight != nullptr ? a.weight[row] : 1.f;
-    if (weight == 0.f) {  // the whole cluster leaves: the row's logits are not read
-        if (GRAD) store_zeros<T>(r, out, on_grid, sl.wlo, sl.whi);
-        if (rank == 0 && tid == 0) {
-            a.loss[row] = 0.f;
-            a.lse[row] = 0.f;
-        }
-        return;
-    }
     if (cs > 1) cluster_arrive();  // met by cluster_wait below: every CTA has started
 
     sl.start(r);
     const Teacher t(smem, a.K);
     // rank 0, which makes the loss, needs z at all of the teacher's tokens
     if (warp == G::kWarps - 1)
-        teacher_load(t, a, row, r.row, rank == 0 ? 0 : e_lo, rank == 0 ? a.V : e_hi, rank == 0);
+        teacher_load(t, a, row, r.row, LOSS && rank == 0 ? 0 : e_lo,
+                     LOSS && rank == 0 ? a.V : e_hi, rank == 0);
     // The warp's sum of powers against the largest logit of its first vectors: fp32 has
     // room for sums 2^66 times above that.  Where one was larger (or the base was -inf,
     // or a NaN is among them), once more against the largest of all.
@@ -347,7 +331,7 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas) distill_kernel(DistillA
     const MaxSum all = join(parts, cs * G::kWarps, a.c);
     const Power pg(all.max, a.c);
     const float S = all.sum;
-    if (rank == 0 && warp == G::kWarps - 1) {
+    if (LOSS && rank == 0 && warp == G::kWarps - 1) {
         const float ls = log2f(S);
         double loss = 0;
         for (int k = lane; k < a.K; k += 32)
@@ -363,7 +347,7 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas) distill_kernel(DistillA
     }
     if (GRAD) {
         // without a teacher the whole gradient is 0
-        const float scale = weight * a.inv_t;
+        const float scale = up * weight * a.inv_t;
         const float per_s = S == 0.f || has_teacher == 0.f ? 0.f : 1.f / S;
         const float k = scale * per_s;
         sl.hint = l2_policy_evict_first();
@@ -391,10 +375,53 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas) distill_kernel(DistillA
     }
 }
 
-// The gradient alone, from lse and the upstream gradient: the CTAs of a row do not
-// wait on one another.
+// One cluster per row: lse and loss, and the gradient when GRAD.
+template <typename T, bool GRAD, typename G>
+__global__ void __launch_bounds__(G::kThreads, G::kCtas) distill_kernel(DistillArgs a) {
+    extern __shared__ __align__(16) char smem[];
+    const int tid = threadIdx.x, rank = a.lg > 0 ? (int)cluster_ctarank() : 0;
+    const int row = blockIdx.x >> a.lg;
+    const RowView<T> r(a.logits, a.ld, row, a.V);
+    RowSlice<G> sl(r, a.per, a.ring, rank, tid >> 5, smem + (size_t)a.K * 16,
+                   GRAD ? l2_policy_evict_last() : l2_policy_evict_first());
+    T* out = GRAD ? static_cast<T*>(a.grad) + (long long)row * a.grad_ld : nullptr;
+    const bool on_grid =
+        GRAD &&
+        ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(r.row)) & 15u) == 0;
+    const float weight = a.weight != nullptr ? a.weight[row] : 1.f;
+    if (weight == 0.f) {  // the whole cluster leaves: the row's logits are not read
+        if (GRAD) store_zeros<T>(r, out, on_grid, sl.wlo, sl.whi);
+        if (rank == 0 && tid == 0) {
+            a.loss[row] = 0.f;
+            a.lse[row] = 0.f;
+        }
+        return;
+    }
+    whole_row<T, true, GRAD, G>(a, r, sl, smem, row, rank, out, on_grid, weight, 1.f);
+}
+
+// The gradient alone of a row whose lse is far from 0: its sum is taken again.  A call, so
+// that other rows keep their registers.
 template <typename T, typename G>
-__global__ void __launch_bounds__(G::kThreads, G::kCtas) distill_grad_kernel(DistillArgs a) {
+__device__ __noinline__ void far_row(const DistillArgs& a, char* smem, float weight, float up) {
+    const int row = blockIdx.x >> a.lg, rank = a.lg > 0 ? (int)cluster_ctarank() : 0;
+    const RowView<T> r(a.logits, a.ld, row, a.V);
+    RowSlice<G> sl(r, a.per, a.ring, rank, threadIdx.x >> 5, smem + (size_t)a.K * 16,
+                   l2_policy_evict_last());
+    T* out = static_cast<T*>(a.grad) + (long long)row * a.grad_ld;
+    const bool on_grid =
+        ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(r.row)) & 15u) == 0;
+    whole_row<T, false, true, G>(a, r, sl, smem, row, rank, out, on_grid, weight, up);
+}
+
+// The gradient alone, from lse and the upstream gradient: the CTAs of a row do not
+// wait on one another, unless |lse| is kFarLse or more.  exp(z / T - lse) is off by half a unit
+// of lse, 2^-17 below 256; at 1e4 it is 5e-4, and a row masked by the type's lowest value all
+// over has an lse that holds nothing of its sum (or none in fp32's range, with T < 1).
+constexpr float kFarLse = 256.f;
+template <typename T, typename G>
+__global__ void __launch_bounds__(G::kThreads, G::kCtas)
+    distill_grad_kernel(const __grid_constant__ DistillArgs a) {
     constexpr int E = VecOf<T>::kElems;
     extern __shared__ __align__(16) char smem[];
     __shared__ float has_teacher;
@@ -413,6 +440,11 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas) distill_grad_kernel(Dis
         store_zeros<T>(r, out, on_grid, sl.wlo, sl.whi);
         return;
     }
+    const float lse = a.lse[row];
+    if (fabsf(lse) >= kFarLse) {  // the same in all CTAs of the row
+        far_row<T, G>(a, smem, weight, up);
+        return;
+    }
     sl.start(r);
     const Teacher t(smem, a.K);
     if (warp == 0) {
@@ -422,12 +454,9 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas) distill_grad_kernel(Dis
     }
     __syncthreads();  // also: z is read before the gradient may take its place
     const float scale = up * weight * a.inv_t;
-    const float lse = a.lse[row];
     const bool none = has_teacher == 0.f;
-    auto share = [&](float z) {
-        return lse == neg_inf() ? 0.f : ex2(fmaf(z, a.inv_t, -lse) * kLog2e);
-    };
-    const float k = none || lse == neg_inf() ? 0.f : scale;
+    auto share = [&](float z) { return ex2(fmaf(z, a.inv_t, -lse) * kLog2e); };
+    const float k = none ? 0.f : scale;
     const f32x2 it = pair(a.inv_t, a.inv_t), nl = pair(-lse, -lse), le = pair(kLog2e, kLog2e);
     sl.pass(r, [&](int v, const uint4& vec, bool whole) {
         f32x2 f[E / 2];

@@ -393,6 +393,8 @@ int dflash2_distill(const void* logits, long long ld, const int32_t* teacher_ids
  * The gradient of dflash2_distill alone, for an upstream gradient known only after the
  * loss:  grad_j = grad_loss[r] * weight[r] * (exp(z_j / T - lse[r]) - sum q) / T.
  *   grad_loss [rows] fp32; lse [rows] as dflash2_distill wrote it; the rest as there.
+ *           Where |lse| is 256 or more, or infinite, its fp32 rounding would show in the
+ *           gradient: the row's sum is taken again from the logits
  * A row with grad_loss or weight 0 is not read and its gradient is 0.
  */
 int dflash2_distill_backward(const float* grad_loss, const void* logits, long long ld,
