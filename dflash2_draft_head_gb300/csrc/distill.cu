@@ -346,9 +346,12 @@ __device__ __forceinline__ void whole_row(const DistillArgs& a, const RowView<T>
         }
     }
     if (GRAD) {
-        // without a teacher the whole gradient is 0
+        if (has_teacher == 0.f) {  // whatever the logits are, a NaN too
+            store_zeros<T>(r, out, on_grid, sl.wlo, sl.whi);
+            return;
+        }
         const float scale = up * weight * a.inv_t;
-        const float per_s = S == 0.f || has_teacher == 0.f ? 0.f : 1.f / S;
+        const float per_s = S == 0.f ? 0.f : 1.f / S;
         const float k = scale * per_s;
         sl.hint = l2_policy_evict_first();
         if (pg.fast && on_grid) {
@@ -369,7 +372,6 @@ __device__ __forceinline__ void whole_row(const DistillArgs& a, const RowView<T>
                 store_vec<T>(r, out, whole && on_grid, v, sl.whi, slow_grad<T>(vec, pg, k));
             });
         }
-        if (has_teacher == 0.f) return;
         __syncthreads();
         fix_tokens<G, T>(t, a.K, out, e_lo, e_hi, scale, [&](float z) { return pg(z) * per_s; });
     }

@@ -375,10 +375,11 @@ int dflash2_sample(const void* logits, long long ld, const float* uniform,
  *           bytes, single elements otherwise
  *   err_flag one device int32 or NULL: DF2_FLAG_BAD_ID when an id is >= V (an empty slot)
  * A row with weight 0 is not read: its loss, lse and gradient are 0.  A row whose slots
- * are all empty or -inf has loss and gradient 0.  A token at -inf in z with q > 0 makes the
- * loss +inf, the gradient stays finite; a row with no z above -inf counts as a softmax
- * that is 0 everywhere (lse -inf).  NaN or +inf in a row's z or teacher logits makes its
- * outputs NaN.  All sums are in fp32 or more.  rows == 0 launches nothing.
+ * are all empty or -inf has loss and gradient 0, whatever its z are.  A token at -inf in z
+ * with q > 0 makes the loss +inf, the gradient stays finite; a row with no z above -inf counts
+ * as a softmax that is 0 everywhere (lse -inf).  Apart from those, NaN or +inf in a row's z or
+ * teacher logits makes its outputs NaN.  All sums are in fp32 or more.  rows == 0 launches
+ * nothing.
  * INVALID_ARG: rows < 0; V or K <= 0; ld or grad_ld < V; a temperature that is not
  * positive and finite; NULL required pointer; misalignment (vectors of one or K values
  * per row: 4 bytes); an output overlapping another buffer, other than grad in place.
