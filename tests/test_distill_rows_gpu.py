@@ -1,9 +1,11 @@
-"""More of the distillation loss: rows without a teacher whose logits are not finite."""
+"""More of the distillation loss: rows without a teacher whose logits are not finite, and
+one row in batches that split it in different ways."""
+import numpy as np
 import pytest
 import torch
 
 import dflash2_draft_head_gb300 as df2
-from test_distill_gpu import INF, NAN, _built, _inputs  # noqa: F401
+from test_distill_gpu import INF, NAN, _bounds, _built, _formula, _inputs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +33,21 @@ def test_no_teacher_hides_what_is_not_finite(V, dtype):
     other = torch.full((5 * V + 9,), NAN, dtype=z.dtype, device="cuda")[5:5 + 5 * V].view(5, V)
     assert torch.equal(df2.distill(z, ids, y, grad=other)[2], grad)
     assert torch.equal(df2.distill(z, ids, y, grad=z)[2], grad)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [3000, 151936])
+def test_a_row_in_batches_of_other_sizes(V, dtype):
+    """The number of rows decides how a row is split, and with it the order of its fp32 sums:
+    each result is inside its bound, and a batch's rows are the same bits."""
+    z, ids, y = _inputs(1, V, 32, dtype, 12)
+    rl, rs, rg = _formula(z[0], ids[0], y[0], 1.0, 1.0)
+    lb, ob, gb = _bounds(z[0], y[0], 1.0, rs)
+    rnd = 2.0 ** -8 * np.abs(rg) if dtype == "bf16" else 0
+    for rows in (1, 64, 640, 1300):
+        loss, lse, grad = df2.distill(z.expand(rows, V).contiguous(), ids.expand(rows, 32).contiguous(),
+                                      y.expand(rows, 32).contiguous(), grad=True)
+        for t in (loss, lse, grad):
+            assert (t == t[:1]).all()
+        assert abs(lse[0].item() - rs) <= lb and abs(loss[0].item() - rl) <= ob + 2.0 ** -23 * abs(rl)
+        assert (np.abs(grad[0].double().cpu().numpy() - rg) <= gb + rnd).all()
