@@ -12,6 +12,7 @@ import os
 import threading
 
 import torch
+from torch.autograd.graph import increment_version  # for what autograd may have saved
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdflash2.so")
@@ -435,13 +436,15 @@ def distill(logits, teacher_ids, teacher_logits, temperature=1.0, weight=None, g
     (loss [...] fp32, lse [...] fp32, grad): loss[r] = weight[r] * KL(teacher's
     softmax over its K || student), lse for distill_backward, and with grad=True (or
     a tensor to write, which may be logits) the gradient of the sum of the losses;
-    else None."""
+    else None.  The results carry no autograd graph, also where logits do: hand the
+    gradient on by logits.backward(grad)."""
     shape, rows, V, ld = _logit_rows(logits, "logits")
     K, ids_ptr, teacher_ptr, weight_ptr = _teacher(teacher_ids, teacher_logits, weight, shape)
     dev = logits.device
     loss, loss_ptr = _out_rows(loss, "loss", torch.float32, shape, dev, weight)
     lse, lse_ptr = _out_rows(lse, "lse", torch.float32, shape, dev, loss)
     _need(err_flag, "err_flag", torch.int32)
+    given = isinstance(grad, torch.Tensor)
     if grad is None or grad is False:
         grad, grad_ptr, grad_ld = None, None, 0
     else:
@@ -452,6 +455,8 @@ def distill(logits, teacher_ids, teacher_logits, temperature=1.0, weight=None, g
                                _raw_stream(dev.index))
     if st != DF2_OK:
         _check(st)
+    if given:
+        increment_version(grad)
     return loss, lse, grad
 
 
@@ -459,12 +464,13 @@ def distill_backward(grad_loss, logits, teacher_ids, teacher_logits, lse, temper
                      weight=None, grad=True, err_flag=None):
     """The gradient of distill() by its logits alone, from the gradient by its losses,
     grad_loss [...] fp32, and the lse [...] that it returned.  grad may be a tensor to
-    write (also logits)."""
+    write (also logits).  It carries no autograd graph."""
     shape, rows, V, ld = _logit_rows(logits, "logits")
     K, ids_ptr, teacher_ptr, weight_ptr = _teacher(teacher_ids, teacher_logits, weight, shape)
     up = _need_rows(grad_loss, "grad_loss", torch.float32, shape)
     lse_ptr = _need_rows(lse, "lse", torch.float32, shape)
     _need(err_flag, "err_flag", torch.int32)
+    given = isinstance(grad, torch.Tensor)
     grad, grad_ptr, grad_ld = _grad_rows(grad, logits, ld)
     st = lib().dflash2_distill_backward(up, logits.data_ptr(), ld, ids_ptr, teacher_ptr,
                                         weight_ptr, lse_ptr, rows, V, K, temperature,
@@ -473,6 +479,8 @@ def distill_backward(grad_loss, logits, teacher_ids, teacher_logits, lse, temper
                                         _raw_stream(logits.device.index))
     if st != DF2_OK:
         _check(st)
+    if given:
+        increment_version(grad)
     return grad
 
 
