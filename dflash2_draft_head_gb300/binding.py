@@ -109,8 +109,10 @@ def _stream(dev) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
-# The current stream's handle without a Stream object around it (2 us a call).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _raw_stream(index: int) -> int:
+    """The current stream's handle without a Stream object around it (2 us a call).  Looked
+    up at the call: a torch without CUDA has no such function."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _code(dt: torch.dtype) -> int:
