@@ -341,6 +341,8 @@ def _logit_rows(t, name):
         ld, unit = t.stride()
         if (unit == 1 or V <= 1) and ld >= V:
             return shape[:1], shape[0], V, ld
+    if 0 in shape[:-1]:  # the strides of a tensor without elements say nothing
+        return shape[:-1], 0, V, max(V, 1)
     strides = t.stride()
     if V > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must have its last dimension contiguous")

@@ -1,7 +1,14 @@
-"""The Python binding of the operators on vocabulary rows, as far as it goes without a GPU."""
+"""The Python binding of the operators on vocabulary rows, as far as it goes without a GPU:
+what it needs of torch when it is imported, and the row layouts that it takes."""
 import os
 import subprocess
 import sys
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from dflash2_draft_head_gb300 import binding
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -15,3 +22,28 @@ def test_import_on_a_torch_without_cuda():
             "assert df2.sample and df2.distill and df2.topk\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def _fake(shape, stride):
+    return SimpleNamespace(is_cuda=True, shape=torch.Size(shape), stride=lambda: stride)
+
+
+@pytest.mark.parametrize("shape", [(0, 8), (5, 0, 8), (0, 5, 8), (5, 0, 3, 8), (2, 3, 0, 8), (0, 0, 8)])
+def test_no_rows_in_any_leading_dimension(shape):
+    t = torch.empty(shape)
+    lead, rows, V, ld = binding._logit_rows(_fake(shape, t.stride()), "logits")
+    assert (tuple(lead), rows, V) == (shape[:-1], 0, 8) and ld >= 8
+
+
+@pytest.mark.parametrize("shape,stride,want", [
+    ((4, 100), (104, 1), (4, 100, 104)), ((2, 3, 100), (312, 104, 1), (6, 100, 104)),
+    ((1, 100), (7, 1), (1, 100, 100)), ((2, 1, 100), (104, 5, 1), (2, 100, 104)),
+    ((100,), (1,), (1, 100, 100)),
+])
+def test_evenly_spaced_rows(shape, stride, want):
+    assert binding._logit_rows(_fake(shape, stride), "logits")[1:] == want
+
+
+def test_uneven_rows_are_refused():
+    with pytest.raises(ValueError):
+        binding._logit_rows(_fake((2, 3, 100), (400, 104, 1)), "logits")
