@@ -396,6 +396,7 @@ def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, toke
     up = _need_rows(uniform, "uniform", torch.float32, shape)
     tp, t0 = _setting(temperature, "temperature", torch.float32, shape)
     kp, k0 = _setting(top_k, "top_k", torch.int32, shape)
+    k0 = max(-1, min(k0, 0x7fffffff))  # the entry takes 32 bits; both ends are no limit
     pp, p0 = _setting(top_p, "top_p", torch.float32, shape)
     mp, m0 = _setting(min_p, "min_p", torch.float32, shape)
     dev = logits.device

@@ -1,5 +1,6 @@
 """The Python binding of the operators on vocabulary rows, as far as it goes without a GPU:
 what it needs of torch when it is imported, and the row layouts that it takes."""
+import ctypes
 import os
 import subprocess
 import sys
@@ -47,3 +48,37 @@ def test_evenly_spaced_rows(shape, stride, want):
 def test_uneven_rows_are_refused():
     with pytest.raises(ValueError):
         binding._logit_rows(_fake((2, 3, 100), (400, 104, 1)), "logits")
+
+
+class _Tensor(SimpleNamespace):
+    """As much of a CUDA tensor as sample() looks at."""
+
+    def data_ptr(self):
+        return 1 << 20
+
+    def is_contiguous(self):
+        return True
+
+
+@pytest.mark.parametrize("top_k,limit", [
+    (0, None), (-1, None), (5, 5), (2 ** 21 - 1, 2 ** 21 - 1), (2 ** 31 - 1, None), (2 ** 31, None),
+    (2 ** 32 + 5, None), (sys.maxsize, None), (-2 ** 32 + 5, None),
+])
+def test_a_top_k_beyond_32_bits_is_no_limit(monkeypatch, top_k, limit):
+    """The C entry takes 32 bits: a number beyond them must not come out as a small one.  No
+    row has more than 2^21 entries."""
+    got = []
+
+    def entry(*args):
+        got.append(ctypes.c_int(args[8]).value)
+        return 0
+
+    rows, dev = torch.Size((2,)), SimpleNamespace(index=0)
+    x = _Tensor(is_cuda=True, dtype=torch.float32, shape=torch.Size((2, 8)), stride=lambda: (8, 1),
+                device=dev)
+    u = _Tensor(is_cuda=True, dtype=torch.float32, shape=rows, device=dev)
+    tok = _Tensor(is_cuda=True, dtype=torch.int32, shape=rows, device=dev)
+    monkeypatch.setattr(binding, "lib", lambda: SimpleNamespace(dflash2_sample=entry))
+    monkeypatch.setattr(binding, "_raw_stream", lambda i: 0)
+    binding.sample(x, u, top_k=top_k, tokens=tok, probs=u)
+    assert (got[0] if 0 < got[0] < 2 ** 21 else None) == limit
