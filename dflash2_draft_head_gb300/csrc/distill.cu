@@ -402,8 +402,9 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas) distill_kernel(DistillA
     whole_row<T, true, GRAD, G>(a, r, sl, smem, row, rank, out, on_grid, weight, 1.f);
 }
 
-// The gradient alone of a row whose lse is far from 0: its sum is taken again.  A call, so
-// that other rows keep their registers.
+// The gradient alone of a row whose lse is far from 0: its sum is taken again (1024 x 151936
+// bf16 from HBM, all rows so: 142 us, 108 with the given lse).  A call, so that other rows keep
+// their registers.
 template <typename T, typename G>
 __device__ __noinline__ void far_row(const DistillArgs& a, char* smem, float weight, float up) {
     const int row = blockIdx.x >> a.lg, rank = a.lg > 0 ? (int)cluster_ctarank() : 0;
