@@ -419,8 +419,9 @@ __device__ __noinline__ void far_row(const DistillArgs& a, char* smem, float wei
 
 // The gradient alone, from lse and the upstream gradient: the CTAs of a row do not
 // wait on one another, unless |lse| is kFarLse or more.  exp(z / T - lse) is off by half a unit
-// of lse, 2^-17 below 256; at 1e4 it is 5e-4, and a row masked by the type's lowest value all
-// over has an lse that holds nothing of its sum (or none in fp32's range, with T < 1).
+// of lse, 2^-17 below 256, and by the rounding of log2(e) / T behind lse, 2^-16 there at most; at
+// 1e4 the first is 5e-4, and a row masked by the type's lowest value all over has an lse that
+// holds nothing of its sum (or none in fp32's range, with T < 1).
 constexpr float kFarLse = 256.f;
 template <typename T, typename G>
 __global__ void __launch_bounds__(G::kThreads, G::kCtas)
