@@ -10,11 +10,15 @@ ggml-org/llama.cpp PR #27342, "spec : add DFlash2 support (local convolution
 + candidate selector)".  Next to it stand two operators on the vocabulary rows
 that the top-K reads: sampling with temperature, top-k, top-p and min-p (the
 verification of a draft), and the distillation loss against a teacher's top
-logits with its gradient (the training of a draft head).  This package is the
-thin Python binding over it.
+logits with its gradient (the training of a draft head); and what a draft head's
+training needs behind that: the clipped policy loss and the preference loss on
+such rows, the gradients' norm, and AdamW over many tensors with states in 32 or
+8 bits.  This package is the thin Python binding over it.
 """
-from .binding import (Dflash2Error, chain, distill, distill_backward, dynconv,  # noqa: F401
-                      dynconv_predicted, edges, lib, predict_delta, probe_gather, project,
-                      project_noalloc, project_workspace_bytes, sample, select, select_plan,
-                      take_device_faults, topk, version)
+from .binding import (Dflash2Error, adamw, chain, distill, distill_backward, dynconv,  # noqa: F401
+                      dynconv_predicted, edges, grad_norm, lib, policy_loss,
+                      policy_loss_backward, predict_delta, preference_loss,
+                      preference_loss_backward, probe_gather, project, project_noalloc,
+                      project_workspace_bytes, sample, select, select_plan, state_decode,
+                      state_encode, take_device_faults, topk, version)
 from .build import build as build_library  # noqa: F401

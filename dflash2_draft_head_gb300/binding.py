@@ -8,6 +8,7 @@ fallback: if the library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 
@@ -84,6 +85,30 @@ def lib() -> ctypes.CDLL:
             L.dflash2_distill_backward.argtypes = [vp, vp, ll, vp, vp, vp, vp, i, i, i, f, i, vp,
                                                    ll, vp, vp]
             L.dflash2_distill_backward.restype = i
+            d = ctypes.c_double
+            L.dflash2_policy_loss.argtypes = [vp, ll, vp, vp, vp, vp, vp, i, i, f, f, f, f, i, vp,
+                                              vp, vp, vp, ll, vp, vp]
+            L.dflash2_policy_loss.restype = i
+            L.dflash2_policy_loss_backward.argtypes = [vp, vp, ll, vp, vp, vp, vp, vp, vp, vp, i,
+                                                       i, f, f, f, f, i, vp, ll, vp, vp]
+            L.dflash2_policy_loss_backward.restype = i
+            L.dflash2_preference_loss.argtypes = [vp, ll, vp, vp, vp, vp, i, i, i, f, f, f, i, i,
+                                                  vp, vp, vp, vp, vp, ll, vp, vp]
+            L.dflash2_preference_loss.restype = i
+            L.dflash2_preference_loss_backward.argtypes = [vp, vp, ll, vp, vp, vp, vp, vp, vp, i,
+                                                           i, i, f, f, f, i, i, vp, ll, vp, vp]
+            L.dflash2_preference_loss_backward.restype = i
+            L.dflash2_grad_norm_workspace_bytes.argtypes = [i, vp]
+            L.dflash2_grad_norm_workspace_bytes.restype = ctypes.c_size_t
+            L.dflash2_grad_norm.argtypes = [i, vp, vp, i, vp, ctypes.c_size_t, vp, vp]
+            L.dflash2_grad_norm.restype = i
+            L.dflash2_adamw.argtypes = [i, vp, vp, vp, vp, vp, vp, vp, vp, i, i, vp, vp, i, d, d,
+                                        d, d, d, vp, d, d, i, ctypes.c_uint64, vp]
+            L.dflash2_adamw.restype = i
+            L.dflash2_state_decode.argtypes = [vp, vp, ll, i, i, vp, vp]
+            L.dflash2_state_decode.restype = i
+            L.dflash2_state_encode.argtypes = [vp, i, ll, i, vp, vp, vp]
+            L.dflash2_state_encode.restype = i
             L.dflash2_select_plan.argtypes = [i, i, i, i, i, i, ctypes.POINTER(ctypes.c_int)]
             L.dflash2_select_plan.restype = i
             L.dflash2_probe_gather.argtypes = [vp, ctypes.c_longlong, i, vp, i, vp, vp]
@@ -487,6 +512,311 @@ def distill_backward(grad_loss, logits, teacher_ids, teacher_logits, lse, temper
     if given:
         increment_version(grad)
     return grad
+
+
+def _launch(index: int, entry, *args):
+    """Calls an entry whose last argument is the stream, with the tensors' device current."""
+    if torch.cuda.current_device() == index:
+        st = entry(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = entry(*args, _raw_stream(index))
+    if st != DF2_OK:
+        _check(st)
+
+
+def _on(t, name, dtype, shape, index):
+    """Pointer of an input of this type and shape on the device; None for None."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _need_rows(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on device cuda:{index}, got {t.device}")
+
+
+def _out_on(t, name, dtype, shape, dev):
+    """(tensor, pointer) of an output, allocated for None."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _on(t, name, dtype, shape, dev.index)
+
+
+def _grad_on(grad, logits, ld):
+    """_grad_rows, with no gradient for None or False and on the logits' device."""
+    if grad is None or grad is False:
+        return None, None, 0
+    grad, ptr, grad_ld = _grad_rows(grad, logits, ld)
+    if grad.get_device() != logits.get_device():
+        raise ValueError("grad must be on the device of logits")
+    return grad, ptr, grad_ld
+
+
+def policy_loss(logits, tokens, old_logp, advantage, ref_logp=None, temperature=1.0, clip_low=0.2,
+                clip_high=0.2, kl_coef=0.0, weight=None, grad=False, loss=None, logp=None, lse=None,
+                err_flag=None):
+    """The clipped policy loss with a KL term at the drawn tokens: logits [..., V] (fp32 or
+    bf16; the rows may be evenly spaced views), tokens [...] int32 (negative: not counted),
+    old_logp, advantage, ref_logp [...] fp32 (ref_logp may be None where kl_coef is 0), weight
+    [...] fp32 or None.  Returns (loss, logp, lse [...] fp32, grad): with rho = exp(logp -
+    old_logp) and d = ref_logp - logp,
+    loss = weight * (kl_coef * (exp(d) - d - 1) - min(rho * A, clamp(rho, 1 - clip_low,
+    1 + clip_high) * A)); logp and lse for policy_loss_backward; and with grad=True (or a
+    tensor to write, which may be logits) the gradient of the sum of the losses; else None.
+    The results carry no autograd graph: hand the gradient on by logits.backward(grad)."""
+    shape, rows, V, ld = _logit_rows(logits, "logits")
+    dev = logits.device
+    at, f32 = dev.index, torch.float32
+    ins = (_on(tokens, "tokens", torch.int32, shape, at), _on(old_logp, "old_logp", f32, shape, at),
+           _on(advantage, "advantage", f32, shape, at), _on(ref_logp, "ref_logp", f32, shape, at),
+           _on(weight, "weight", f32, shape, at))
+    loss, loss_ptr = _out_on(loss, "loss", f32, shape, dev)
+    logp, logp_ptr = _out_on(logp, "logp", f32, shape, dev)
+    lse, lse_ptr = _out_on(lse, "lse", f32, shape, dev)
+    flag = _on(err_flag, "err_flag", torch.int32, (1,), at)
+    given = isinstance(grad, torch.Tensor)
+    grad, grad_ptr, grad_ld = _grad_on(grad, logits, ld)
+    _launch(at, lib().dflash2_policy_loss, logits.data_ptr(), ld, *ins, rows, V, temperature,
+            clip_low, clip_high, kl_coef, _code(logits.dtype), loss_ptr, logp_ptr, lse_ptr,
+            grad_ptr, grad_ld, flag)
+    if given:
+        increment_version(grad)
+    return loss, logp, lse, grad
+
+
+def policy_loss_backward(grad_loss, logits, tokens, old_logp, advantage, logp, lse, ref_logp=None,
+                         temperature=1.0, clip_low=0.2, clip_high=0.2, kl_coef=0.0, weight=None,
+                         grad=True, err_flag=None):
+    """The gradient of policy_loss() by its logits alone, from the gradient by its losses,
+    grad_loss [...] fp32, and the logp and lse [...] that it returned.  grad may be a tensor
+    to write (also logits).  It carries no autograd graph."""
+    shape, rows, V, ld = _logit_rows(logits, "logits")
+    at, f32 = logits.device.index, torch.float32
+    up = _on(grad_loss, "grad_loss", f32, shape, at)
+    ins = (_on(tokens, "tokens", torch.int32, shape, at), _on(old_logp, "old_logp", f32, shape, at),
+           _on(advantage, "advantage", f32, shape, at), _on(ref_logp, "ref_logp", f32, shape, at),
+           _on(weight, "weight", f32, shape, at), _on(logp, "logp", f32, shape, at),
+           _on(lse, "lse", f32, shape, at))
+    flag = _on(err_flag, "err_flag", torch.int32, (1,), at)
+    given = isinstance(grad, torch.Tensor)
+    grad, grad_ptr, grad_ld = _grad_on(grad, logits, ld)
+    _launch(at, lib().dflash2_policy_loss_backward, up, logits.data_ptr(), ld, *ins, rows, V,
+            temperature, clip_low, clip_high, kl_coef, _code(logits.dtype), grad_ptr, grad_ld,
+            flag)
+    if given:
+        increment_version(grad)
+    return grad
+
+
+def _pairs(offsets):
+    """Number of pairs that offsets [2 * pairs + 1] divides the rows into."""
+    if offsets.dim() != 1 or offsets.numel() % 2 != 1:
+        raise ValueError("offsets must have the shape [2 * pairs + 1], got "
+                         f"{tuple(offsets.shape)}")
+    return offsets.numel() // 2
+
+
+def preference_loss(logits, tokens, offsets, ref_logp=None, beta=0.1, label_smoothing=0.0,
+                    margin=0.0, average=False, weight=None, grad=False, loss=None, seq_logp=None,
+                    logp=None, lse=None, err_flag=None):
+    """The preference loss of pairs of sequences by their log ratios: logits [..., V] (fp32 or
+    bf16; the rows may be evenly spaced views), tokens [...] int32 (negative: not counted, as
+    a prompt's), offsets [2 * pairs + 1] int32: sequence s has the rows offsets[s] to
+    offsets[s + 1] - 1, pair i consists of the chosen sequence i and the rejected one pairs + i;
+    ref_logp [2 * pairs] fp32, the reference's sums of log-probabilities (means with average=True),
+    or None; weight [pairs] fp32 or None.  With S the sequences' sums (means) and m = beta *
+    ((S_c - ref_c) - (S_r - ref_r)) - margin, loss = weight * ((1 - label_smoothing) * log(1 +
+    exp(-m)) + label_smoothing * log(1 + exp(m))).  Returns (loss [pairs], seq_logp [2 * pairs],
+    logp [...], lse [...], grad): seq_logp and lse for preference_loss_backward; grad as
+    policy_loss()'s."""
+    shape, rows, V, ld = _logit_rows(logits, "logits")
+    dev, pairs = logits.device, _pairs(offsets)
+    at, f32 = dev.index, torch.float32
+    ins = (_on(tokens, "tokens", torch.int32, shape, at),
+           _on(offsets, "offsets", torch.int32, (2 * pairs + 1,), at),
+           _on(ref_logp, "ref_logp", f32, (2 * pairs,), at),
+           _on(weight, "weight", f32, (pairs,), at))
+    loss, loss_ptr = _out_on(loss, "loss", f32, (pairs,), dev)
+    seq_logp, seq_ptr = _out_on(seq_logp, "seq_logp", f32, (2 * pairs,), dev)
+    logp, logp_ptr = _out_on(logp, "logp", f32, shape, dev)
+    lse, lse_ptr = _out_on(lse, "lse", f32, shape, dev)
+    flag = _on(err_flag, "err_flag", torch.int32, (1,), at)
+    given = isinstance(grad, torch.Tensor)
+    grad, grad_ptr, grad_ld = _grad_on(grad, logits, ld)
+    _launch(at, lib().dflash2_preference_loss, logits.data_ptr(), ld, *ins, rows, V, pairs, beta,
+            label_smoothing, margin, average, _code(logits.dtype), loss_ptr, seq_ptr, logp_ptr,
+            lse_ptr, grad_ptr, grad_ld, flag)
+    if given:
+        increment_version(grad)
+    return loss, seq_logp, logp, lse, grad
+
+
+def preference_loss_backward(grad_loss, logits, tokens, offsets, seq_logp, lse, ref_logp=None,
+                             beta=0.1, label_smoothing=0.0, margin=0.0, average=False, weight=None,
+                             grad=True, err_flag=None):
+    """The gradient of preference_loss() by its logits alone, from the gradient by its losses,
+    grad_loss [pairs] fp32, and the seq_logp and lse that it returned.  grad may be a tensor
+    to write (also logits).  It carries no autograd graph."""
+    shape, rows, V, ld = _logit_rows(logits, "logits")
+    pairs, at, f32 = _pairs(offsets), logits.device.index, torch.float32
+    up = _on(grad_loss, "grad_loss", f32, (pairs,), at)
+    ins = (_on(tokens, "tokens", torch.int32, shape, at),
+           _on(offsets, "offsets", torch.int32, (2 * pairs + 1,), at),
+           _on(ref_logp, "ref_logp", f32, (2 * pairs,), at),
+           _on(weight, "weight", f32, (pairs,), at),
+           _on(seq_logp, "seq_logp", f32, (2 * pairs,), at), _on(lse, "lse", f32, shape, at))
+    flag = _on(err_flag, "err_flag", torch.int32, (1,), at)
+    given = isinstance(grad, torch.Tensor)
+    grad, grad_ptr, grad_ld = _grad_on(grad, logits, ld)
+    _launch(at, lib().dflash2_preference_loss_backward, up, logits.data_ptr(), ld, *ins, rows, V,
+            pairs, beta, label_smoothing, margin, average, _code(logits.dtype), grad_ptr, grad_ld,
+            flag)
+    if given:
+        increment_version(grad)
+    return grad
+
+
+_device_of, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
+_data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
+_dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape")
+
+
+def _many(ts, name, dtype, index, shapes):
+    """The tensors' pointers as a C array: of one type, on one device, contiguous, of these
+    shapes; None for None."""
+    if ts is None:
+        return None
+    if len(ts) != len(shapes):
+        raise ValueError(f"{name} has {len(ts)} tensors, {len(shapes)} are needed")
+    if set(map(_device_of, ts)) != {index}:
+        raise ValueError(f"{name} must be CUDA tensors on one device, that of all others")
+    if not all(map(_is_contiguous, ts)):
+        raise ValueError(f"{name} must be contiguous")
+    if set(map(_dtype_of, ts)) != {dtype}:
+        raise TypeError(f"{name} must be {dtype} all")
+    if list(map(_shape_of, ts)) != shapes:
+        raise ValueError(f"{name} must have the shapes {[tuple(s) for s in shapes]}")
+    return (ctypes.c_void_p * len(ts))(*map(_data_ptr, ts))
+
+
+def _first(ts, name):
+    """The first of a list that is not empty, with nothing but tensors in it."""
+    for t in ts:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be tensors, got {type(t).__name__}")
+    return ts[0]
+
+
+def _sizes(ts):
+    return (ctypes.c_int64 * len(ts))(*map(_numel, ts))
+
+
+def grad_norm(grads, out=None, workspace=None):
+    """The 2-norm of a list of gradients together (fp32 or bf16, one type) -> [1] fp32, without
+    waiting for it.  workspace: a uint8 CUDA tensor, allocated for None; calls that may run at
+    the same time each need one of their own."""
+    if len(grads) == 0:
+        raise ValueError("grad_norm needs at least one tensor")
+    first = _first(grads, "grads")
+    dev = first.device
+    ptrs = _many(grads, "grads", first.dtype, first.get_device(), list(map(_shape_of, grads)))
+    if dev.type != "cuda":
+        raise ValueError("grads must be CUDA tensors")
+    sizes, L = _sizes(grads), lib()
+    out, out_ptr = _out_on(out, "out", torch.float32, (1,), dev)
+    need = L.dflash2_grad_norm_workspace_bytes(len(grads), sizes)
+    if workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    ws = _on(workspace, "workspace", torch.uint8, workspace.shape, dev.index)
+    _launch(dev.index, L.dflash2_grad_norm, len(grads), ptrs, sizes, _code(first.dtype), ws,
+            workspace.numel(), out_ptr)
+    return out
+
+
+def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
+          weight_decay=0.01, master=None, exp_avg_scale=None, exp_avg_sq_scale=None, norm=None,
+          max_norm=None, grad_scale=1.0, seed=None):
+    """One AdamW step over lists of tensors, in place: params and grads (each fp32 or bf16, one
+    type a list), exp_avg and exp_avg_sq fp32, or uint8 with the lists exp_avg_scale and
+    exp_avg_sq_scale ([(numel + 31) // 32] uint8 each): states in 8 bits, zeros to begin with
+    (state_encode and state_decode go from values to them and back).  master: fp32 copies of bf16
+    params, which take the step.  step: the step's number, 1 for the first, or an int32 CUDA
+    tensor [1] with it; lr: a number or an fp32 CUDA tensor [1] (both for captured graphs).
+    norm: the gradients' norm (grad_norm); where it is not finite, nothing is changed; with
+    max_norm it clips grads * grad_scale.  seed: an integer, by which 8-bit states, and bf16
+    params without master, are rounded up or down with odds by the distance (else to the
+    nearest, where 8-bit states and small steps of bf16 params get stuck)."""
+    if len(params) == 0:
+        if any(len(v) for v in (grads, exp_avg, exp_avg_sq)):
+            raise ValueError("params is empty, other lists are not")
+        return
+    first = _first(params, "params")
+    at, shapes, f32 = first.get_device(), list(map(_shape_of, params)), torch.float32
+    if at < 0:
+        raise ValueError("params must be CUDA tensors")
+    if len(grads) == 0:
+        raise ValueError(f"grads has 0 tensors, {len(shapes)} are needed")
+    small = exp_avg_scale is not None or exp_avg_sq_scale is not None
+    state = torch.uint8 if small else f32
+    ptrs = [_many(params, "params", first.dtype, at, shapes),
+            _many(grads, "grads", _first(grads, "grads").dtype, at, shapes),
+            _many(exp_avg, "exp_avg", state, at, shapes),
+            _many(exp_avg_sq, "exp_avg_sq", state, at, shapes),
+            _many(master, "master", f32, at, shapes)]
+    sizes = _sizes(params)
+    blocks = [(-(-n // 32),) for n in sizes] if small else None
+    ptrs += [_many(exp_avg_scale, "exp_avg_scale", torch.uint8, at, blocks),
+             _many(exp_avg_sq_scale, "exp_avg_sq_scale", torch.uint8, at, blocks)]
+    step_at, step = _setting_on(step, "step", torch.int32, at)
+    if step_at is None and not 1 <= step < 1 << 31:  # the entry takes 32 bits
+        raise ValueError(f"step={step}: the first step is 1, the last one 2^31 - 1")
+    lr_at, lr = _setting_on(lr, "lr", f32, at)
+    norm_at = _on(norm, "norm", f32, (1,), at)
+    for ts in (params, exp_avg, exp_avg_sq, master, exp_avg_scale, exp_avg_sq_scale):
+        if ts is not None:  # before the launch, which an inference tensor outside its mode forbids
+            increment_version(ts)
+    _launch(at, lib().dflash2_adamw, len(params), *ptrs, sizes, _code(first.dtype),
+            _code(grads[0].dtype), step_at, lr_at, step, lr, beta1, beta2, eps, weight_decay,
+            norm_at, 0.0 if max_norm is None else max_norm, grad_scale, seed is not None,
+            0 if seed is None else seed & 0xffffffffffffffff)
+
+
+def _setting_on(v, name, dtype, index):
+    """(pointer, number) of a setting given as a tensor [1] on the device or as a number."""
+    if isinstance(v, torch.Tensor):
+        return _on(v, name, dtype, (1,), index), 0
+    return None, v
+
+
+def state_decode(codes, scale, squares=False, dtype=torch.float32, out=None):
+    """The values of an 8-bit state of adamw(): codes uint8 of any shape, scale uint8
+    [(numel + 31) // 32]; squares=True for exp_avg_sq.  Exact in fp32 and bf16."""
+    index = codes.get_device()
+    if index < 0:
+        raise ValueError("codes must be a CUDA tensor")
+    n = codes.numel()
+    c = _on(codes, "codes", torch.uint8, codes.shape, index)
+    s = _on(scale, "scale", torch.uint8, (-(-n // 32),), index)
+    dtype = out.dtype if out is not None else dtype
+    code = _code(dtype)
+    out, out_ptr = _out_on(out, "out", dtype, codes.shape, codes.device)
+    _launch(index, lib().dflash2_state_decode, c, s, n, squares, code, out_ptr)
+    return out
+
+
+def state_encode(values, squares=False, codes=None, scale=None):
+    """An 8-bit state of adamw() from values (fp32 or bf16, contiguous), to the nearest:
+    (codes uint8 of the same shape, scale uint8 [(numel + 31) // 32])."""
+    index = values.get_device()
+    if index < 0:
+        raise ValueError("values must be a CUDA tensor")
+    n = values.numel()
+    v = _on(values, "values", values.dtype, values.shape, index)
+    codes, c = _out_on(codes, "codes", torch.uint8, values.shape, values.device)
+    scale, s = _out_on(scale, "scale", torch.uint8, (-(-n // 32),), values.device)
+    _launch(index, lib().dflash2_state_encode, v, _code(values.dtype), n, squares, c, s)
+    return codes, scale
 
 
 def take_device_faults() -> int:

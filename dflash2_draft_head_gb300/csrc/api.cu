@@ -1,12 +1,15 @@
 // C ABI of the DFlash2 draft-head library: argument validation on the host,
 // then dispatch to the kernels.  Nothing here allocates device memory or
 // synchronises the host (except dflash2_take_device_faults, by contract).
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <new>
+#include <vector>
 
 #include "common.cuh"
 #include "dflash2.h"
@@ -267,6 +270,225 @@ int run_distill(const char* what, bool backward, df2::DistillArgs a, float tempe
                                         num_sms_of_current_device());
     if (e != cudaSuccess) return cuda_fail(e, what);
     return DF2_OK;
+}
+
+// The checks and the launch of the policy and preference losses and of their gradients alone
+// (`backward`: grad_loss, lse and, by the policy, logp or, by the preference, seq_logp are inputs).
+int run_token_loss(const char* what, bool pairwise, bool backward, df2::TokenLossArgs a,
+                   float temperature, int dtype, void* stream) {
+    if (a.rows < 0 || a.V <= 0 || a.pairs < 0)
+        return fail(DF2_ERR_INVALID_ARG, "%s: bad sizes rows=%d V=%d pairs=%d", what, a.rows, a.V,
+                    a.pairs);
+    if (!valid_dtype(dtype)) return fail(DF2_ERR_INVALID_ARG, "%s: bad dtype %d", what, dtype);
+    a.inv_t = 1.f / temperature;
+    a.c = a.inv_t * 1.44269504088896341f;
+    if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(a.c) || a.c == 0.f)
+        return fail(DF2_ERR_INVALID_ARG, "%s: temperature=%g must be positive and finite", what,
+                    (double)temperature);
+    if (pairwise) {
+        if (!std::isfinite(a.beta) || !std::isfinite(a.margin) ||
+            !(a.smoothing >= 0.f && a.smoothing <= 1.f))
+            return fail(DF2_ERR_INVALID_ARG,
+                        "%s: beta=%g and margin=%g must be finite, label_smoothing=%g in [0, 1]",
+                        what, (double)a.beta, (double)a.margin, (double)a.smoothing);
+    } else if (!(a.ratio_lo <= 1.f) || !(a.ratio_hi >= 1.f) || !std::isfinite(a.kl_coef)) {
+        return fail(DF2_ERR_INVALID_ARG,
+                    "%s: clip_low and clip_high must not be negative, kl_coef=%g finite", what,
+                    (double)a.kl_coef);
+    }
+    if (a.rows == 0 && (backward || a.pairs == 0)) return DF2_OK;
+    if (a.rows > 0 &&
+        (a.logits == nullptr || a.tokens == nullptr || a.lse == nullptr ||
+         (backward && a.grad == nullptr) || (a.logp == nullptr && !(pairwise && backward)) ||
+         (!pairwise && (a.old_logp == nullptr || a.advantage == nullptr ||
+                        (backward ? a.grad_loss : a.loss) == nullptr ||
+                        (a.kl_coef != 0.f && a.ref_logp == nullptr)))))
+        return fail(DF2_ERR_INVALID_ARG, "%s: NULL required pointer", what);
+    if (pairwise && (a.offsets == nullptr ||
+                     (a.pairs > 0 && (a.seq_logp == nullptr ||
+                                      (backward ? a.grad_loss : a.loss) == nullptr))))
+        return fail(DF2_ERR_INVALID_ARG, "%s: NULL required pointer", what);
+    int st = DF2_OK;
+    if (a.rows > 0) {
+        st = validate_rows(what, "logits", a.logits, a.ld, a.rows, a.V, dtype);
+        if (st == DF2_OK && a.grad != nullptr)
+            st = validate_rows(what, "grad", a.grad, a.grad_ld, a.rows, a.V, dtype);
+        if (st != DF2_OK) return st;
+    }
+    if (a.pairs > (1 << 24))
+        return fail(DF2_ERR_UNSUPPORTED, "%s: pairs=%d > %d", what, a.pairs, 1 << 24);
+    const size_t R4 = (size_t)a.rows * 4, P4 = (size_t)a.pairs * 4;
+    const size_t L4 = pairwise ? P4 : R4;  // a loss
+    const bool some = a.rows > 0;
+    const Buf ins[11] = {{a.tokens, R4, "tokens"},
+                         {a.old_logp, R4, "old_logp"},
+                         {a.advantage, R4, "advantage"},
+                         {a.weight, L4, "weight"},
+                         {a.ref_logp, pairwise ? 2 * P4 : R4, "ref_logp"},
+                         {a.offsets, 2 * P4 + 4, "offsets"},
+                         {a.grad_loss, L4, "grad_loss"},
+                         {backward ? a.lse : nullptr, R4, "lse"},
+                         {backward ? a.logp : nullptr, R4, "logp"},
+                         {backward ? a.seq_logp : nullptr, 2 * P4, "seq_logp"},
+                         {a.logits, some ? rows_bytes(a.ld, a.rows, a.V, dtype) : 0, "logits"}};
+    const Buf outs[6] = {
+        {backward ? nullptr : a.loss, L4, "loss"},
+        {backward ? nullptr : a.lse, R4, "lse"},
+        {backward ? nullptr : a.logp, R4, "logp"},
+        {backward ? nullptr : a.seq_logp, 2 * P4, "seq_logp"},
+        {a.err_flag, 4, "err_flag"},
+        {a.grad, some && a.grad ? rows_bytes(a.grad_ld, a.rows, a.V, dtype) : 0, "grad"}};
+    st = check_aligned4(what, ins, 10);
+    if (st == DF2_OK) st = check_aligned4(what, outs, 5);
+    // the gradient may take the logits' place, exactly
+    const bool in_place = a.grad == a.logits && (a.grad_ld == a.ld || a.rows == 1);
+    if (st == DF2_OK) st = check_disjoint(outs, 6, ins, 10);
+    if (st == DF2_OK) st = check_disjoint(outs, in_place ? 5 : 6, ins + 10, 1);
+    if (st != DF2_OK) return st;
+    if (a.V > df2::kDistillMaxV)
+        return fail(DF2_ERR_UNSUPPORTED, "%s: V=%d > %d", what, a.V, df2::kDistillMaxV);
+    const auto pass = backward ? df2::TokenLossPass::kGrad : df2::TokenLossPass::kLoss;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int sms = num_sms_of_current_device();
+    const cudaError_t e = pairwise
+                              ? df2::launch_preference_loss(a, pass, dtype == DF2_BF16, s, sms)
+                              : df2::launch_policy_loss(a, pass, dtype == DF2_BF16, s, sms);
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    return DF2_OK;
+}
+
+// Largest number of elements of a tensor: a launch's chunks stay inside 32 bits.
+constexpr long long kMostElements = 1ll << 40;
+
+int validate_tensors(const char* what, int count, const long long* sizes) {
+    if (count < 0) return fail(DF2_ERR_INVALID_ARG, "%s: count=%d is negative", what, count);
+    if (count > 0 && sizes == nullptr) return fail(DF2_ERR_INVALID_ARG, "%s: NULL sizes", what);
+    for (int k = 0; k < count; ++k) {
+        if (sizes[k] < 0)
+            return fail(DF2_ERR_INVALID_ARG, "%s: size of tensor %d is negative", what, k);
+        if (sizes[k] > kMostElements)
+            return fail(DF2_ERR_UNSUPPORTED, "%s: tensor %d has more than 2^40 elements", what, k);
+    }
+    return DF2_OK;
+}
+
+// Pointers of tensors that have elements: there, and aligned to one of them.
+int validate_pointers(const char* what, const char* name, int count, const void* const* p,
+                      const long long* sizes, size_t es) {
+    if (p == nullptr && count > 0) return fail(DF2_ERR_INVALID_ARG, "%s: NULL %s", what, name);
+    for (int k = 0; k < count; ++k) {
+        if (sizes[k] == 0) continue;
+        if (p[k] == nullptr) return fail(DF2_ERR_INVALID_ARG, "%s: %s[%d] is NULL", what, name, k);
+        if (reinterpret_cast<uintptr_t>(p[k]) % es != 0)
+            return fail(DF2_ERR_INVALID_ARG, "%s: %s[%d] is not aligned to its elements", what,
+                        name, k);
+    }
+    return DF2_OK;
+}
+
+// A stretch of memory that a call reads or writes.
+struct Span {
+    uintptr_t lo, hi;
+    bool write;
+};
+
+// Whether a stretch that is written overlaps another one.
+bool any_overlap(std::vector<Span>& v) {
+    std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+    uintptr_t end = 0, written = 0;  // of the stretches before
+    for (const Span& s : v) {
+        if (s.lo < written || (s.write && s.lo < end)) return true;
+        end = std::max(end, s.hi);
+        if (s.write) written = std::max(written, s.hi);
+    }
+    return false;
+}
+
+int run_adamw(const df2::AdamwArgs& a, int param_dtype, int grad_dtype, void* stream) {
+    const char* what = "adamw";
+    int st = validate_tensors(what, a.count, a.sizes);
+    if (st != DF2_OK) return st;
+    if (!valid_dtype(param_dtype) || !valid_dtype(grad_dtype))
+        return fail(DF2_ERR_INVALID_ARG, "adamw: bad dtype");
+    if (!(a.beta1 >= 0 && a.beta1 < 1) || !(a.beta2 >= 0 && a.beta2 < 1))
+        return fail(DF2_ERR_INVALID_ARG, "adamw: beta1=%g and beta2=%g must be in [0, 1)", a.beta1,
+                    a.beta2);
+    // in fp32, as the kernel takes it
+    if (!((float)a.eps > 0.f) || !std::isfinite((float)a.eps))
+        return fail(DF2_ERR_INVALID_ARG, "adamw: eps=%g must be positive and finite", a.eps);
+    if (!std::isfinite((float)a.weight_decay) || !std::isfinite((float)a.grad_scale) ||
+        (a.lr_at == nullptr && !std::isfinite((float)a.lr)))
+        return fail(DF2_ERR_INVALID_ARG, "adamw: lr, weight_decay and grad_scale must be finite");
+    if (!(a.max_norm >= 0))
+        return fail(DF2_ERR_INVALID_ARG, "adamw: max_norm=%g must not be negative", a.max_norm);
+    if (a.max_norm > 0 && a.norm == nullptr)
+        return fail(DF2_ERR_INVALID_ARG, "adamw: max_norm needs the gradients' norm");
+    if (a.step_at == nullptr && a.step < 1)
+        return fail(DF2_ERR_INVALID_ARG, "adamw: step=%d: the first step is 1", a.step);
+    const bool s8 = a.exp_avg_scale != nullptr;
+    if (s8 != (a.exp_avg_sq_scale != nullptr))
+        return fail(DF2_ERR_INVALID_ARG, "adamw: 8-bit states need both scales");
+    if (a.master != nullptr && param_dtype != DF2_BF16)
+        return fail(DF2_ERR_INVALID_ARG, "adamw: master copies belong to bf16 parameters");
+    const size_t ps = esize(param_dtype), gs = esize(grad_dtype), ss = s8 ? 1 : 4;
+    auto as_const = [](auto p) { return reinterpret_cast<const void* const*>(p); };
+    struct {
+        const char* name;
+        const void* const* p;
+        size_t es;
+        bool write, scale;
+    } const list[7] = {{"params", as_const(a.params), ps, true, false},
+                       {"grads", a.grads, gs, false, false},
+                       {"exp_avg", as_const(a.exp_avg), ss, true, false},
+                       {"exp_avg_sq", as_const(a.exp_avg_sq), ss, true, false},
+                       {"master", as_const(a.master), 4, true, false},
+                       {"exp_avg_scale", as_const(a.exp_avg_scale), 1, true, true},
+                       {"exp_avg_sq_scale", as_const(a.exp_avg_sq_scale), 1, true, true}};
+    for (int j = 0; j < 7 && st == DF2_OK; ++j)
+        if (j < 4 || list[j].p != nullptr)
+            st = validate_pointers(what, list[j].name, a.count, list[j].p, a.sizes, list[j].es);
+    if (st != DF2_OK) return st;
+    const Buf scalars[3] = {{a.step_at, 4, "step"}, {a.lr_at, 4, "lr"}, {a.norm, 4, "norm"}};
+    st = check_aligned4(what, scalars, 3);
+    if (st != DF2_OK) return st;
+    std::vector<Span> spans;
+    spans.reserve((size_t)a.count * 7 + 3);
+    auto add = [&](const void* p, size_t bytes, bool write) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        if (p != nullptr && bytes > 0) spans.push_back({lo, lo + bytes, write});
+    };
+    for (const Buf& b : scalars) add(b.p, b.bytes, false);
+    for (const auto& l : list) {
+        if (l.p == nullptr) continue;
+        for (int k = 0; k < a.count; ++k)
+            add(l.p[k], (size_t)(l.scale ? (a.sizes[k] + 31) / 32 : a.sizes[k]) * l.es, l.write);
+    }
+    if (any_overlap(spans))
+        return fail(DF2_ERR_INVALID_ARG,
+                    "adamw: a tensor that is written overlaps another (one is listed twice?)");
+    const cudaError_t e = df2::launch_adamw(a, param_dtype == DF2_BF16, grad_dtype == DF2_BF16,
+                                            static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "adamw launch");
+    return DF2_OK;
+}
+
+// codes, their scales and n values of `dtype`.
+int validate_state(const char* what, const void* codes, const void* scale, long long n,
+                   const void* values, int dtype, bool encode) {
+    if (n < 0) return fail(DF2_ERR_INVALID_ARG, "%s: n=%lld is negative", what, n);
+    if (!valid_dtype(dtype)) return fail(DF2_ERR_INVALID_ARG, "%s: bad dtype %d", what, dtype);
+    if (n == 0) return DF2_OK;
+    if (codes == nullptr || scale == nullptr || values == nullptr)
+        return fail(DF2_ERR_INVALID_ARG, "%s: NULL required pointer", what);
+    if (n > kMostElements)
+        return fail(DF2_ERR_UNSUPPORTED, "%s: more than 2^40 elements", what);
+    if (reinterpret_cast<uintptr_t>(values) % esize(dtype) != 0)
+        return fail(DF2_ERR_INVALID_ARG, "%s: values are not aligned to their elements", what);
+    const Buf b[3] = {{codes, (size_t)n, "codes"},
+                      {scale, (size_t)((n + 31) / 32), "scale"},
+                      {values, (size_t)n * esize(dtype), "values"}};
+    if (encode) return check_disjoint(b, 2, b + 2, 1);
+    return check_disjoint(b + 2, 1, b, 2);
 }
 
 }  // namespace
@@ -673,6 +895,209 @@ int dflash2_distill_backward(const float* grad_loss, const void* logits, long lo
     df2::DistillArgs a{logits, ld, teacher_ids, teacher_logits, weight, grad_loss, rows, V, K, 0.f,
                        0.f, nullptr, const_cast<float*>(lse), grad, grad_ld, err_flag};
     return run_distill("distill_backward", true, a, temperature, dtype, stream);
+}
+
+int dflash2_policy_loss(const void* logits, long long ld, const int32_t* tokens,
+                        const float* old_logp, const float* advantage, const float* ref_logp,
+                        const float* weight, int rows, int V, float temperature, float clip_low,
+                        float clip_high, float kl_coef, int dtype, float* loss, float* logp,
+                        float* lse, void* grad, long long grad_ld, int32_t* err_flag,
+                        void* stream) {
+    g_err[0] = 0;
+    df2::TokenLossArgs a{};
+    a.logits = logits;
+    a.ld = ld;
+    a.tokens = tokens;
+    a.rows = rows;
+    a.V = V;
+    a.weight = weight;
+    a.ref_logp = ref_logp;
+    a.old_logp = old_logp;
+    a.advantage = advantage;
+    a.ratio_lo = 1.f - clip_low;
+    a.ratio_hi = 1.f + clip_high;
+    a.kl_coef = kl_coef;
+    a.loss = loss;
+    a.logp = logp;
+    a.lse = lse;
+    a.grad = grad;
+    a.grad_ld = grad_ld;
+    a.err_flag = err_flag;
+    return run_token_loss("policy_loss", false, false, a, temperature, dtype, stream);
+}
+
+int dflash2_policy_loss_backward(const float* grad_loss, const void* logits, long long ld,
+                                 const int32_t* tokens, const float* old_logp,
+                                 const float* advantage, const float* ref_logp,
+                                 const float* weight, const float* logp, const float* lse,
+                                 int rows, int V, float temperature, float clip_low,
+                                 float clip_high, float kl_coef, int dtype, void* grad,
+                                 long long grad_ld, int32_t* err_flag, void* stream) {
+    g_err[0] = 0;
+    df2::TokenLossArgs a{};
+    a.logits = logits;
+    a.ld = ld;
+    a.tokens = tokens;
+    a.rows = rows;
+    a.V = V;
+    a.weight = weight;
+    a.ref_logp = ref_logp;
+    a.grad_loss = grad_loss;
+    a.old_logp = old_logp;
+    a.advantage = advantage;
+    a.ratio_lo = 1.f - clip_low;
+    a.ratio_hi = 1.f + clip_high;
+    a.kl_coef = kl_coef;
+    a.logp = const_cast<float*>(logp);
+    a.lse = const_cast<float*>(lse);
+    a.grad = grad;
+    a.grad_ld = grad_ld;
+    a.err_flag = err_flag;
+    return run_token_loss("policy_loss_backward", false, true, a, temperature, dtype, stream);
+}
+
+int dflash2_preference_loss(const void* logits, long long ld, const int32_t* tokens,
+                            const int32_t* offsets, const float* ref_logp, const float* weight,
+                            int rows, int V, int pairs, float beta, float label_smoothing,
+                            float margin, int average, int dtype, float* loss, float* seq_logp,
+                            float* logp, float* lse, void* grad, long long grad_ld,
+                            int32_t* err_flag, void* stream) {
+    g_err[0] = 0;
+    df2::TokenLossArgs a{};
+    a.logits = logits;
+    a.ld = ld;
+    a.tokens = tokens;
+    a.rows = rows;
+    a.V = V;
+    a.weight = weight;
+    a.ref_logp = ref_logp;
+    a.offsets = offsets;
+    a.pairs = pairs;
+    a.average = average != 0;
+    a.beta = beta;
+    a.smoothing = label_smoothing;
+    a.margin = margin;
+    a.seq_logp = seq_logp;
+    a.loss = loss;
+    a.logp = logp;
+    a.lse = lse;
+    a.grad = grad;
+    a.grad_ld = grad_ld;
+    a.err_flag = err_flag;
+    return run_token_loss("preference_loss", true, false, a, 1.f, dtype, stream);
+}
+
+int dflash2_preference_loss_backward(const float* grad_loss, const void* logits, long long ld,
+                                     const int32_t* tokens, const int32_t* offsets,
+                                     const float* ref_logp, const float* weight,
+                                     const float* seq_logp, const float* lse, int rows, int V,
+                                     int pairs, float beta, float label_smoothing, float margin,
+                                     int average, int dtype, void* grad, long long grad_ld,
+                                     int32_t* err_flag, void* stream) {
+    g_err[0] = 0;
+    df2::TokenLossArgs a{};
+    a.logits = logits;
+    a.ld = ld;
+    a.tokens = tokens;
+    a.rows = rows;
+    a.V = V;
+    a.weight = weight;
+    a.ref_logp = ref_logp;
+    a.grad_loss = grad_loss;
+    a.offsets = offsets;
+    a.pairs = pairs;
+    a.average = average != 0;
+    a.beta = beta;
+    a.smoothing = label_smoothing;
+    a.margin = margin;
+    a.seq_logp = const_cast<float*>(seq_logp);
+    a.lse = const_cast<float*>(lse);
+    a.grad = grad;
+    a.grad_ld = grad_ld;
+    a.err_flag = err_flag;
+    return run_token_loss("preference_loss_backward", true, true, a, 1.f, dtype, stream);
+}
+
+size_t dflash2_grad_norm_workspace_bytes(int count, const int64_t* sizes) {
+    static_assert(sizeof(int64_t) == sizeof(long long), "sizes are passed on");
+    const long long* n = reinterpret_cast<const long long*>(sizes);
+    if (validate_tensors("grad_norm", count, n) != DF2_OK) return 0;
+    return (size_t)df2::grad_norm_chunks(count, n) * sizeof(double);
+}
+
+int dflash2_grad_norm(int count, const void* const* grads, const int64_t* sizes, int grad_dtype,
+                      void* workspace, size_t workspace_bytes, float* norm, void* stream) {
+    g_err[0] = 0;
+    const long long* n = reinterpret_cast<const long long*>(sizes);
+    int st = validate_tensors("grad_norm", count, n);
+    if (st != DF2_OK) return st;
+    if (!valid_dtype(grad_dtype))
+        return fail(DF2_ERR_INVALID_ARG, "grad_norm: bad dtype %d", grad_dtype);
+    if (norm == nullptr) return fail(DF2_ERR_INVALID_ARG, "grad_norm: NULL norm");
+    st = validate_pointers("grad_norm", "grads", count, grads, n, esize(grad_dtype));
+    if (st != DF2_OK) return st;
+    const size_t need = (size_t)df2::grad_norm_chunks(count, n) * sizeof(double);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+        return fail(DF2_ERR_INVALID_ARG, "grad_norm: workspace of %zu bytes, %zu are needed",
+                    workspace == nullptr ? (size_t)0 : workspace_bytes, need);
+    if (reinterpret_cast<uintptr_t>(workspace) % sizeof(double) != 0)
+        return fail(DF2_ERR_INVALID_ARG, "grad_norm: workspace is not 8-byte aligned");
+    const Buf outs[2] = {{norm, 4, "norm"}, {workspace, need, "workspace"}};
+    st = check_aligned4("grad_norm", outs, 1);
+    for (int k = 0; k < count && st == DF2_OK; ++k) {
+        const Buf in = {grads[k], (size_t)n[k] * esize(grad_dtype), "grads"};
+        st = check_disjoint(outs, 2, &in, 1);
+    }
+    if (st == DF2_OK) st = check_disjoint(outs, 2, nullptr, 0);
+    if (st != DF2_OK) return st;
+    df2::GradNormArgs a{count, grads, n, static_cast<double*>(workspace), norm};
+    const cudaError_t e = df2::launch_grad_norm(a, grad_dtype == DF2_BF16,
+                                                static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "grad_norm launch");
+    return DF2_OK;
+}
+
+int dflash2_adamw(int count, void* const* params, const void* const* grads, void* const* exp_avg,
+                  void* const* exp_avg_sq, float* const* master, uint8_t* const* exp_avg_scale,
+                  uint8_t* const* exp_avg_sq_scale, const int64_t* sizes, int param_dtype,
+                  int grad_dtype, const int32_t* step_at, const float* lr_at, int step, double lr,
+                  double beta1, double beta2, double eps, double weight_decay, const float* norm,
+                  double max_norm, double grad_scale, int by_chance, uint64_t seed, void* stream) {
+    g_err[0] = 0;
+    df2::AdamwArgs a{count, params, grads, exp_avg, exp_avg_sq, master, exp_avg_scale,
+                     exp_avg_sq_scale, reinterpret_cast<const long long*>(sizes), step_at, lr_at,
+                     step_at != nullptr ? 1 : step, lr, beta1, beta2, eps, weight_decay, norm,
+                     max_norm, grad_scale, by_chance != 0, seed};
+    try {
+        return run_adamw(a, param_dtype, grad_dtype, stream);
+    } catch (const std::bad_alloc&) {
+        return fail(DF2_ERR_INVALID_ARG, "adamw: no host memory for the checks of %d tensors",
+                    count);
+    }
+}
+
+int dflash2_state_decode(const uint8_t* codes, const uint8_t* scale, int64_t n, int squares,
+                         int out_dtype, void* out, void* stream) {
+    g_err[0] = 0;
+    const int st = validate_state("state_decode", codes, scale, n, out, out_dtype, false);
+    if (st != DF2_OK || n == 0) return st;
+    const cudaError_t e =
+        df2::launch_state_decode(codes, scale, n, squares, out, out_dtype == DF2_BF16,
+                                 static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "state_decode launch");
+    return DF2_OK;
+}
+
+int dflash2_state_encode(const void* values, int in_dtype, int64_t n, int squares, uint8_t* codes,
+                         uint8_t* scale, void* stream) {
+    g_err[0] = 0;
+    const int st = validate_state("state_encode", codes, scale, n, values, in_dtype, true);
+    if (st != DF2_OK || n == 0) return st;
+    const cudaError_t e =
+        df2::launch_state_encode(values, in_dtype == DF2_BF16, n, squares, codes, scale,
+                                 static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "state_encode launch");
+    return DF2_OK;
 }
 
 int dflash2_probe_gather(const void* table, long long rows, int row_bytes, const int32_t* ids,

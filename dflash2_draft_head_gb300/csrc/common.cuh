@@ -207,6 +207,81 @@ struct SampleArgs {
 constexpr int kSampleMaxV = 1 << 21;
 cudaError_t launch_sample(SampleArgs a, int bf16, cudaStream_t stream, int num_sms);
 
+// Losses of a token's log-probability by row (token_loss.cu): the clipped policy loss with a
+// KL term, and the preference loss of pairs of sequences.
+struct TokenLossArgs {
+    const void* logits;   // [rows, V], rows `ld` elements apart
+    long long ld;
+    const int32_t* tokens;  // [rows], negative: none
+    int rows, V;
+    float inv_t, c;       // 1 / T and log2(e) / T
+    const float* weight;  // [rows] (policy) or [pairs], or nullptr (1)
+    const float* ref_logp;  // [rows], or [2 * pairs] or nullptr
+    const float* grad_loss;  // [rows] or [pairs]; nullptr in the call with the loss
+    // policy
+    const float* old_logp;  // [rows]
+    const float* advantage;  // [rows]
+    float ratio_lo, ratio_hi, kl_coef;
+    // preference: sequence s has the rows offsets[s] to offsets[s + 1]; pair i consists of the
+    // chosen one i and the rejected one pairs + i
+    const int32_t* offsets;  // [2 * pairs + 1]
+    int pairs, average;
+    float beta, smoothing, margin;
+    float* seq_logp;      // [2 * pairs]
+    float* loss;          // [rows] or [pairs]
+    float* logp;          // [rows]
+    float* lse;           // [rows]
+    void* grad;           // [rows, V], rows `grad_ld` elements apart, or nullptr
+    long long grad_ld;
+    int32_t* err_flag;
+    int lg = 0, per = 0, ring = 0;  // the split of a row, set by the launcher
+};
+enum class TokenLossPass { kLoss, kGrad };  // the loss (with grad when it is set); grad alone
+cudaError_t launch_policy_loss(const TokenLossArgs& a, TokenLossPass pass, int bf16,
+                               cudaStream_t stream, int num_sms);
+cudaError_t launch_preference_loss(const TokenLossArgs& a, TokenLossPass pass, int bf16,
+                                   cudaStream_t stream, int num_sms);
+
+// Steps on the weights of many tensors (adamw.cu).  The arrays have an entry for each tensor and
+// are read during the call.
+struct GradNormArgs {
+    int count;
+    const void* const* grads;
+    const long long* sizes;
+    double* workspace;   // grad_norm_chunks(...) values
+    float* norm;
+};
+long long grad_norm_chunks(int count, const long long* sizes);
+cudaError_t launch_grad_norm(const GradNormArgs& a, int grad_bf16, cudaStream_t stream);
+
+struct AdamwArgs {
+    int count;
+    void* const* params;
+    const void* const* grads;
+    void* const* exp_avg;
+    void* const* exp_avg_sq;
+    float* const* master;             // or nullptr
+    uint8_t* const* exp_avg_scale;    // 8-bit states, or nullptr
+    uint8_t* const* exp_avg_sq_scale;
+    const long long* sizes;
+    const int32_t* step_at;           // on the device, or nullptr: `step`
+    const float* lr_at;               // on the device, or nullptr: `lr`
+    int step;
+    double lr, beta1, beta2, eps, weight_decay;
+    const float* norm;                // on the device, or nullptr
+    double max_norm;                  // 0: no limit
+    double grad_scale;
+    int by_chance;
+    unsigned long long seed;
+};
+cudaError_t launch_adamw(const AdamwArgs& a, int param_bf16, int grad_bf16, cudaStream_t stream);
+
+// 8-bit optimizer states to values and back (to the nearest).
+cudaError_t launch_state_decode(const uint8_t* codes, const uint8_t* scale, long long n, int squares,
+                                void* out, int out_bf16, cudaStream_t stream);
+cudaError_t launch_state_encode(const void* values, int in_bf16, long long n, int squares,
+                                uint8_t* codes, uint8_t* scale, cudaStream_t stream);
+
 // Measurement aid: random-row gather (probe.cu).  out[i] = XOR of the 32-bit
 // words of row ids[i] (ids clamped into [0, rows)); row_bytes a power of two
 // in [16, 512].

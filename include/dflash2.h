@@ -405,6 +405,187 @@ int dflash2_distill_backward(const float* grad_loss, const void* logits, long lo
                              int32_t* err_flag, void* stream);
 
 /*
+ * The clipped policy loss with a KL term, of every row of a policy's logits at the token that
+ * was drawn there, and when grad is not NULL its gradient, in one pass over the rows: the
+ * training of a draft head on rewards (its drafts' acceptance), beside dflash2_distill.  For
+ * row r with logits z, token t, A = advantage, T = temperature:
+ *   lse  = log sum_j exp(z_j / T),   logp = z_t / T - lse
+ *   rho  = exp(logp - old_logp),     d = ref_logp - logp
+ *   loss = weight * (kl_coef * (exp(d) - d - 1)
+ *                    - min(rho * A, clamp(rho, 1 - clip_low, 1 + clip_high) * A))
+ *   g    = d loss / d logp = weight * (kl_coef * (1 - exp(d)) - (A * rho, or 0 where the clamp holds))
+ *   grad_j = g * ((j == t) - exp(z_j / T - lse)) / T
+ * exp(d) - d - 1 is an estimate of the Kullback-Leibler divergence from the reference by the
+ * drawn token alone.  Fold a mean or position weights into weight.
+ *   logits  [rows,V] in `dtype`, element (r, j) at r * ld + j, ld >= V; any start
+ *           aligned to an element
+ *   tokens  [rows] int32; negative: the row is not counted
+ *   old_logp, advantage [rows] fp32; ref_logp [rows] fp32, or NULL where kl_coef is 0
+ *   weight  [rows] fp32, or NULL for 1
+ *   loss, logp, lse [rows] fp32 out
+ *   grad    [rows,V] in `dtype` out (rounded once), rows grad_ld elements apart, or NULL;
+ *           may be the logits themselves (same pointer and spacing).  Stores are 16 bytes
+ *           wide where a row of grad and of logits start at the same place modulo 16
+ *           bytes, single elements otherwise
+ *   err_flag one device int32 or NULL: DF2_FLAG_BAD_ID when a token is >= V (not counted)
+ * A row that is not counted, or has weight 0, is not read: its loss, logp, lse and gradient are
+ * 0.  clip_low and clip_high may be infinite (no limit).  A = 0 leaves the first term out,
+ * kl_coef = 0 the second, whatever rho and d are.  A token at -inf in z has logp -inf
+ * and rho 0; a row with no z above -inf counts as a softmax that is 0 everywhere (lse -inf, logp
+ * -inf).  A row whose g is 0 has gradient 0.  Otherwise NaN or +inf in a row's z makes its outputs
+ * NaN, and an infinite g what the formula gives.  Sums are in fp32 or more.  rows == 0 launches
+ * nothing.
+ * INVALID_ARG: rows < 0; V <= 0; ld or grad_ld < V; a temperature that is not positive and
+ * finite; clip_low or clip_high negative or NaN; kl_coef not finite; NULL required pointer;
+ * misalignment (vectors of one value per row: 4 bytes); an output overlapping another buffer,
+ * other than grad in place.  UNSUPPORTED: V > 2^28; rows > 2^24.
+ */
+int dflash2_policy_loss(const void* logits, long long ld, const int32_t* tokens,
+                        const float* old_logp, const float* advantage, const float* ref_logp,
+                        const float* weight, int rows, int V, float temperature, float clip_low,
+                        float clip_high, float kl_coef, int dtype, float* loss, float* logp,
+                        float* lse, void* grad, long long grad_ld, int32_t* err_flag,
+                        void* stream);
+
+/*
+ * The gradient of dflash2_policy_loss alone, times an upstream gradient known only after the
+ * loss: grad_loss [rows] fp32; logp, lse [rows] as dflash2_policy_loss wrote them; the rest as
+ * there.  Where |lse| is 256 or more, or infinite, its fp32 rounding would show in the
+ * gradient: the row's sum is taken again from the logits.  A row with grad_loss or weight 0 is
+ * not read and its gradient is 0.
+ */
+int dflash2_policy_loss_backward(const float* grad_loss, const void* logits, long long ld,
+                                 const int32_t* tokens, const float* old_logp,
+                                 const float* advantage, const float* ref_logp,
+                                 const float* weight, const float* logp, const float* lse,
+                                 int rows, int V, float temperature, float clip_low,
+                                 float clip_high, float kl_coef, int dtype, void* grad,
+                                 long long grad_ld, int32_t* err_flag, void* stream);
+
+/*
+ * The preference loss of pairs of sequences by their log ratios to a reference, on the
+ * policy's logits at the sequences' tokens, and when grad is not NULL its gradient.  Sequence s
+ * has the rows offsets[s] to offsets[s+1] - 1; pair i consists of the chosen sequence i and
+ * the rejected one pairs + i.  With logp as in dflash2_policy_loss (T = 1), over the rows whose
+ * token is not negative (a prompt's tokens are given as -1):
+ *   S_s  = sum of logp over the sequence's rows (average != 0: their mean; without rows: 0)
+ *   m    = beta * ((S_c - ref_c) - (S_r - ref_r)) - margin
+ *   loss = weight * ((1 - e) * log(1 + exp(-m)) + e * log(1 + exp(m)))      (e = label_smoothing)
+ *   d loss / d S_c = -beta * weight * ((1 - e) / (1 + exp(m)) - e / (1 + exp(-m))) = -d loss / d S_r
+ *   grad_j = d loss / d S (/ the number of rows) * ((j == t) - exp(z_j - lse))
+ *   logits, ld, dtype, grad, grad_ld, err_flag as in dflash2_policy_loss; tokens [rows] int32
+ *   offsets  [2*pairs+1] int32, not falling, in [0, rows]
+ *   ref_logp [2*pairs] fp32, the reference's S (sums or means alike), or NULL for 0
+ *   weight   [pairs] fp32, or NULL for 1
+ *   loss [pairs], seq_logp [2*pairs] (S), logp [rows], lse [rows] fp32 out
+ * Rows with a negative token have logp, lse and gradient 0 and are not read; so has a
+ * token >= V, which is flagged.  A row in no sequence has its logp and lse, and gradient 0.  A
+ * pair with weight 0 has loss and gradient 0.  Offsets that fall or leave [0, rows] are
+ * flagged (DF2_FLAG_BAD_ID) and taken into range: no memory outside is touched, the outputs
+ * of their pairs are undefined.  With the gradient the rows are read twice, as every row of
+ * a pair weighs on every other's gradient.  Sums over rows are in 64 bits, in an order that
+ * depends on nothing but the sequence.  rows == 0 and pairs == 0 launches nothing.
+ * INVALID_ARG and UNSUPPORTED as dflash2_policy_loss; pairs < 0; beta or margin not finite;
+ * label_smoothing outside [0, 1]; UNSUPPORTED: pairs > 2^24.
+ */
+int dflash2_preference_loss(const void* logits, long long ld, const int32_t* tokens,
+                            const int32_t* offsets, const float* ref_logp, const float* weight,
+                            int rows, int V, int pairs, float beta, float label_smoothing,
+                            float margin, int average, int dtype, float* loss, float* seq_logp,
+                            float* logp, float* lse, void* grad, long long grad_ld,
+                            int32_t* err_flag, void* stream);
+
+/*
+ * The gradient of dflash2_preference_loss alone: grad_loss [pairs] fp32; seq_logp [2*pairs]
+ * and lse [rows] as dflash2_preference_loss wrote them; the rest as there.  A far lse as
+ * in dflash2_policy_loss_backward.
+ */
+int dflash2_preference_loss_backward(const float* grad_loss, const void* logits, long long ld,
+                                     const int32_t* tokens, const int32_t* offsets,
+                                     const float* ref_logp, const float* weight,
+                                     const float* seq_logp, const float* lse, int rows, int V,
+                                     int pairs, float beta, float label_smoothing, float margin,
+                                     int average, int dtype, void* grad, long long grad_ld,
+                                     int32_t* err_flag, void* stream);
+
+/*
+ * The 2-norm of many tensors' gradients together, as clipping needs it:
+ *   norm = sqrt(sum over all elements of all tensors of g^2)
+ *   grads      count device pointers (an array on the host, read during the call) to
+ *              tensors of grad_dtype, aligned to an element; sizes: their elements (host)
+ *   workspace  device memory of dflash2_grad_norm_workspace_bytes(count, sizes) bytes, 8-byte
+ *              aligned, not shared with a call that may run at the same time
+ *   norm       one fp32 out
+ * Squares are added in fp32 over 2048 values and in 64 bits beyond, in an order that depends on
+ * the sizes alone; where they leave fp32's range, in 64 bits altogether.  A NaN or an infinity
+ * makes the norm NaN or infinite.  count == 0, or tensors without elements alone: norm 0.
+ * INVALID_ARG: count < 0; a negative size; NULL required pointer; bad dtype; misalignment; too
+ * small a workspace; norm or workspace overlapping a gradient or one another.  UNSUPPORTED: a
+ * tensor of more than 2^40 elements.  The workspace's size is 0 for sizes that are refused.
+ */
+size_t dflash2_grad_norm_workspace_bytes(int count, const int64_t* sizes);
+int dflash2_grad_norm(int count, const void* const* grads, const int64_t* sizes, int grad_dtype,
+                      void* workspace, size_t workspace_bytes, float* norm, void* stream);
+
+/*
+ * One AdamW step over many tensors, in place:
+ *   g' = g * grad_scale * min(1, max_norm / (norm * |grad_scale|))
+ *   m  = beta1 * m + (1 - beta1) * g',    v = beta2 * v + (1 - beta2) * g'^2
+ *   p  = p - lr * weight_decay * p
+ *          - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32, with p from `master` where there are such copies, and p rounded to its type.
+ *   params, grads, exp_avg (m), exp_avg_sq (v): count device pointers each (arrays on the host,
+ *           read during the call); sizes [count]: elements of each tensor (host); all params of
+ *           one type, all grads of one type
+ *   master  NULL, or count pointers to fp32 copies of bf16 parameters: they take the step
+ *   exp_avg_scale, exp_avg_sq_scale: both NULL (states in fp32), or count pointers each to
+ *           (size + 31) / 32 bytes: states in 8 bits, one byte an element.  Elements 32 b to 32 b +
+ *           31 share scale byte b: value = code's value * 2^(scale - 127).  exp_avg's code: sign
+ *           bit, 4 bits of exponent, 3 of mantissa, i.e. (-1)^sign * (1 + f/8) * 2^(e - 7), e = 0:
+ *           f/8 * 2^-6.  exp_avg_sq's: 5 bits of exponent, 3 of mantissa, (1 + f/8) * 2^(e - 15), e
+ *           = 0: f/8 * 2^-14.  All bytes 0 is a state of zeros.  The step takes m and v before
+ *           they are rounded; a v above 0 keeps a code above 0.  A block with an infinite or NaN
+ *           value gets scale 255 and codes 0, which read as NaN
+ *   step    number of the step, 1 for the first; step_at: not NULL, one device int32 that holds
+ *           it (for a captured graph that is replayed).  lr_at likewise, one fp32 for lr
+ *   norm    NULL, or one device fp32, the gradients' norm: where it is not finite nothing is
+ *           changed.  max_norm > 0 clips by it; 0: no limit
+ *   by_chance  0: all rounding is to the nearest.  Else 8-bit states, and bf16 parameters without
+ *           master copies, are rounded up or down with odds by the distance, by bits made of
+ *           seed, step, the tensor's place in the list and the element's place in it: the
+ *           same call gives the same bits.  With 8-bit states this is what lets v follow: it moves
+ *           by 1 - beta2 of itself a step, a 30th of half of a code's distance, and to the nearest
+ *           it would stay where it is
+ * Vectors of 8 elements are taken at once where all of a tensor's pointers are aligned to 16
+ * bytes (8-bit states: 8), single elements otherwise.
+ * INVALID_ARG: count < 0; a negative size; NULL required pointer; bad dtype; misalignment to an
+ * element; beta1 or beta2 outside [0, 1); eps not positive (in fp32) or not finite; lr, weight_decay
+ * or grad_scale not finite; max_norm negative or NaN, or without norm; step < 1; one scale
+ * array without the other; master with fp32 parameters; a tensor that is written overlapping any
+ * other (or listed twice).  UNSUPPORTED: a tensor of more than 2^40 elements.
+ */
+int dflash2_adamw(int count, void* const* params, const void* const* grads, void* const* exp_avg,
+                  void* const* exp_avg_sq, float* const* master, uint8_t* const* exp_avg_scale,
+                  uint8_t* const* exp_avg_sq_scale, const int64_t* sizes, int param_dtype,
+                  int grad_dtype, const int32_t* step_at, const float* lr_at, int step, double lr,
+                  double beta1, double beta2, double eps, double weight_decay, const float* norm,
+                  double max_norm, double grad_scale, int by_chance, uint64_t seed, void* stream);
+
+/*
+ * 8-bit states (as dflash2_adamw keeps them) to values and back, for checkpoints and for going on
+ * from states in fp32.  squares: 0 for exp_avg's codes, else exp_avg_sq's (a negative value there
+ * counts as NaN).  codes [n], scale [(n + 31) / 32] bytes; values [n] in the given dtype.  Decoded
+ * values are exact in both types, but for bf16's range; encoding rounds to the nearest (a square above
+ * 0 to a code above 0).  n == 0 launches nothing.
+ * INVALID_ARG: n < 0; NULL; bad dtype; misalignment to an element; an output overlapping another
+ * buffer.  UNSUPPORTED: n > 2^40.
+ */
+int dflash2_state_decode(const uint8_t* codes, const uint8_t* scale, int64_t n, int squares,
+                         int out_dtype, void* out, void* stream);
+int dflash2_state_encode(const void* values, int in_dtype, int64_t n, int squares, uint8_t* codes,
+                         uint8_t* scale, void* stream);
+
+/*
  * Measurement aid (no counterpart in the DFlash2 pull request): the rate at
  * which this GPU gathers random rows, the bound the edge kernel's codebook
  * gathers work against.  For i < n_ids:
