@@ -16,8 +16,8 @@ such rows, the gradients' norm, and AdamW over many tensors with states in 32 or
 8 bits.  This package is the thin Python binding over it.
 """
 from .binding import (Dflash2Error, adamw, chain, distill, distill_backward, dynconv,  # noqa: F401
-                      dynconv_predicted, edges, grad_norm, lib, policy_loss,
-                      policy_loss_backward, predict_delta, preference_loss,
+                      dynconv_predicted, edges, grad_norm, grad_norm_workspace_bytes, lib,
+                      policy_loss, policy_loss_backward, predict_delta, preference_loss,
                       preference_loss_backward, probe_gather, project, project_noalloc,
                       project_workspace_bytes, sample, select, select_plan, state_decode,
                       state_encode, take_device_faults, topk, version)

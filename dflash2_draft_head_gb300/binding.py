@@ -7,6 +7,7 @@ fallback: if the library is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import operator
 import os
@@ -535,10 +536,14 @@ def _on(t, name, dtype, shape, index):
     raise ValueError(f"{name} must be on device cuda:{index}, got {t.device}")
 
 
-def _out_on(t, name, dtype, shape, dev):
-    """(tensor, pointer) of an output, allocated for None."""
+def _out_on(t, name, dtype, shape, dev, like=None):
+    """(tensor, pointer) of an output, allocated for None (from `like`, a contiguous tensor of
+    this type and shape, where there is one: that takes less time)."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        if like is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            t = torch.empty_like(like)
         return t, t.data_ptr()
     return t, _on(t, name, dtype, shape, dev.index)
 
@@ -571,10 +576,10 @@ def policy_loss(logits, tokens, old_logp, advantage, ref_logp=None, temperature=
     ins = (_on(tokens, "tokens", torch.int32, shape, at), _on(old_logp, "old_logp", f32, shape, at),
            _on(advantage, "advantage", f32, shape, at), _on(ref_logp, "ref_logp", f32, shape, at),
            _on(weight, "weight", f32, shape, at))
-    loss, loss_ptr = _out_on(loss, "loss", f32, shape, dev)
-    logp, logp_ptr = _out_on(logp, "logp", f32, shape, dev)
-    lse, lse_ptr = _out_on(lse, "lse", f32, shape, dev)
-    flag = _on(err_flag, "err_flag", torch.int32, (1,), at)
+    loss, loss_ptr = _out_on(loss, "loss", f32, shape, dev, old_logp)
+    logp, logp_ptr = _out_on(logp, "logp", f32, shape, dev, old_logp)
+    lse, lse_ptr = _out_on(lse, "lse", f32, shape, dev, old_logp)
+    flag = None if err_flag is None else _on(err_flag, "err_flag", torch.int32, (1,), at)
     given = isinstance(grad, torch.Tensor)
     grad, grad_ptr, grad_ld = _grad_on(grad, logits, ld)
     _launch(at, lib().dflash2_policy_loss, logits.data_ptr(), ld, *ins, rows, V, temperature,
@@ -637,10 +642,10 @@ def preference_loss(logits, tokens, offsets, ref_logp=None, beta=0.1, label_smoo
            _on(offsets, "offsets", torch.int32, (2 * pairs + 1,), at),
            _on(ref_logp, "ref_logp", f32, (2 * pairs,), at),
            _on(weight, "weight", f32, (pairs,), at))
-    loss, loss_ptr = _out_on(loss, "loss", f32, (pairs,), dev)
-    seq_logp, seq_ptr = _out_on(seq_logp, "seq_logp", f32, (2 * pairs,), dev)
+    loss, loss_ptr = _out_on(loss, "loss", f32, (pairs,), dev, weight)
+    seq_logp, seq_ptr = _out_on(seq_logp, "seq_logp", f32, (2 * pairs,), dev, ref_logp)
     logp, logp_ptr = _out_on(logp, "logp", f32, shape, dev)
-    lse, lse_ptr = _out_on(lse, "lse", f32, shape, dev)
+    lse, lse_ptr = _out_on(lse, "lse", f32, shape, dev, logp)
     flag = _on(err_flag, "err_flag", torch.int32, (1,), at)
     given = isinstance(grad, torch.Tensor)
     grad, grad_ptr, grad_ld = _grad_on(grad, logits, ld)
@@ -682,55 +687,78 @@ _data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
 _dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape")
 
 
-def _many(ts, name, dtype, index, shapes):
-    """The tensors' pointers as a C array: of one type, on one device, contiguous, of these
-    shapes; None for None."""
-    if ts is None:
-        return None
-    if len(ts) != len(shapes):
-        raise ValueError(f"{name} has {len(ts)} tensors, {len(shapes)} are needed")
-    if set(map(_device_of, ts)) != {index}:
-        raise ValueError(f"{name} must be CUDA tensors on one device, that of all others")
-    if not all(map(_is_contiguous, ts)):
-        raise ValueError(f"{name} must be contiguous")
-    if set(map(_dtype_of, ts)) != {dtype}:
-        raise TypeError(f"{name} must be {dtype} all")
-    if list(map(_shape_of, ts)) != shapes:
-        raise ValueError(f"{name} must have the shapes {[tuple(s) for s in shapes]}")
-    return (ctypes.c_void_p * len(ts))(*map(_data_ptr, ts))
+class _Lists:
+    """Lists of tensors, one tensor of every list for each parameter, as arrays of pointers for a C
+    entry.  The checks run over all of them at once, by functions that need no Python in
+    between; only a failing one asks which list it was."""
+
+    def __init__(self, **lists):
+        self.lists = {k: v for k, v in lists.items() if v is not None}
+        self.n = len(next(iter(self.lists.values())))
+        for name, ts in self.lists.items():
+            if len(ts) != self.n:
+                raise ValueError(f"{name} has {len(ts)} tensors, {self.n} are needed")
+            for t in ts:
+                if not isinstance(t, torch.Tensor):
+                    raise TypeError(f"{name} must be tensors, got {type(t).__name__}")
+        self.all = [t for ts in self.lists.values() for t in ts]
+        self.index = self.all[0].get_device()
+        if self.index < 0 or set(map(_device_of, self.all)) != {self.index}:
+            self._blame(lambda t: t.get_device() == self.index >= 0,
+                        "must be CUDA tensors on one device, that of all others")
+        if not all(map(_is_contiguous, self.all)):
+            self._blame(_is_contiguous, "must be contiguous")
+
+    def _blame(self, fine, what, error=ValueError):
+        raise error(next(f"{name} {what}" for name, ts in self.lists.items()
+                         if not all(map(fine, ts))))
+
+    def dtype(self, name, dtype=None):
+        """The type of a list: of all its tensors, and the given one, if any."""
+        ts = self.lists[name]
+        dtype = ts[0].dtype if dtype is None else dtype
+        if set(map(_dtype_of, ts)) != {dtype}:
+            raise TypeError(f"{name} must be {dtype} all")
+        return dtype
+
+    def elements(self, name, want):
+        if list(map(_numel, self.lists[name])) != want:
+            raise ValueError(f"{name} must have {want} elements")
+
+    def arrays(self, sizes):
+        """(what has to live until the call returns, the sizes' address, the lists' by name)."""
+        held = array.array("Q", [*sizes, *map(_data_ptr, self.all)])
+        at, step = held.buffer_info()[0], 8 * self.n
+        return held, at, {name: at + step * (k + 1) for k, name in enumerate(self.lists)}
 
 
-def _first(ts, name):
-    """The first of a list that is not empty, with nothing but tensors in it."""
-    for t in ts:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be tensors, got {type(t).__name__}")
-    return ts[0]
-
-
-def _sizes(ts):
-    return (ctypes.c_int64 * len(ts))(*map(_numel, ts))
+def grad_norm_workspace_bytes(grads) -> int:
+    """Bytes of workspace that grad_norm() needs for these gradients."""
+    sizes = array.array("Q", map(_numel, grads))
+    return int(lib().dflash2_grad_norm_workspace_bytes(len(grads), sizes.buffer_info()[0]))
 
 
 def grad_norm(grads, out=None, workspace=None):
     """The 2-norm of a list of gradients together (fp32 or bf16, one type) -> [1] fp32, without
-    waiting for it.  workspace: a uint8 CUDA tensor, allocated for None; calls that may run at
-    the same time each need one of their own."""
+    waiting for it.  workspace: a uint8 CUDA tensor of at least grad_norm_workspace_bytes(grads)
+    bytes, allocated for None; calls that may run at the same time each need one of their own."""
     if len(grads) == 0:
         raise ValueError("grad_norm needs at least one tensor")
-    first = _first(grads, "grads")
-    dev = first.device
-    ptrs = _many(grads, "grads", first.dtype, first.get_device(), list(map(_shape_of, grads)))
-    if dev.type != "cuda":
-        raise ValueError("grads must be CUDA tensors")
-    sizes, L = _sizes(grads), lib()
+    ts, L = _Lists(grads=grads), lib()
+    code = _code(ts.dtype("grads"))
+    dev = ts.all[0].device
+    held, sizes, ptrs = ts.arrays(map(_numel, grads))
     out, out_ptr = _out_on(out, "out", torch.float32, (1,), dev)
-    need = L.dflash2_grad_norm_workspace_bytes(len(grads), sizes)
-    if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-    ws = _on(workspace, "workspace", torch.uint8, workspace.shape, dev.index)
-    _launch(dev.index, L.dflash2_grad_norm, len(grads), ptrs, sizes, _code(first.dtype), ws,
-            workspace.numel(), out_ptr)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws, ws_bytes = _on(workspace, "workspace", torch.uint8, workspace.shape, ts.index), \
+            workspace.numel()
+    else:
+        ws_bytes = L.dflash2_grad_norm_workspace_bytes(ts.n, sizes)
+        if ws_bytes > 0:
+            workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=dev)
+            ws = workspace.data_ptr()
+    _launch(ts.index, L.dflash2_grad_norm, ts.n, ptrs["grads"], sizes, code, ws, ws_bytes, out_ptr)
     return out
 
 
@@ -738,7 +766,7 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, beta1=0.9, beta2=0.999, 
           weight_decay=0.01, master=None, exp_avg_scale=None, exp_avg_sq_scale=None, norm=None,
           max_norm=None, grad_scale=1.0, seed=None):
     """One AdamW step over lists of tensors, in place: params and grads (each fp32 or bf16, one
-    type a list), exp_avg and exp_avg_sq fp32, or uint8 with the lists exp_avg_scale and
+    type a list), exp_avg and exp_avg_sq fp32 of as many elements, or uint8 with the lists exp_avg_scale and
     exp_avg_sq_scale ([(numel + 31) // 32] uint8 each): states in 8 bits, zeros to begin with
     (state_encode and state_decode go from values to them and back).  master: fp32 copies of bf16
     params, which take the step.  step: the step's number, 1 for the first, or an int32 CUDA
@@ -751,35 +779,40 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, beta1=0.9, beta2=0.999, 
         if any(len(v) for v in (grads, exp_avg, exp_avg_sq)):
             raise ValueError("params is empty, other lists are not")
         return
-    first = _first(params, "params")
-    at, shapes, f32 = first.get_device(), list(map(_shape_of, params)), torch.float32
-    if at < 0:
-        raise ValueError("params must be CUDA tensors")
-    if len(grads) == 0:
-        raise ValueError(f"grads has 0 tensors, {len(shapes)} are needed")
+    ts = _Lists(params=params, grads=grads, exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, master=master,
+                exp_avg_scale=exp_avg_scale, exp_avg_sq_scale=exp_avg_sq_scale)
+    f32, at = torch.float32, ts.index
     small = exp_avg_scale is not None or exp_avg_sq_scale is not None
     state = torch.uint8 if small else f32
-    ptrs = [_many(params, "params", first.dtype, at, shapes),
-            _many(grads, "grads", _first(grads, "grads").dtype, at, shapes),
-            _many(exp_avg, "exp_avg", state, at, shapes),
-            _many(exp_avg_sq, "exp_avg_sq", state, at, shapes),
-            _many(master, "master", f32, at, shapes)]
-    sizes = _sizes(params)
-    blocks = [(-(-n // 32),) for n in sizes] if small else None
-    ptrs += [_many(exp_avg_scale, "exp_avg_scale", torch.uint8, at, blocks),
-             _many(exp_avg_sq_scale, "exp_avg_sq_scale", torch.uint8, at, blocks)]
+    param_code, grad_code = _code(ts.dtype("params")), _code(ts.dtype("grads"))
+    if list(map(_shape_of, grads)) != list(map(_shape_of, params)):
+        raise ValueError("grads must have the shapes of params")
+    sizes = list(map(_numel, params))
+    for name, dtype in (("exp_avg", state), ("exp_avg_sq", state), ("master", f32)):
+        if name in ts.lists:
+            ts.dtype(name, dtype)
+            ts.elements(name, sizes)
+    if small:
+        blocks = [-(-n // 32) for n in sizes]
+        for name in ("exp_avg_scale", "exp_avg_sq_scale"):
+            if name not in ts.lists:
+                raise ValueError("states in 8 bits need exp_avg_scale and exp_avg_sq_scale")
+            ts.dtype(name, torch.uint8)
+            ts.elements(name, blocks)
     step_at, step = _setting_on(step, "step", torch.int32, at)
     if step_at is None and not 1 <= step < 1 << 31:  # the entry takes 32 bits
         raise ValueError(f"step={step}: the first step is 1, the last one 2^31 - 1")
     lr_at, lr = _setting_on(lr, "lr", f32, at)
     norm_at = _on(norm, "norm", f32, (1,), at)
-    for ts in (params, exp_avg, exp_avg_sq, master, exp_avg_scale, exp_avg_sq_scale):
-        if ts is not None:  # before the launch, which an inference tensor outside its mode forbids
-            increment_version(ts)
-    _launch(at, lib().dflash2_adamw, len(params), *ptrs, sizes, _code(first.dtype),
-            _code(grads[0].dtype), step_at, lr_at, step, lr, beta1, beta2, eps, weight_decay,
-            norm_at, 0.0 if max_norm is None else max_norm, grad_scale, seed is not None,
-            0 if seed is None else seed & 0xffffffffffffffff)
+    for name, written in ts.lists.items():
+        if name != "grads":  # before the launch: not allowed for an inference tensor outside its mode
+            increment_version(written)
+    held, sizes_at, ptr = ts.arrays(sizes)
+    _launch(at, lib().dflash2_adamw, ts.n, ptr["params"], ptr["grads"], ptr["exp_avg"],
+            ptr["exp_avg_sq"], ptr.get("master"), ptr.get("exp_avg_scale"),
+            ptr.get("exp_avg_sq_scale"), sizes_at, param_code, grad_code, step_at, lr_at, step, lr,
+            beta1, beta2, eps, weight_decay, norm_at, 0.0 if max_norm is None else max_norm,
+            grad_scale, seed is not None, 0 if seed is None else seed & 0xffffffffffffffff)
 
 
 def _setting_on(v, name, dtype, index):

@@ -13,8 +13,10 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
+#include "rows.cuh"
 #include "state8.cuh"
 
 namespace df2 {
@@ -27,72 +29,93 @@ constexpr int kTurn = kThreads * kVec;
 // Tensors of a launch: few with short parameters, or as many as 32 KB of parameters hold.
 constexpr int kFew = 16, kMany = 384;
 
-__device__ __forceinline__ void load_vec(const float* p, float (&x)[kVec]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&x)[kVec]) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[2 * j] = __uint_as_float(w[j] << 16);
-        x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+// Eight neighbours of a tensor as they lie in memory.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
     }
-}
-__device__ __forceinline__ void load_vec(const uint8_t* p, uint32_t (&x)[kVec]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[j] = v.x >> 8 * j & 0xffu;
-        x[j + 4] = v.y >> 8 * j & 0xffu;
+    __device__ __forceinline__ void store(float* p) const {
+        __stcs(reinterpret_cast<float4*>(p), a);
+        __stcs(reinterpret_cast<float4*>(p) + 1, b);
     }
-}
-__device__ __forceinline__ void store_vec(float* p, const float (&x)[kVec]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const __nv_bfloat16 (&x)[kVec]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 h = __halves2bfloat162(x[2 * j], x[2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    __device__ __forceinline__ void get(float (&x)[kVec]) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void store_vec(uint8_t* p, const uint32_t (&x)[kVec]) {
-    uint2 v = make_uint2(0, 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v.x |= x[j] << 8 * j;
-        v.y |= x[j + 4] << 8 * j;
+    __device__ __forceinline__ void set(const float (&x)[kVec]) {
+        a = make_float4(x[0], x[1], x[2], x[3]);
+        b = make_float4(x[4], x[5], x[6], x[7]);
     }
-    *reinterpret_cast<uint2*>(p) = v;
-}
-__device__ __forceinline__ float to_value(float x) { return x; }
-__device__ __forceinline__ float to_value(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ uint32_t to_value(uint8_t x) { return x; }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        a = __ldcs(reinterpret_cast<const uint4*>(p));
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+        __stcs(reinterpret_cast<uint4*>(p), a);
+    }
+    __device__ __forceinline__ void get(float (&x)[kVec]) const { unpack(a, x); }
+    __device__ __forceinline__ void set(const float (&x)[kVec]) { a = pack(x); }
+    // Numbers whose upper halves are to be taken as they are.
+    __device__ __forceinline__ void set_upper(const uint32_t (&x)[kVec]) {
+        a = make_uint4(__byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632),
+                       __byte_perm(x[4], x[5], 0x7632), __byte_perm(x[6], x[7], 0x7632));
+    }
+};
+template <>
+struct alignas(8) Vec<uint8_t> {
+    uint32_t a[2];
+    __device__ __forceinline__ void load(const uint8_t* p) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
+        a[0] = v.x;
+        a[1] = v.y;
+    }
+    __device__ __forceinline__ void store(uint8_t* p) const {
+        __stcs(reinterpret_cast<uint2*>(p), make_uint2(a[0], a[1]));
+    }
+    // Byte j in bits 24 to 31, something below it.
+    __device__ __forceinline__ uint32_t high(int j) const { return a[j / 4] << (24 - 8 * (j & 3)); }
+    // From bits 24 to 31 of numbers.
+    __device__ __forceinline__ void set_high(const uint32_t (&x)[kVec]) {
+#pragma unroll
+        for (int q = 0; q < kVec / 4; ++q) {
+            const uint32_t* y = x + 4 * q;
+            a[q] = __byte_perm(__byte_perm(y[0], y[1], 0x0073), __byte_perm(y[2], y[3], 0x0073), 0x5410);
+        }
+    }
+};
 
-// Elements [i, i + 8) of n, zeros beyond; `wide`: the tensor's vectors are aligned.
-template <typename T, typename X>
-__device__ __forceinline__ void load(const T* p, long long i, long long n, bool wide, X (&x)[kVec]) {
-    if (wide && i + kVec <= n) {
-        load_vec(p + i, x);
+// Elements [i, i + 8) of n: at once where they are known to be there and aligned (FULL), else one
+// by one, zeros beyond n.
+template <bool FULL, typename T>
+__device__ __forceinline__ Vec<T> load(const T* p, long long i, long long n) {
+    Vec<T> o;
+    if (FULL) {
+        o.load(p + i);
     } else {
+        alignas(16) T x[kVec];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) x[j] = i + j < n ? to_value(p[i + j]) : X(0);
+        for (int j = 0; j < kVec; ++j) x[j] = i + j < n ? p[i + j] : T(0.f);
+        o = *reinterpret_cast<const Vec<T>*>(x);
     }
+    return o;
 }
-template <typename T, typename X>
-__device__ __forceinline__ void store(T* p, long long i, long long n, bool wide, const X (&x)[kVec]) {
-    if (wide && i + kVec <= n) {
-        store_vec(p + i, x);
+template <bool FULL, typename T>
+__device__ __forceinline__ void store(T* p, long long i, long long n, const Vec<T>& o) {
+    if (FULL) {
+        o.store(p + i);
     } else {
+        const T* x = reinterpret_cast<const T*>(&o);
 #pragma unroll
         for (int j = 0; j < kVec; ++j)
-            if (i + j < n) p[i + j] = (T)x[j];
+            if (i + j < n) p[i + j] = x[j];
     }
 }
 
@@ -138,24 +161,41 @@ struct NormBatch {
     double* sums;  // of this launch's chunks
 };
 
+// A chunk's sum of squares, by thread: 64 values in fp32.
+template <bool FULL, typename T>
+__device__ __forceinline__ float thread_squares(const T* g, long long i, long long n) {
+    Vec<T> o[kNormTurns];
+#pragma unroll
+    for (int k = 0; k < kNormTurns; ++k) o[k] = load<FULL>(g, i + (long long)k * kTurn, n);
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kNormTurns; ++k) {
+        float x[kVec];
+        o[k].get(x);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) s[j & 1] = fmaf(x[j], x[j], s[j & 1]);
+    }
+    return s[0] + s[1];
+}
+
 // The sum of a chunk's squares where fp32's is not good: in 64 bits.  By the whole block.
 template <typename T>
-__device__ __noinline__ double far_sum(const T* g, long long lo, long long n, bool wide,
-                                       double* part) {
+__device__ __noinline__ double far_squares(const T* g, long long i, long long n, double* part) {
     double s = 0;
     bool any = false;
-    for (int k = 0; k < kNormTurns; ++k) {
-        float x[kVec];
-        load(g, lo + (long long)k * kTurn + (long long)threadIdx.x * kVec, n, wide, x);
+    for (int turn = 0; turn < 2; ++turn) {
+        for (int k = 0; k < kNormTurns; ++k) {
+            float x[kVec];
+            load<false>(g, i + (long long)k * kTurn, n).get(x);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) any = any || x[j] != 0.f;
-    }
-    if (__syncthreads_or(any) == 0) return 0;
-    for (int k = 0; k < kNormTurns; ++k) {
-        float x[kVec];
-        load(g, lo + (long long)k * kTurn + (long long)threadIdx.x * kVec, n, wide, x);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) s += (double)x[j] * x[j];
+            for (int j = 0; j < kVec; ++j) {
+                if (turn == 0)
+                    any = any || x[j] != 0.f;
+                else
+                    s += (double)x[j] * x[j];
+            }
+        }
+        if (turn == 0 && __syncthreads_or(any) == 0) return 0;
     }
     s = warp_sum(s);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
@@ -165,41 +205,68 @@ __device__ __noinline__ double far_sum(const T* g, long long lo, long long n, bo
     return s;
 }
 
-// The sum of the squares of a chunk: 64 values a thread and 32 threads in fp32, the rest in
-// 64 bits.  Squares leave fp32 from 1.8e19 on and lose bits below 1e-19: a sum outside
-// [1e-24, 1e30] is taken again.
+// The sum of the squares of a chunk, for thread 0: 64 values a thread and 32 threads in fp32, the
+// rest in 64 bits (by one thread: an SM adds two such numbers a cycle).  Squares leave fp32 from
+// 1.8e19 on and lose bits below 1e-19: a chunk whose sum is outside [1e-24, 1e30] is taken again.
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ NormBatch<N> b) {
-    __shared__ double part[kThreads / 32];
+__device__ __forceinline__ double chunk_squares(const NormBatch<N>& b, int chunk, float* part,
+                                                double* far_part) {
     const int tid = threadIdx.x;
-    const NormTensor& t = b.t[tensor_of(b, blockIdx.x)];
+    const NormTensor& t = b.t[tensor_of(b, chunk)];
     const T* g = static_cast<const T*>(t.g);
-    const long long lo = (long long)((int)blockIdx.x - t.first) * kNormChunk, n = t.n;
-    const bool wide = t.wide != 0;
-    float s[2] = {0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < kNormTurns; ++k) {
-        float x[kVec];
-        load(g, lo + (long long)k * kTurn + (long long)tid * kVec, n, wide, x);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) s[j & 1] = fmaf(x[j], x[j], s[j & 1]);
-    }
-    const float sum = warp_sum(s[0] + s[1]);
+    const long long lo = (long long)(chunk - t.first) * kNormChunk, n = t.n;
+    const long long i = lo + (long long)tid * kVec;
+    const float sum = warp_sum(t.wide != 0 && lo + kNormChunk <= n
+                                   ? thread_squares<true>(g, i, n)
+                                   : thread_squares<false>(g, i, n));
     if ((tid & 31) == 0) part[tid >> 5] = sum;
     __syncthreads();
-    double all = 0;
+    float all = 0.f;
     for (int w = 0; w < kThreads / 32; ++w) all += part[w];
-    if (!(all >= 1e-24 && all <= 1e30)) {
-        __syncthreads();
-        all = far_sum(g, lo, n, wide, part);
-    }
-    if (tid == 0) b.sums[blockIdx.x] = all;
+    if (!(all >= 1e-24f && all <= 1e30f)) return far_squares(g, i, n, far_part);
+    double exact = 0;
+    if (tid == 0)
+        for (int w = 0; w < kThreads / 32; ++w) exact += part[w];
+    return exact;
+}
+
+// One CTA a chunk: 40.4 M bf16 gradients in 13 us, 136 M fp32 ones in 81 us (6.7 TB/s).
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant__ NormBatch<N> b) {
+    __shared__ float part[kThreads / 32];
+    __shared__ double far_part[kThreads / 32];
+    griddep_launch_dependents();
+    const double s = chunk_squares<T>(b, blockIdx.x, part, far_part);
+    if (threadIdx.x == 0) b.sums[blockIdx.x] = s;
+}
+
+// Few chunks: one cluster, whose first CTA adds up what the others have written to its shared
+// memory; a launch less.
+constexpr int kNormCluster = 8;
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads)
+    norm_few_kernel(const __grid_constant__ NormBatch<N> b, int chunks, float* norm) {
+    __shared__ float part[kThreads / 32];
+    __shared__ double far_part[kThreads / 32];
+    __shared__ double sums[kNormCluster];
+    const int rank = (int)cluster_ctarank();
+    cluster_arrive();
+    const double s = rank < chunks ? chunk_squares<T>(b, rank, part, far_part) : 0;
+    cluster_wait();  // every CTA has started
+    if (threadIdx.x == 0)
+        st_cluster_b64(map_cluster(smem_u32(&sums[rank]), 0), __builtin_bit_cast(uint64_t, s));
+    cluster_sync();
+    if (rank != 0 || threadIdx.x != 0) return;
+    double all = 0;
+    for (int k = 0; k < kNormCluster; ++k) all += sums[k];
+    *norm = (float)sqrt(all);
 }
 
 constexpr int kJoinThreads = 512;
 __global__ void __launch_bounds__(kJoinThreads)
     norm_join_kernel(const double* sums, long long n, float* norm) {
     __shared__ double part[kJoinThreads / 32];
+    griddep_wait();
     double s = 0;
     for (long long i = threadIdx.x; i < n; i += kJoinThreads) s += sums[i];
     s = warp_sum(s);
@@ -213,9 +280,17 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 // ------------------------------------------------------------------ AdamW
 
-constexpr int kAdamTurns = 2;
-constexpr long long kAdamChunk = (long long)kAdamTurns * kTurn;
-static_assert(kAdamChunk % kStateBlock == 0, "a block of 8-bit states lies in one chunk");
+// How a launch takes its chunks.  With states in 8 bits instructions bound the step, 62 a weight,
+// and warps to cover their latency count: 128 threads at 64 registers, 81 us for 40.4 M weights in
+// bf16 (5.0 TB/s), against 95 us with 256 threads at 80 and 107 us at 106.  With states in fp32 HBM
+// does: 541 to 546 us for 136 M fp32 weights (7.0 TB/s) in all of these shapes.
+template <bool S8>
+struct AdamShape {
+    static constexpr int kThreads = S8 ? 128 : 256, kMinCtas = S8 ? 8 : 1;
+    static constexpr int kTurns = 2, kStride = kThreads * kVec;  // vectors of a thread, all loads first
+    static constexpr long long kChunk = (long long)kTurns * kStride;
+    static_assert(kChunk % kStateBlock == 0, "a block of 8-bit states lies in one chunk");
+};
 
 struct AdamTensor {
     void* p;
@@ -237,7 +312,7 @@ struct AdamBatch {
     float beta1, beta2, one_less1, one_less2, ln_beta1, ln_beta2;
     float lr, decay, rate, root, eps, weight_decay;  // decay = lr * weight_decay
     float max_norm, grad_scale;
-    int step, by_chance;
+    int step, by_chance, fine;
     uint32_t seed_lo, seed_hi;
 };
 
@@ -251,192 +326,330 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
     x = (x ^ x >> 15) * kMul2;
     return x ^ x >> 16;
 }
-__device__ __forceinline__ uint32_t chance_bits(uint32_t i, uint32_t key1, uint32_t key2) {
-    uint32_t x = (i ^ key1) * kMul1;
-    x = ((x ^ x >> 16) + key2) * kMul2;
+// Of element i with key1 already in it (the exclusive or of both) and times kMul1.
+__device__ __forceinline__ uint32_t chance_bits(uint32_t first, uint32_t key2_mul2) {
+    const uint32_t x = (first ^ first >> 16) * kMul2 + key2_mul2;
     return x ^ x >> 15;
 }
 
-// bf16 of x by 16 bits of chance; what is not finite stays so.
-__device__ __forceinline__ __nv_bfloat16 round_by(float x, uint32_t chance) {
-    const uint32_t w = __float_as_uint(x);
-    if ((w & 0x7f800000u) == 0x7f800000u) return __float2bfloat16_rn(x);
-    return __ushort_as_bfloat16((unsigned short)((w + chance) >> 16));
+// The root and the quotient of a step, within 2 units of the last place of fp32.  The quick ones
+// take numbers below fp32's normal range as 0: a divisor moves by 1.1e-19 * root at most, which is
+// nothing beside eps where it counts (`fine` says that it would be).
+__device__ __forceinline__ float quick_root(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
+__device__ __forceinline__ float quick_inverse(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The largest magnitude of three, NaN where one is.
+__device__ __forceinline__ float max_abs_or_nan(float a, float b, float c) {
+    float m;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+// What a launch's threads take from the device, and the key of their chunk's chance.
+struct Coefficients {
+    float scale, rate, root, decay;
+    uint32_t key1, key2;  // key1's exclusive or with an element's place; key2 * kMul2
+};
 
-template <typename P, typename Gr, bool S8, bool MASTER, int N>
-__global__ void __launch_bounds__(kThreads)
-    adamw_kernel(const __grid_constant__ AdamBatch<N> b) {
+// TURNS vectors of a thread, from element i on, a stride apart.
+template <typename P, typename Gr, bool S8, bool MASTER, bool CHANCE, int TURNS, bool FULL,
+          typename Batch>
+__device__ __forceinline__ void adam_vectors(const Batch& b, const AdamTensor& t,
+                                           const Coefficients& c, long long i) {
     using S = typename std::conditional<S8, uint8_t, float>::type;
-    using X = typename std::conditional<S8, uint32_t, float>::type;
-    const int k = tensor_of(b, blockIdx.x);
-    const AdamTensor& t = b.t[k];
-    const long long lo = (long long)((int)blockIdx.x - t.first) * kAdamChunk, n = t.n;
-    const bool wide = t.wide != 0;
-    P* const p = static_cast<P*>(t.p);
-    const Gr* const g = static_cast<const Gr*>(t.g);
-    S* const m = static_cast<S*>(t.m);
-    S* const v = static_cast<S*>(t.v);
-
-    float scale = b.grad_scale;
-    if (b.norm != nullptr) {
-        const float norm = *b.norm;
-        if (!(fabsf(norm) < INFINITY)) return;  // the step is left out
-        if (b.max_norm > 0.f) scale *= fminf(b.max_norm / (norm * fabsf(b.grad_scale)), 1.f);
-    }
-    const int step = b.step_at != nullptr ? *b.step_at : b.step;
-    float rate = b.rate, root = b.root, decay = b.decay;
-    if (b.step_at != nullptr || b.lr_at != nullptr) {
-        const float lr = b.lr_at != nullptr ? *b.lr_at : b.lr;
-        decay = lr * b.weight_decay;
-        rate = lr / -expm1f((float)step * b.ln_beta1);
-        root = rsqrtf(-expm1f((float)step * b.ln_beta2));
-    }
-    const uint32_t key1 = mix(b.seed_lo ^ mix(b.seed_hi ^ mix((uint32_t)step)));
-    uint32_t key2 = mix(key1 + (uint32_t)(b.ordinal + k) + 1u);
-
+    using W = typename std::conditional<MASTER, float, P>::type;
+    constexpr int kStride = AdamShape<S8>::kStride;
+    const long long n = t.n;
+    W* const w_at = MASTER ? reinterpret_cast<W*>(t.master) : static_cast<W*>(t.p);
+    S* const m_at = static_cast<S*>(t.m);
+    S* const v_at = static_cast<S*>(t.v);
+    Vec<W> wo[TURNS];
+    Vec<Gr> go[TURNS];
+    Vec<S> mo[TURNS], vo[TURNS];
+    uint32_t ms[TURNS], vs[TURNS];
 #pragma unroll
-    for (int turn = 0; turn < kAdamTurns; ++turn) {
-        const long long i = lo + turn * kTurn + (long long)threadIdx.x * kVec;
-        float w[kVec], x[kVec], m1[kVec], v1[kVec];
-        X mc[kVec], vc[kVec];
-        if (MASTER)
-            load(t.master, i, n, wide, w);
-        else
-            load(p, i, n, wide, w);
-        load(g, i, n, wide, x);
-        load(m, i, n, wide, mc);
-        load(v, i, n, wide, vc);
-        float mu = 0.f, vu = 0.f;
+    for (int k = 0; k < TURNS; ++k) {
+        const long long at = i + k * kStride;
+        wo[k] = load<FULL>(w_at, at, n);
+        go[k] = load<FULL>(static_cast<const Gr*>(t.g), at, n);
+        mo[k] = load<FULL>(m_at, at, n);
+        vo[k] = load<FULL>(v_at, at, n);
+        if (S8) {
+            ms[k] = FULL || at < n ? t.m_scale[at >> 5] : 0u;
+            vs[k] = FULL || at < n ? t.v_scale[at >> 5] : 0u;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < TURNS; ++k) {
+        const long long at = i + k * kStride;
+        float w[kVec], g[kVec], m[kVec], v[kVec];
+        wo[k].get(w);
+        go[k].get(g);
+        float mb = b.beta1, vb = b.beta2;
         if constexpr (S8) {
-            if (i < n) {
-                mu = State8<false>::unit(t.m_scale[i / kStateBlock]);
-                vu = State8<true>::unit(t.v_scale[i / kStateBlock]);
+            // a product with a power of two is exact: where in the chain it stands does not show
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                m[j] = State8<false>::raw(mo[k].high(j));
+                v[j] = State8<true>::raw(vo[k].high(j));
             }
+            if (__any_sync(0xffffffffu, ms[k] >= State8<false>::kFar || vs[k] >= State8<true>::kFar)) {
+                const float mu = State8<false>::unit(ms[k]), vu = State8<true>::unit(vs[k]);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    m[j] *= mu;
+                    v[j] *= vu;
+                }
+                mb *= State8<false>::far_unit(ms[k]);
+                vb *= State8<true>::far_unit(vs[k]);
+            } else {
+                mb *= State8<false>::near_unit(ms[k]);
+                vb *= State8<true>::near_unit(vs[k]);
+            }
+        } else {
+            mo[k].get(m);
+            vo[k].get(v);
         }
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-            if constexpr (S8) {
-                m1[j] = State8<false>::decode(mc[j], mu);
-                v1[j] = State8<true>::decode(vc[j], vu);
-            } else {
-                m1[j] = mc[j];
-                v1[j] = vc[j];
-            }
-            // no contraction: the states' last bits do not depend on how the code is compiled
-            const float gs = __fmul_rn(x[j], scale);
-            m1[j] = __fadd_rn(__fmul_rn(m1[j], b.beta1), __fmul_rn(gs, b.one_less1));
-            v1[j] = __fadd_rn(__fmul_rn(v1[j], b.beta2),
-                              __fmul_rn(__fmul_rn(gs, gs), b.one_less2));
-            const float by = m1[j] / fmaf(sqrtf(v1[j]), root, b.eps);
-            w[j] -= fmaf(decay, w[j], rate * by);
+            // products and sums rounded one by one: the states' last bits depend on nothing else
+            const float gs = __fmul_rn(g[j], c.scale);
+            m[j] = __fadd_rn(__fmul_rn(m[j], mb), __fmul_rn(gs, b.one_less1));
+            v[j] = __fadd_rn(__fmul_rn(v[j], vb), __fmul_rn(__fmul_rn(gs, gs), b.one_less2));
         }
-        uint32_t chance[kVec];
-        const bool by_chance = b.by_chance != 0;
-        if ((S8 || (!MASTER && sizeof(P) == 2)) && by_chance) {
-            const uint32_t high = (uint32_t)(i >> 32) * kMul1;  // the same for all 8
+        if (b.fine) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) g[j] = m[j] / fmaf(sqrtf(v[j]), c.root, b.eps);
+        } else {
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
-                chance[j] = chance_bits((uint32_t)i + j, key1, key2 + high);
+                g[j] = m[j] * quick_inverse(fmaf(quick_root(v[j]), c.root, b.eps));
+        }
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) w[j] -= fmaf(c.decay, w[j], c.rate * g[j]);
+        uint32_t chance[kVec];
+        if (CHANCE) {
+            // the places of 8 neighbours differ in their lowest bits, and so do those in front of the
+            // first product, by the same for all vectors
+            const uint32_t low = c.key1 & (kVec - 1u), first = ((uint32_t)at ^ c.key1) * kMul1;
+            const uint32_t key2 = c.key2 + (uint32_t)(at >> 32) * (kMul1 * kMul2);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j)
+                chance[j] = chance_bits(first + ((low ^ (uint32_t)j) - low) * kMul1, key2);
+        }
+        // the weights leave before the states are rounded, and with them their registers
+        if constexpr (MASTER || sizeof(P) == 4 || !CHANCE) {
+            wo[k].set(w);
+        } else {
+            // the upper half of a number and 16 bits of chance
+            uint32_t up[kVec];
+            float odd = 0.f;  // NaN with one among the numbers, or an infinity
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                odd = fmaf(w[j], 0.f, odd);
+                up[j] = __float_as_uint(w[j]) + (chance[j] * kMul1 >> 16);
+            }
+            if (!(odd == 0.f)) {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                    if (w[j] != w[j]) up[j] = 0x7fffffffu;
+            }
+            wo[k].set_upper(up);
+        }
+        store<FULL>(w_at, at, n, wo[k]);
+        if constexpr (MASTER) {
+            Vec<P> p;
+            p.set(w);
+            store<FULL>(static_cast<P*>(t.p), at, n, p);
         }
         if constexpr (S8) {
-            uint32_t mt = 0, vt = 0;
+            if (!FULL) {
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                if (i + j >= n) m1[j] = v1[j] = 0.f;
-                mt = max(mt, __float_as_uint(m1[j]) & 0x7fffffffu);
-                vt = max(vt, __float_as_uint(v1[j]) & 0x7fffffffu);
+                for (int j = 0; j < kVec; ++j)
+                    if (at + j >= n) m[j] = v[j] = 0.f;
             }
+            float mt = fabsf(m[0]), vt = v[0];
+#pragma unroll
+            for (int j = 1; j + 1 < kVec; j += 2) {
+                mt = max_abs_or_nan(mt, m[j], m[j + 1]);
+                vt = max_abs_or_nan(vt, v[j], v[j + 1]);
+            }
+            mt = max_or_nan(mt, fabsf(m[kVec - 1]));
+            vt = max_or_nan(vt, v[kVec - 1]);
 #pragma unroll
             for (int o = 1; o < kStateBlock / kVec; o *= 2) {
-                mt = max(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-                vt = max(vt, __shfl_xor_sync(0xffffffffu, vt, o));
+                mt = max_or_nan(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+                vt = max_or_nan(vt, __shfl_xor_sync(0xffffffffu, vt, o));
             }
-            const uint32_t ms = State8<false>::scale_of(mt), vs = State8<true>::scale_of(vt);
-            const float md = State8<false>::down(ms), vd = State8<true>::down(vs);
+            uint32_t mn, vn, wm[kVec], wv[kVec];  // the scales; the magnitudes on their grids
+            if (__all_sync(0xffffffffu, State8<false>::near(mt) && State8<true>::near(vt))) {
+                mn = State8<false>::near_scale_of(mt);
+                vn = State8<true>::near_scale_of(vt);
+                const float md = State8<false>::near_down(mn), vd = State8<true>::near_down(vn);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    wm[j] = __float_as_uint(fabsf(m[j]) * md);
+                    wv[j] = __float_as_uint(v[j] * vd);
+                }
+            } else {
+                mn = State8<false>::scale_of(mt);
+                vn = State8<true>::scale_of(vt);
+                const float md = State8<false>::down(mn), vd = State8<true>::down(vn);
+                const float mf = State8<false>::far_down(mn), vf = State8<true>::far_down(vn);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    wm[j] = mn == 255u ? 0u : __float_as_uint(fabsf(m[j]) * md * mf);
+                    wv[j] = vn == 255u ? 0u : __float_as_uint(v[j] * vd * vf);
+                    if (mn == 255u) m[j] = 0.f;
+                    if (vn == 255u) v[j] = 0.f;
+                }
+            }
+            uint32_t mc[kVec], vc[kVec], least = 0xffffffffu;
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                if (by_chance) {
-                    mc[j] = State8<false>::template encode<true>(m1[j], md, chance[j] & 0xffffu);
-                    vc[j] = State8<true>::template encode<true>(v1[j], vd, chance[j] >> 16);
-                } else {
-                    mc[j] = State8<false>::template encode<false>(m1[j], md, 0);
-                    vc[j] = State8<true>::template encode<false>(v1[j], vd, 0);
-                }
-                if (ms == 255u) mc[j] = 0;
-                if (vs == 255u) vc[j] = 0;
+                // the lower and the upper 16 bits in bits 8 to 23, bit 7 set below them
+                const uint32_t ml = CHANCE ? __byte_perm(chance[j], 0x80u, 0x5104) : 0u;
+                const uint32_t vl = CHANCE ? __byte_perm(chance[j], 0x80u, 0x5324) : 0u;
+                mc[j] = State8<false>::template encode<CHANCE>(m[j], wm[j], ml);
+                vc[j] = State8<true>::template encode<CHANCE>(v[j], wv[j], vl);
+                least = min(least, vc[j]);
             }
-            store(m, i, n, wide, mc);
-            store(v, i, n, wide, vc);
-            if (i < n && i % kStateBlock == 0) {
-                t.m_scale[i / kStateBlock] = (uint8_t)ms;
-                t.v_scale[i / kStateBlock] = (uint8_t)vs;
-            }
-        } else {
-            store(m, i, n, wide, m1);
-            store(v, i, n, wide, v1);
-        }
-        if (MASTER) store(t.master, i, n, wide, w);
-        if constexpr (sizeof(P) == 2) {
-            __nv_bfloat16 h[kVec];
+            if (least < State8<true>::kOne) {
 #pragma unroll
-            for (int j = 0; j < kVec; ++j)
-                h[j] = !MASTER && by_chance ? round_by(w[j], chance[j] * kMul1 >> 16)
-                                            : __float2bfloat16_rn(w[j]);
-            store(p, i, n, wide, h);
+                for (int j = 0; j < kVec; ++j) vc[j] = State8<true>::above_zero(v[j], vc[j]);
+            }
+            mo[k].set_high(mc);
+            vo[k].set_high(vc);
+            if ((FULL || at < n) && (threadIdx.x & (kStateBlock / kVec - 1)) == 0) {
+                t.m_scale[at >> 5] = (uint8_t)mn;
+                t.v_scale[at >> 5] = (uint8_t)vn;
+            }
         } else {
-            store(p, i, n, wide, w);
+            mo[k].set(m);
+            vo[k].set(v);
         }
+        store<FULL>(m_at, at, n, mo[k]);
+        store<FULL>(v_at, at, n, vo[k]);
     }
+}
+
+// The end of a tensor, or one whose vectors are not aligned.  A call, so that the others keep their
+// registers.
+template <typename P, typename Gr, bool S8, bool MASTER, bool CHANCE, typename Batch>
+__device__ __noinline__ void adam_edge(const Batch& b, const AdamTensor& t, const Coefficients c,
+                                       long long i) {
+    adam_vectors<P, Gr, S8, MASTER, CHANCE, 1, false>(b, t, c, i);
+}
+
+template <typename P, typename Gr, bool S8, bool MASTER, bool CHANCE, int N>
+__global__ void __launch_bounds__(AdamShape<S8>::kThreads, AdamShape<S8>::kMinCtas)
+    adamw_kernel(const __grid_constant__ AdamBatch<N> b) {
+    const int k = tensor_of(b, blockIdx.x);
+    const AdamTensor& t = b.t[k];
+    using Shape = AdamShape<S8>;
+    const long long lo = (long long)((int)blockIdx.x - t.first) * Shape::kChunk;
+    Coefficients c = {b.grad_scale, b.rate, b.root, b.decay, 0, 0};
+    if (b.norm != nullptr) {
+        const float norm = *b.norm;
+        if (!(fabsf(norm) < INFINITY)) return;  // the step is left out
+        if (b.max_norm > 0.f) c.scale *= fminf(b.max_norm / (norm * fabsf(b.grad_scale)), 1.f);
+    }
+    const int step = b.step_at != nullptr ? *b.step_at : b.step;
+    if (b.step_at != nullptr || b.lr_at != nullptr) {
+        const float lr = b.lr_at != nullptr ? *b.lr_at : b.lr;
+        c.decay = lr * b.weight_decay;
+        c.rate = lr / -expm1f((float)step * b.ln_beta1);
+        c.root = rsqrtf(-expm1f((float)step * b.ln_beta2));
+    }
+    if (CHANCE) {
+        c.key1 = mix(b.seed_lo ^ mix(b.seed_hi ^ mix((uint32_t)step)));
+        c.key2 = mix(c.key1 + (uint32_t)(b.ordinal + k) + 1u) * kMul2;
+    }
+    const long long i = lo + (long long)threadIdx.x * kVec;
+    if (t.wide != 0 && lo + Shape::kChunk <= t.n)
+        adam_vectors<P, Gr, S8, MASTER, CHANCE, Shape::kTurns, true>(b, t, c, i);
+    else
+#pragma unroll 1
+        for (int turn = 0; turn < Shape::kTurns; ++turn) {
+            // by warp, whose lanes share blocks of 8-bit states: the last one has less than a whole
+            const long long at = i + turn * Shape::kStride;
+            const long long warp_lo = at - (threadIdx.x & 31) * kVec;
+            if (t.wide != 0 && warp_lo + 32 * kVec <= t.n)
+                adam_vectors<P, Gr, S8, MASTER, CHANCE, 1, true>(b, t, c, at);
+            else if (warp_lo < t.n)
+                adam_edge<P, Gr, S8, MASTER, CHANCE>(b, t, c, at);
+        }
 }
 
 // ------------------------------------------------------------------ states to values and back
 
+template <typename T, bool SQUARES, bool FULL>
+__device__ __forceinline__ void decode_octet(const uint8_t* codes, const uint8_t* scale,
+                                             long long i, long long n, T* out) {
+    const Vec<uint8_t> o = load<FULL>(codes, i, n);
+    const uint32_t s = FULL || i < n ? scale[i >> 5] : 0u;
+    const float unit = State8<SQUARES>::unit(s), far = State8<SQUARES>::far_unit(s);
+    float x[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) x[j] = State8<SQUARES>::raw(o.high(j)) * unit * far;
+    Vec<T> y;
+    y.set(x);
+    store<FULL>(out, i, n, y);
+}
 template <typename T, bool SQUARES>
 __global__ void __launch_bounds__(kThreads)
     decode_kernel(const uint8_t* codes, const uint8_t* scale, long long n, bool wide, T* out) {
-    const long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * kVec;
-    if (i >= n) return;
-    uint32_t c[kVec];
-    load(codes, i, n, wide, c);
-    const float unit = State8<SQUARES>::unit(scale[i / kStateBlock]);
-    T x[kVec];
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-        const float f = State8<SQUARES>::decode(c[j], unit);
-        if constexpr (sizeof(T) == 2)
-            x[j] = __float2bfloat16_rn(f);
-        else
-            x[j] = f;
-    }
-    store(out, i, n, wide, x);
+    const long long lo = (long long)blockIdx.x * kTurn, i = lo + (long long)threadIdx.x * kVec;
+    if (wide && lo + kTurn <= n)
+        decode_octet<T, SQUARES, true>(codes, scale, i, n, out);
+    else
+        decode_octet<T, SQUARES, false>(codes, scale, i, n, out);
 }
 
-template <typename T, bool SQUARES>
-__global__ void __launch_bounds__(kThreads)
-    encode_kernel(const T* in, long long n, bool wide, uint8_t* codes, uint8_t* scale) {
-    const long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * kVec;
-    float x[kVec];
-    load(in, i, n, wide, x);  // zeros from n on
-    uint32_t top = 0;
+template <typename T, bool SQUARES, bool FULL>
+__device__ __forceinline__ void encode_octet(const T* in, long long i, long long n, uint8_t* codes,
+                                             uint8_t* scale) {
+    float x[kVec], top = 0.f;
+    load<FULL>(in, i, n).get(x);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
         // a square is not negative: one that is reads as NaN, which a scale can say
         if (SQUARES && x[j] < 0.f) x[j] = NAN;
-        top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+        top = max_or_nan(top, fabsf(x[j]));
     }
 #pragma unroll
     for (int o = 1; o < kStateBlock / kVec; o *= 2)
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
     const uint32_t s = State8<SQUARES>::scale_of(top);
-    const float down = State8<SQUARES>::down(s);
+    const float down = State8<SQUARES>::down(s), far = State8<SQUARES>::far_down(s);
     uint32_t c[kVec];
 #pragma unroll
-    for (int j = 0; j < kVec; ++j)
-        c[j] = s == 255u ? 0u : State8<SQUARES>::template encode<false>(x[j], down, 0);
-    if (i >= n) return;
-    store(codes, i, n, wide, c);
-    if (i % kStateBlock == 0) scale[i / kStateBlock] = (uint8_t)s;
+    for (int j = 0; j < kVec; ++j) {
+        const uint32_t w = __float_as_uint(fabsf(x[j]) * down * far);
+        c[j] = State8<SQUARES>::template encode<false>(x[j], w, 0);
+        if (SQUARES) c[j] = State8<SQUARES>::above_zero(x[j], c[j]);
+        if (s == 255u) c[j] = 0u;
+    }
+    Vec<uint8_t> o;
+    o.set_high(c);
+    store<FULL>(codes, i, n, o);
+    if ((FULL || i < n) && (threadIdx.x & (kStateBlock / kVec - 1)) == 0)
+        scale[i >> 5] = (uint8_t)s;
+}
+template <typename T, bool SQUARES>
+__global__ void __launch_bounds__(kThreads)
+    encode_kernel(const T* in, long long n, bool wide, uint8_t* codes, uint8_t* scale) {
+    const long long lo = (long long)blockIdx.x * kTurn, i = lo + (long long)threadIdx.x * kVec;
+    if (wide && lo + kTurn <= n)
+        encode_octet<T, SQUARES, true>(in, i, n, codes, scale);
+    else
+        encode_octet<T, SQUARES, false>(in, i, n, codes, scale);
 }
 
 // ------------------------------------------------------------------ host
@@ -451,7 +664,13 @@ template <typename T, int N>
 cudaError_t norm_batches(const GradNormArgs& a, cudaStream_t stream) {
     NormBatch<N> b;
     double* sums = a.workspace;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = {};
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     for (int k = 0; k < a.count;) {
+        const bool from_first = sums == a.workspace;
         b.count = 0;
         b.sums = sums;
         long long first = 0;
@@ -463,38 +682,69 @@ cudaError_t norm_batches(const GradNormArgs& a, cudaStream_t stream) {
             first += c;
         }
         if (b.count == 0) break;  // nothing but empty tensors left
+        if (k == a.count && from_first && first <= kNormCluster) {  // see grad_norm_chunks
+            cfg.gridDim = dim3(kNormCluster);
+            cfg.blockDim = dim3(kThreads);
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = kNormCluster;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            return cudaLaunchKernelEx(&cfg, norm_few_kernel<T, N>, b, (int)first, a.norm);
+        }
         norm_kernel<T, N><<<(unsigned)first, kThreads, 0, stream>>>(b);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         sums += first;
     }
-    norm_join_kernel<<<1, kJoinThreads, 0, stream>>>(a.workspace, sums - a.workspace, a.norm);
-    return cudaGetLastError();
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kJoinThreads);
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, norm_join_kernel, (const double*)a.workspace,
+                              (long long)(sums - a.workspace), a.norm);
 }
 
-template <typename P, typename Gr, bool S8, bool MASTER, int N>
+template <typename P, typename Gr, bool S8, bool MASTER, bool CHANCE, int N>
 cudaError_t adam_batches(const AdamwArgs& a, AdamBatch<N>& b, cudaStream_t stream) {
     for (int k = 0; k < a.count;) {
         b.count = 0;
         b.ordinal = k;
         long long first = 0;
         for (; k < a.count && b.count < N; ++k) {
-            const long long c = chunks_of(a.sizes[k], kAdamChunk);
+            const long long c = chunks_of(a.sizes[k], AdamShape<S8>::kChunk);
             if (first + c > kMostChunks) break;
             AdamTensor& t = b.t[b.count++];
             t = {a.params[k], a.grads[k], a.exp_avg[k], a.exp_avg_sq[k],
                  MASTER ? a.master[k] : nullptr, S8 ? a.exp_avg_scale[k] : nullptr,
                  S8 ? a.exp_avg_sq_scale[k] : nullptr, a.sizes[k], (int)first, 0};
-            t.wide = aligned(t.p, 16) && aligned(t.g, 16) && aligned(t.m, S8 ? 8 : 16) &&
-                     aligned(t.v, S8 ? 8 : 16) && (!MASTER || aligned(t.master, 16));
+            t.wide = aligned(t.p, 16) && aligned(t.g, 16) && aligned(t.m, S8 ? kVec : 16) &&
+                     aligned(t.v, S8 ? kVec : 16) && (!MASTER || aligned(t.master, 16));
             first += c;
         }
         if (first == 0) continue;  // a batch of empty tensors
-        adamw_kernel<P, Gr, S8, MASTER, N><<<(unsigned)first, kThreads, 0, stream>>>(b);
+        adamw_kernel<P, Gr, S8, MASTER, CHANCE, N>
+            <<<(unsigned)first, AdamShape<S8>::kThreads, 0, stream>>>(b);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+template <typename P, typename Gr, bool S8, bool MASTER, int N>
+cudaError_t adam_rounding(const AdamwArgs& a, AdamBatch<N>& b, cudaStream_t stream) {
+    // chance has a part where something is rounded to fewer bits
+    constexpr bool kCan = S8 || (std::is_same<P, __nv_bfloat16>::value && !MASTER);
+    if (kCan && a.by_chance) return adam_batches<P, Gr, S8, MASTER, kCan, N>(a, b, stream);
+    return adam_batches<P, Gr, S8, MASTER, false, N>(a, b, stream);
+}
+
+template <typename P, typename Gr, int N>
+cudaError_t adam_states(const AdamwArgs& a, AdamBatch<N>& b, cudaStream_t stream) {
+    constexpr bool kCopies = std::is_same<P, __nv_bfloat16>::value;
+    if (kCopies && a.master != nullptr)
+        return a.exp_avg_scale != nullptr ? adam_rounding<P, Gr, true, kCopies, N>(a, b, stream)
+                                          : adam_rounding<P, Gr, false, kCopies, N>(a, b, stream);
+    return a.exp_avg_scale != nullptr ? adam_rounding<P, Gr, true, false, N>(a, b, stream)
+                                      : adam_rounding<P, Gr, false, false, N>(a, b, stream);
 }
 
 template <int N>
@@ -519,18 +769,15 @@ cudaError_t adam_typed(const AdamwArgs& a, int param_bf16, int grad_bf16, cudaSt
     b.grad_scale = (float)a.grad_scale;
     b.step = a.step;
     b.by_chance = a.by_chance;
+    // see quick_root: its error, by the largest root a step can have, against 2^-24 of eps
+    b.fine = 1.1e-19 / std::sqrt(1.0 - a.beta2) > a.eps * 0x1p-24;
     b.seed_lo = (uint32_t)a.seed;
     b.seed_hi = (uint32_t)(a.seed >> 32);
-    const bool s8 = a.exp_avg_scale != nullptr, master = a.master != nullptr;
     using bf = __nv_bfloat16;
-#define DF2_ADAM(P, GR)                                                                       \
-    (s8 ? (master ? adam_batches<P, GR, true, sizeof(P) == 2, N>(a, b, stream)               \
-                  : adam_batches<P, GR, true, false, N>(a, b, stream))                       \
-        : (master ? adam_batches<P, GR, false, sizeof(P) == 2, N>(a, b, stream)              \
-                  : adam_batches<P, GR, false, false, N>(a, b, stream)))
-    if (param_bf16) return grad_bf16 ? DF2_ADAM(bf, bf) : DF2_ADAM(bf, float);
-    return grad_bf16 ? DF2_ADAM(float, bf) : DF2_ADAM(float, float);
-#undef DF2_ADAM
+    if (param_bf16)
+        return grad_bf16 ? adam_states<bf, bf, N>(a, b, stream) : adam_states<bf, float, N>(a, b, stream);
+    return grad_bf16 ? adam_states<float, bf, N>(a, b, stream)
+                     : adam_states<float, float, N>(a, b, stream);
 }
 
 unsigned vec_grid(long long n) { return (unsigned)chunks_of(n, kTurn); }
@@ -540,7 +787,7 @@ unsigned vec_grid(long long n) { return (unsigned)chunks_of(n, kTurn); }
 long long grad_norm_chunks(int count, const long long* sizes) {
     long long n = 0;
     for (int k = 0; k < count; ++k) n += chunks_of(sizes[k], kNormChunk);
-    return n;
+    return n <= kNormCluster ? 0 : n;
 }
 
 cudaError_t launch_grad_norm(const GradNormArgs& a, int grad_bf16, cudaStream_t stream) {

@@ -392,9 +392,8 @@ struct Span {
     bool write;
 };
 
-// Whether a stretch that is written overlaps another one.
-bool any_overlap(std::vector<Span>& v) {
-    std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+// Whether a stretch that is written overlaps another one; v in order of the starts.
+bool any_overlap(const std::vector<Span>& v) {
     uintptr_t end = 0, written = 0;  // of the stretches before
     for (const Span& s : v) {
         if (s.lo < written || (s.write && s.lo < end)) return true;
@@ -457,11 +456,21 @@ int run_adamw(const df2::AdamwArgs& a, int param_dtype, int grad_dtype, void* st
         const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
         if (p != nullptr && bytes > 0) spans.push_back({lo, lo + bytes, write});
     };
+    // a list's addresses often rise: each is sorted where they do not, then merged
+    const auto by_start = [](const Span& x, const Span& y) { return x.lo < y.lo; };
+    const auto merge_from = [&](size_t mid) {
+        const auto at = spans.begin() + (ptrdiff_t)mid;
+        if (!std::is_sorted(at, spans.end(), by_start)) std::sort(at, spans.end(), by_start);
+        std::inplace_merge(spans.begin(), at, spans.end(), by_start);
+    };
     for (const Buf& b : scalars) add(b.p, b.bytes, false);
+    merge_from(0);
     for (const auto& l : list) {
         if (l.p == nullptr) continue;
+        const size_t mid = spans.size();
         for (int k = 0; k < a.count; ++k)
             add(l.p[k], (size_t)(l.scale ? (a.sizes[k] + 31) / 32 : a.sizes[k]) * l.es, l.write);
+        merge_from(mid);
     }
     if (any_overlap(spans))
         return fail(DF2_ERR_INVALID_ARG,

@@ -251,6 +251,7 @@ struct GradNormArgs {
     double* workspace;   // grad_norm_chunks(...) values
     float* norm;
 };
+// Values of workspace: one for each chunk, none where a single launch does.
 long long grad_norm_chunks(int count, const long long* sizes);
 cudaError_t launch_grad_norm(const GradNormArgs& a, int grad_bf16, cudaStream_t stream);
 

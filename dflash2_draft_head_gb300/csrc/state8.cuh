@@ -20,35 +20,66 @@ constexpr int kStateBlock = 32;  // elements that share a scale
 
 template <bool SQUARES>
 struct State8 {
-    // of the short float's smallest exponent to fp32's, and the highest one that is used
-    static constexpr float kUp = SQUARES ? 0x1p112f : 0x1p120f;
-    static constexpr float kDown = SQUARES ? 0x1p-112f : 0x1p-120f;
+    // from the short float's exponents to the lowest of fp32's, and the highest that is used
+    static constexpr uint32_t kField = SQUARES ? 112u : 120u;
     static constexpr int kTop = SQUARES ? 15 : 7;
+    // Scales from here on take their power of two in two factors.
+    static constexpr uint32_t kFar = 254u - kField;
 
+    // 2^(scale - 127) * 2^kField as two factors, the first of which is all of it below kFar.  The
+    // second says what scale 255 does.
     static __device__ __forceinline__ float unit(uint32_t scale) {
-        return __uint_as_float(scale << 23);
+        return __uint_as_float(min(scale + kField, 254u) << 23);
     }
-    static __device__ __forceinline__ float decode(uint32_t code, float unit) {
-        const uint32_t bits =
-            SQUARES ? code << 20 : (code & 0x80u) << 24 | (code & 0x7fu) << 20;
-        return __uint_as_float(bits) * kUp * unit;
+    static __device__ __forceinline__ float far_unit(uint32_t scale) {
+        if (scale == 255u) return __uint_as_float(0x7f800000u);
+        return __uint_as_float((127u + max((int)(scale + kField) - 254, 0)) << 23);
     }
-    // The scale of a block whose largest magnitude has these bits.
-    static __device__ __forceinline__ uint32_t scale_of(uint32_t top) {
-        const int field = (int)(top >> 23);
-        return field == 255 ? 255u : (uint32_t)max(field - kTop, 1);
+    // The short float of the code in bits 24 to 31 (anything below), times 2^-kField.
+    static __device__ __forceinline__ float raw(uint32_t high) {
+        return __uint_as_float(SQUARES ? high >> 4 & 0x0ff00000u
+                                       : (uint32_t)((int32_t)high >> 4) & 0x87f00000u);
     }
+
+    // The scale of a block whose largest magnitude is `top` (NaN where one value is).
+    static __device__ __forceinline__ uint32_t scale_of(float top) {
+        const int field = (int)(__float_as_uint(top) >> 23);
+        return field >= 255 ? 255u : (uint32_t)max(field - kTop, 1);
+    }
+    // Whether that is below kFar, and then by fewer operations.
+    static __device__ __forceinline__ bool near(float top) {
+        return __float_as_uint(top) < (kFar + kTop) << 23;
+    }
+    static __device__ __forceinline__ uint32_t near_scale_of(float top) {
+        return (uint32_t)max((int)(__float_as_uint(top) >> 23) - kTop, 1);
+    }
+    static __device__ __forceinline__ float near_unit(uint32_t scale) {
+        return __uint_as_float((scale + kField) << 23);
+    }
+    static __device__ __forceinline__ float near_down(uint32_t scale) {
+        return __uint_as_float((254u - kField - scale) << 23);
+    }
+    // 2^(127 - scale) * 2^-kField, all of it below kFar, else without the second.
     static __device__ __forceinline__ float down(uint32_t scale) {
-        return __uint_as_float((254u - min(scale, 254u)) << 23);
+        return __uint_as_float(scale < kFar ? (254u - kField - scale) << 23
+                                            : (254u - min(scale, 254u)) << 23);
     }
-    // The code of x; `chance`: 16 bits that say which way it goes, or ~0 for the nearest.
-    // A square above 0 keeps a code above 0: at 0 the step would be divided by eps alone.
+    static __device__ __forceinline__ float far_down(uint32_t scale) {
+        return scale < kFar ? 1.f : SQUARES ? 0x1p-112f : 0x1p-120f;
+    }
+    // The code, in bits 24 to 31 over others, of a value x whose magnitude has the bits w after
+    // down (and far_down).  chance: bits 8 to 23 say which way it goes, bit 7 is set, nothing
+    // else; the nearest without CHANCE.
     template <bool CHANCE>
-    static __device__ __forceinline__ uint32_t encode(float x, float down, uint32_t chance) {
-        const uint32_t w = __float_as_uint(fabsf(x) * down * kDown);
-        uint32_t code = (w + (CHANCE ? chance << 4 | 8u : 0x7ffffu + (w >> 20 & 1u))) >> 20;
-        if (SQUARES) return x > 0.f && code == 0u ? 1u : code;
-        return code | (__float_as_uint(x) >> 24 & 0x80u);
+    static __device__ __forceinline__ uint32_t encode(float x, uint32_t w, uint32_t chance) {
+        const uint32_t high =
+            CHANCE ? w * 16u + chance : (w + 0x7ffffu + (w >> 20 & 1u)) * 16u;
+        return SQUARES ? high : high | (__float_as_uint(x) & 0x80000000u);
+    }
+    // A square above 0 keeps a code above 0: at 0 the step would be divided by eps alone.
+    static constexpr uint32_t kOne = 1u << 24;
+    static __device__ __forceinline__ uint32_t above_zero(float x, uint32_t high) {
+        return x > 0.f ? max(high, kOne) : high;
     }
 };
 

@@ -124,7 +124,7 @@ def test_two_streams_and_two_graphs_beside_one_another():
 
 
 def test_refusals():
-    g = torch.zeros(100000, device="cuda")
+    g = torch.zeros(200000, device="cuda")
     for bad in [[], [g, g.bfloat16()], [g.half()], [g[::2]], [g.cpu()], [g, None]]:
         with pytest.raises((TypeError, ValueError)):
             df2.grad_norm(bad)
