@@ -377,10 +377,11 @@ RowSplit split_rows(int rows, int V, size_t es, int num_sms,
 
 // Launches a kernel over `rows` clusters of 2^lg CTAs.  Its shared memory and cluster
 // size go beyond the defaults: the attributes that allow this are set on the first
-// launch on a device, and again where they turn out to be gone (a device reset).
+// launch on a device, and again where they turn out to be gone (a device reset).  early: the
+// kernel waits by itself for the one before it (griddep_wait) and may be scheduled ahead.
 template <typename G, auto KERNEL, typename Args>
 cudaError_t launch_rows(const Args& a, int rows, int lg, size_t smem, size_t most_smem,
-                        cudaStream_t stream) {
+                        cudaStream_t stream, bool early = false) {
     static std::atomic<uint64_t> allowed{0};  // a bit for each device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -391,12 +392,19 @@ cudaError_t launch_rows(const Args& a, int rows, int lg, size_t smem, size_t mos
     cfg.blockDim = dim3(G::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 1u << lg;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = lg > 0 ? 1 : 0;
+    cudaLaunchAttribute attr[2] = {};
+    cfg.attrs = attr;
+    if (lg > 0) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1u << lg;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+    }
+    if (early) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
     const bool known = dev < 64 && (allowed.load(std::memory_order_relaxed) & bit) != 0;
     if (known) {
         e = cudaLaunchKernelEx(&cfg, KERNEL, a);

@@ -13,7 +13,8 @@
 // Bound by HBM.  The policy's g needs nothing but its own row: loss and gradient take the
 // row through both uses of it while it is in L2, as distillation does.  A pair's g needs all
 // rows of both sequences first: one pass over the rows for logp and lse, a kernel over
-// the pairs, and a pass that writes the gradient from lse.
+// the pairs, and a pass that writes the gradient from lse, each scheduled while the one before it
+// ends.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -26,6 +27,29 @@ namespace df2 {
 namespace {
 
 enum class Loss { kPolicy, kPreference };
+
+// How a kernel takes wide rows.  Loss and gradient in one call read a row twice, the second time from
+// the ring and L2: three CTAs an SM with slices of 200 KB keep about 70 MB of rows under way (4096 x
+// 151936 bf16: 374 us; 408 with four CTAs, whose rows do not stay in L2, 438 with whole rows).
+// One reading wants few splits: slices of 640 KB (the loss of 1024 x 151936 bf16 45 us, of 512 x
+// 262144 fp32 84 us; 47 and 88 with 160 KB, 59 and 132 with 80 KB).
+using Twice = RowGeometry<256, 3, 8, 200>;
+using Once = RowGeometry<256, 4, 6, 640>;
+
+// As split_rows, but few rows are split only as far as their CTAs run all at once: the meetings of
+// a cluster cost more than shorter slices bring where a second wave follows (64 x 151936 bf16 with
+// the gradient 13.2 us, 20 without this; 100 rows 17.0 and 25).
+template <typename G>
+RowSplit split_fitting(int rows, int V, size_t es, int num_sms) {
+    const long long vecs = row_max_vecs(V, es), bytes = vecs * 16;
+    int lg = 0;
+    while (lg < 3 && (long long)rows << (lg + 1) <= (long long)G::kCtas * num_sms &&
+           bytes >> lg > kRowSliceMin)
+        ++lg;
+    while (1 << lg < kRowMaxCluster && bytes >> lg > G::kSliceBytes) ++lg;
+    const int per = (int)((vecs + (1 << lg) - 1) >> lg), ring = G::ring_steps(per);
+    return {lg, per, ring, ring * G::kStepBytes};
+}
 
 struct TokenGrad {
     float loss;  // without the row's weight
@@ -173,6 +197,7 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
     token_loss_kernel(const __grid_constant__ TokenLossArgs a) {
     constexpr int E = VecOf<T>::kElems;
     extern __shared__ __align__(16) char smem[];
+    if (L == Loss::kPreference) griddep_launch_dependents();
     const int tid = threadIdx.x, rank = a.lg > 0 ? (int)cluster_ctarank() : 0;
     const int row = blockIdx.x >> a.lg;
     const RowView<T> r(a.logits, a.ld, row, a.V);
@@ -242,6 +267,7 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
     token_grad_kernel(const __grid_constant__ TokenLossArgs a) {
     constexpr int E = VecOf<T>::kElems;
     extern __shared__ __align__(16) char smem[];
+    if (L == Loss::kPreference) griddep_wait();
     const int tid = threadIdx.x;
     const int row = blockIdx.x >> a.lg, rank = blockIdx.x & ((1 << a.lg) - 1);
     const RowView<T> r(a.logits, a.ld, row, a.V);
@@ -274,6 +300,8 @@ constexpr int kPairThreads = 256;
 __global__ void __launch_bounds__(kPairThreads)
     pair_loss_kernel(const __grid_constant__ TokenLossArgs a) {
     __shared__ double part[2][kPairThreads / 32];
+    griddep_launch_dependents();
+    griddep_wait();
     const int i = blockIdx.x, tid = threadIdx.x;
     int n[2];
 #pragma unroll
@@ -308,20 +336,27 @@ __global__ void __launch_bounds__(kPairThreads)
     a.loss[i] = weight == 0.f ? 0.f : weight * loss;
 }
 
-template <typename T, Loss L, typename G>
+template <typename T, Loss L, typename ONCE, typename TWICE>
 cudaError_t launch_typed(TokenLossArgs a, TokenLossPass pass, cudaStream_t stream, int num_sms) {
-    const RowSplit p = split_rows<G>(a.rows, a.V, sizeof(T), num_sms);
-    a.lg = p.lg;
-    a.per = p.per;
-    a.ring = p.ring;
-    const size_t smem = p.smem;
-    constexpr size_t kMost = G::kRingBytes;
-    if (pass == TokenLossPass::kGrad)
-        return launch_rows<G, token_grad_kernel<T, L, G>>(a, a.rows, p.lg, smem, kMost, stream);
-    if (L == Loss::kPolicy && a.grad != nullptr)
-        return launch_rows<G, token_loss_kernel<T, Loss::kPolicy, true, G>>(a, a.rows, p.lg, smem,
-                                                                           kMost, stream);
-    return launch_rows<G, token_loss_kernel<T, L, false, G>>(a, a.rows, p.lg, smem, kMost, stream);
+    const auto take = [&](const RowSplit& p) {
+        a.lg = p.lg;
+        a.per = p.per;
+        a.ring = p.ring;
+        return (size_t)p.smem;
+    };
+    if (pass == TokenLossPass::kGrad) {  // the CTAs of a row do not meet
+        const size_t smem = take(split_rows<ONCE>(a.rows, a.V, sizeof(T), num_sms));
+        return launch_rows<ONCE, token_grad_kernel<T, L, ONCE>>(
+            a, a.rows, a.lg, smem, ONCE::kRingBytes, stream, a.grad_loss == nullptr);
+    }
+    if (L == Loss::kPolicy && a.grad != nullptr) {
+        const size_t smem = take(split_fitting<TWICE>(a.rows, a.V, sizeof(T), num_sms));
+        return launch_rows<TWICE, token_loss_kernel<T, Loss::kPolicy, true, TWICE>>(
+            a, a.rows, a.lg, smem, TWICE::kRingBytes, stream);
+    }
+    const size_t smem = take(split_fitting<ONCE>(a.rows, a.V, sizeof(T), num_sms));
+    return launch_rows<ONCE, token_loss_kernel<T, L, false, ONCE>>(a, a.rows, a.lg, smem,
+                                                                   ONCE::kRingBytes, stream);
 }
 
 template <Loss L>
@@ -329,10 +364,10 @@ cudaError_t launch_pass(const TokenLossArgs& a, TokenLossPass pass, int bf16, cu
                         int num_sms) {
     const bool narrow = (long long)a.V * (bf16 ? 2 : 4) <= kNarrowBytes;
     if (bf16)
-        return narrow ? launch_typed<__nv_bfloat16, L, Narrow>(a, pass, stream, num_sms)
-                      : launch_typed<__nv_bfloat16, L, Wide>(a, pass, stream, num_sms);
-    return narrow ? launch_typed<float, L, Narrow>(a, pass, stream, num_sms)
-                  : launch_typed<float, L, Wide>(a, pass, stream, num_sms);
+        return narrow ? launch_typed<__nv_bfloat16, L, Narrow, Narrow>(a, pass, stream, num_sms)
+                      : launch_typed<__nv_bfloat16, L, Once, Twice>(a, pass, stream, num_sms);
+    return narrow ? launch_typed<float, L, Narrow, Narrow>(a, pass, stream, num_sms)
+                  : launch_typed<float, L, Once, Twice>(a, pass, stream, num_sms);
 }
 
 }  // namespace
@@ -351,8 +386,16 @@ cudaError_t launch_preference_loss(const TokenLossArgs& a, TokenLossPass pass, i
             if (e != cudaSuccess) return e;
         }
         if (a.pairs > 0) {
-            pair_loss_kernel<<<a.pairs, kPairThreads, 0, stream>>>(a);
-            const cudaError_t e = cudaGetLastError();
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr = {};
+            attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr.val.programmaticStreamSerializationAllowed = 1;
+            cfg.gridDim = dim3((unsigned)a.pairs);
+            cfg.blockDim = dim3(kPairThreads);
+            cfg.stream = stream;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            const cudaError_t e = cudaLaunchKernelEx(&cfg, pair_loss_kernel, a);
             if (e != cudaSuccess) return e;
         }
         if (a.grad == nullptr) return cudaSuccess;
