@@ -693,41 +693,41 @@ class _Lists:
     between; only a failing one asks which list it was."""
 
     def __init__(self, **lists):
-        self.lists = {k: v for k, v in lists.items() if v is not None}
-        self.n = len(next(iter(self.lists.values())))
-        for name, ts in self.lists.items():
-            if len(ts) != self.n:
-                raise ValueError(f"{name} has {len(ts)} tensors, {self.n} are needed")
-            for t in ts:
-                if not isinstance(t, torch.Tensor):
-                    raise TypeError(f"{name} must be tensors, got {type(t).__name__}")
-        self.all = [t for ts in self.lists.values() for t in ts]
-        self.index = self.all[0].get_device()
-        if self.index < 0 or set(map(_device_of, self.all)) != {self.index}:
-            self._blame(lambda t: t.get_device() == self.index >= 0,
+        self.lists = lists = {k: v for k, v in lists.items() if v is not None}
+        self.n = n = len(next(iter(lists.values())))
+        self.all = ts = [t for part in lists.values() for t in part]
+        if len(ts) != n * len(lists) or any(len(part) != n for part in lists.values()):
+            raise ValueError(f"all lists must have {n} tensors: " +
+                             ", ".join(f"{name} has {len(part)}" for name, part in lists.items()))
+        devices = set(map(_device_of, ts))  # a TypeError for what is no tensor
+        self.index = index = ts[0].get_device()
+        if devices != {index} or index < 0:
+            self._blame(lambda t: t.get_device() == index >= 0,
                         "must be CUDA tensors on one device, that of all others")
-        if not all(map(_is_contiguous, self.all)):
+        if not all(map(_is_contiguous, ts)):
             self._blame(_is_contiguous, "must be contiguous")
+        self.dtypes, self.numels = list(map(_dtype_of, ts)), list(map(_numel, ts))
+        self.at = {name: slice(k * n, k * n + n) for k, name in enumerate(lists)}
 
-    def _blame(self, fine, what, error=ValueError):
-        raise error(next(f"{name} {what}" for name, ts in self.lists.items()
-                         if not all(map(fine, ts))))
+    def _blame(self, fine, what):
+        raise ValueError(next(f"{name} {what}" for name, part in self.lists.items()
+                              if not all(map(fine, part))))
 
     def dtype(self, name, dtype=None):
         """The type of a list: of all its tensors, and the given one, if any."""
-        ts = self.lists[name]
-        dtype = ts[0].dtype if dtype is None else dtype
-        if set(map(_dtype_of, ts)) != {dtype}:
+        got = self.dtypes[self.at[name]]
+        dtype = got[0] if dtype is None else dtype
+        if got.count(dtype) != self.n:
             raise TypeError(f"{name} must be {dtype} all")
         return dtype
 
     def elements(self, name, want):
-        if list(map(_numel, self.lists[name])) != want:
+        if self.numels[self.at[name]] != want:
             raise ValueError(f"{name} must have {want} elements")
 
     def arrays(self, sizes):
         """(what has to live until the call returns, the sizes' address, the lists' by name)."""
-        held = array.array("Q", [*sizes, *map(_data_ptr, self.all)])
+        held = array.array("Q", sizes + list(map(_data_ptr, self.all)))
         at, step = held.buffer_info()[0], 8 * self.n
         return held, at, {name: at + step * (k + 1) for k, name in enumerate(self.lists)}
 
@@ -747,7 +747,7 @@ def grad_norm(grads, out=None, workspace=None):
     ts, L = _Lists(grads=grads), lib()
     code = _code(ts.dtype("grads"))
     dev = ts.all[0].device
-    held, sizes, ptrs = ts.arrays(map(_numel, grads))
+    held, sizes, ptrs = ts.arrays(ts.numels)
     out, out_ptr = _out_on(out, "out", torch.float32, (1,), dev)
     ws, ws_bytes = None, 0
     if workspace is not None:
@@ -787,7 +787,7 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, beta1=0.9, beta2=0.999, 
     param_code, grad_code = _code(ts.dtype("params")), _code(ts.dtype("grads"))
     if list(map(_shape_of, grads)) != list(map(_shape_of, params)):
         raise ValueError("grads must have the shapes of params")
-    sizes = list(map(_numel, params))
+    sizes = ts.numels[:ts.n]
     for name, dtype in (("exp_avg", state), ("exp_avg_sq", state), ("master", f32)):
         if name in ts.lists:
             ts.dtype(name, dtype)

@@ -331,7 +331,8 @@ __global__ void __launch_bounds__(kPairThreads)
     const float weight = a.weight != nullptr ? a.weight[i] : 1.f;
     const float m = (float)(a.beta * (d[0] - d[1]) - a.margin);
     auto softplus = [](float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); };
-    float loss = (1.f - a.smoothing) * softplus(-m);
+    float loss = 0.f;  // a term with no weight is left out, also where it is infinite
+    if (a.smoothing != 1.f) loss = (1.f - a.smoothing) * softplus(-m);
     if (a.smoothing != 0.f) loss += a.smoothing * softplus(m);
     a.loss[i] = weight == 0.f ? 0.f : weight * loss;
 }

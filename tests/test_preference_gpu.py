@@ -215,6 +215,8 @@ def test_infinite_margins():
     assert loss[0] == INF and loss[1] == 0 and seq[0] == -INF and seq[3] == -INF
     assert torch.isfinite(grad).all() and grad[0].any() and not grad[[1, 3]].any()
     assert df2.preference_loss(z, tokens, offsets, label_smoothing=0.1)[0][1] == INF
+    loss = df2.preference_loss(z, tokens, offsets, label_smoothing=1.0)[0]
+    assert loss[0] == 0 and loss[1] == INF
 
 
 @pytest.mark.parametrize("shift", [300.0, -1e4, 1e6])
