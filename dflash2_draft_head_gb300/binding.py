@@ -766,9 +766,9 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, beta1=0.9, beta2=0.999, 
           weight_decay=0.01, master=None, exp_avg_scale=None, exp_avg_sq_scale=None, norm=None,
           max_norm=None, grad_scale=1.0, seed=None):
     """One AdamW step over lists of tensors, in place: params and grads (each fp32 or bf16, one
-    type a list), exp_avg and exp_avg_sq fp32 of as many elements, or uint8 with the lists exp_avg_scale and
-    exp_avg_sq_scale ([(numel + 31) // 32] uint8 each): states in 8 bits, zeros to begin with
-    (state_encode and state_decode go from values to them and back).  master: fp32 copies of bf16
+    type a list), exp_avg and exp_avg_sq fp32 of as many elements, or uint8 with the lists
+    exp_avg_scale and exp_avg_sq_scale ([(numel + 31) // 32] uint8 each): states in 8 bits, zeros
+    to begin with (state_encode and state_decode go from values to them and back).  master: fp32 copies of bf16
     params, which take the step.  step: the step's number, 1 for the first, or an int32 CUDA
     tensor [1] with it; lr: a number or an fp32 CUDA tensor [1] (both for captured graphs).
     norm: the gradients' norm (grad_norm); where it is not finite, nothing is changed; with

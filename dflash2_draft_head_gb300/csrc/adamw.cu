@@ -351,6 +351,7 @@ __device__ __forceinline__ float max_abs_or_nan(float a, float b, float c) {
     asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
     return m;
 }
+
 // What a launch's threads take from the device, and the key of their chunk's chance.
 struct Coefficients {
     float scale, rate, root, decay;
@@ -361,7 +362,7 @@ struct Coefficients {
 template <typename P, typename Gr, bool S8, bool MASTER, bool CHANCE, int TURNS, bool FULL,
           typename Batch>
 __device__ __forceinline__ void adam_vectors(const Batch& b, const AdamTensor& t,
-                                           const Coefficients& c, long long i) {
+                                             const Coefficients& c, long long i) {
     using S = typename std::conditional<S8, uint8_t, float>::type;
     using W = typename std::conditional<MASTER, float, P>::type;
     constexpr int kStride = AdamShape<S8>::kStride;

@@ -9,6 +9,8 @@ a sum, constants rounded once):
 8-bit codes are compared one by one with the rounding of m and v that numpy's fp32 gives for the
 same operations, which are all rounded to the nearest once each.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -239,7 +241,8 @@ def test_numbers_of_tensors(count):
 
 
 @pytest.mark.parametrize("hyper", [dict(beta1=0.0), dict(beta2=0.0), dict(weight_decay=0.0),
-                                   dict(lr=0.0), dict(eps=1.0), dict(lr=-1e-3), dict(beta2=0.9999)])
+                                   dict(lr=0.0), dict(eps=1.0), dict(lr=-1e-3), dict(beta2=0.9999),
+                                   dict(eps=1e-12), dict(eps=1e-30)])
 def test_settings(hyper):
     _check(Case([1000, 77]), hyper=HYPER | hyper)
     _check(Case([1000, 77], "bf16", "f32", small=True), hyper=HYPER | hyper, seed=1)
@@ -511,6 +514,38 @@ def test_another_stream():
     df2.adamw(*args, step=1, **HYPER, **more)
     for name in case.lists:
         assert all(torch.equal(a, b) for a, b in zip(case.lists[name], plain.lists[name]))
+
+
+def test_two_threads_on_streams_of_their_own():
+    """Calls do not hold Python's lock while they check and launch."""
+    cases, plain = [Case([5000] * 40, seed=k) for k in range(2)], [Case([5000] * 40, seed=k) for k in range(2)]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(case):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                args, more = case.args()
+                for step in range(1, 31):
+                    norm = df2.grad_norm(args[1])
+                    df2.adamw(*args, step=step, norm=norm, max_norm=1.0, **HYPER, **more)
+            stream.synchronize()
+        except Exception as e:  # told by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for c in plain:
+        work(c)
+    torch.cuda.synchronize()
+    for a, b in zip(cases, plain):
+        for name in a.lists:
+            assert all(torch.equal(x, y) for x, y in zip(a.lists[name], b.lists[name]))
 
 
 def test_parameters_of_a_module():
