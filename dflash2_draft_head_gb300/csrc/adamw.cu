@@ -280,10 +280,11 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 // ------------------------------------------------------------------ AdamW
 
-// How a launch takes its chunks.  With states in 8 bits instructions bound the step, 62 a weight,
-// and warps to cover their latency count: 128 threads at 64 registers, 81 us for 40.4 M weights in
-// bf16 (5.0 TB/s), against 95 us with 256 threads at 80 and 107 us at 106.  With states in fp32 HBM
-// does: 541 to 546 us for 136 M fp32 weights (7.0 TB/s) in all of these shapes.
+// How a launch takes its chunks.  With states in 8 bits instructions bound the step, 60 a weight,
+// and warps to cover their latency count: 128 threads at 64 registers, 76 us for 40.4 M weights in
+// bf16 (5.4 TB/s; 78 us with the states' sums one by one), against 81 us at 80 registers and 94 us
+// with one vector a thread.  With states in fp32 HBM does: 535 to 550 us for 136 M fp32 weights
+// (7.1 TB/s) in all of these shapes.
 template <bool S8>
 struct AdamShape {
     static constexpr int kThreads = S8 ? 128 : 256, kMinCtas = S8 ? 8 : 1;
@@ -312,6 +313,7 @@ struct AdamBatch {
     float beta1, beta2, one_less1, one_less2, ln_beta1, ln_beta2;
     float lr, decay, rate, root, eps, weight_decay;  // decay = lr * weight_decay
     float max_norm, grad_scale;
+    float one;  // 1, see sum_of
     int step, by_chance, fine;
     uint32_t seed_lo, seed_hi;
 };
@@ -350,6 +352,14 @@ __device__ __forceinline__ float max_abs_or_nan(float a, float b, float c) {
     float m;
     asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
     return m;
+}
+
+__device__ __forceinline__ f32x2 twice(float x) { return pair(x, x); }
+// The sum of two products, each rounded by itself: a packed addition behind a packed product is
+// compiled into one multiply-add, whose product is not rounded, and so is a multiply-add with
+// 1 unless the 1 comes from the launch's parameters.
+__device__ __forceinline__ f32x2 sum_of(f32x2 a, f32x2 b, float one) {
+    return fma2(a, twice(one), b);
 }
 
 // What a launch's threads take from the device, and the key of their chunk's chance.
@@ -418,11 +428,17 @@ __device__ __forceinline__ void adam_vectors(const Batch& b, const AdamTensor& t
             vo[k].get(v);
         }
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
+        for (int j = 0; j < kVec; j += 2) {
             // products and sums rounded one by one: the states' last bits depend on nothing else
-            const float gs = __fmul_rn(g[j], c.scale);
-            m[j] = __fadd_rn(__fmul_rn(m[j], mb), __fmul_rn(gs, b.one_less1));
-            v[j] = __fadd_rn(__fmul_rn(v[j], vb), __fmul_rn(__fmul_rn(gs, gs), b.one_less2));
+            const f32x2 gs = mul2(pair(g[j], g[j + 1]), twice(c.scale));
+            const float2 mm = halves(sum_of(mul2(pair(m[j], m[j + 1]), twice(mb)),
+                                            mul2(gs, twice(b.one_less1)), b.one));
+            const float2 vv = halves(sum_of(mul2(pair(v[j], v[j + 1]), twice(vb)),
+                                            mul2(mul2(gs, gs), twice(b.one_less2)), b.one));
+            m[j] = mm.x;
+            m[j + 1] = mm.y;
+            v[j] = vv.x;
+            v[j + 1] = vv.y;
         }
         if (b.fine) {
 #pragma unroll
@@ -591,7 +607,7 @@ __global__ void __launch_bounds__(AdamShape<S8>::kThreads, AdamShape<S8>::kMinCt
 // ------------------------------------------------------------------ states to values and back
 
 template <typename T, bool SQUARES, bool FULL>
-__device__ __forceinline__ void decode_octet(const uint8_t* codes, const uint8_t* scale,
+__device__ __forceinline__ void decode_vector(const uint8_t* codes, const uint8_t* scale,
                                              long long i, long long n, T* out) {
     const Vec<uint8_t> o = load<FULL>(codes, i, n);
     const uint32_t s = FULL || i < n ? scale[i >> 5] : 0u;
@@ -608,13 +624,13 @@ __global__ void __launch_bounds__(kThreads)
     decode_kernel(const uint8_t* codes, const uint8_t* scale, long long n, bool wide, T* out) {
     const long long lo = (long long)blockIdx.x * kTurn, i = lo + (long long)threadIdx.x * kVec;
     if (wide && lo + kTurn <= n)
-        decode_octet<T, SQUARES, true>(codes, scale, i, n, out);
+        decode_vector<T, SQUARES, true>(codes, scale, i, n, out);
     else
-        decode_octet<T, SQUARES, false>(codes, scale, i, n, out);
+        decode_vector<T, SQUARES, false>(codes, scale, i, n, out);
 }
 
 template <typename T, bool SQUARES, bool FULL>
-__device__ __forceinline__ void encode_octet(const T* in, long long i, long long n, uint8_t* codes,
+__device__ __forceinline__ void encode_vector(const T* in, long long i, long long n, uint8_t* codes,
                                              uint8_t* scale) {
     float x[kVec], top = 0.f;
     load<FULL>(in, i, n).get(x);
@@ -648,9 +664,9 @@ __global__ void __launch_bounds__(kThreads)
     encode_kernel(const T* in, long long n, bool wide, uint8_t* codes, uint8_t* scale) {
     const long long lo = (long long)blockIdx.x * kTurn, i = lo + (long long)threadIdx.x * kVec;
     if (wide && lo + kTurn <= n)
-        encode_octet<T, SQUARES, true>(in, i, n, codes, scale);
+        encode_vector<T, SQUARES, true>(in, i, n, codes, scale);
     else
-        encode_octet<T, SQUARES, false>(in, i, n, codes, scale);
+        encode_vector<T, SQUARES, false>(in, i, n, codes, scale);
 }
 
 // ------------------------------------------------------------------ host
@@ -768,6 +784,7 @@ cudaError_t adam_typed(const AdamwArgs& a, int param_bf16, int grad_bf16, cudaSt
     b.eps = (float)a.eps;
     b.max_norm = (float)a.max_norm;
     b.grad_scale = (float)a.grad_scale;
+    b.one = 1.f;
     b.step = a.step;
     b.by_chance = a.by_chance;
     // see quick_root: its error, by the largest root a step can have, against 2^-24 of eps
