@@ -768,8 +768,8 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, beta1=0.9, beta2=0.999, 
     """One AdamW step over lists of tensors, in place: params and grads (each fp32 or bf16, one
     type a list), exp_avg and exp_avg_sq fp32 of as many elements, or uint8 with the lists
     exp_avg_scale and exp_avg_sq_scale ([(numel + 31) // 32] uint8 each): states in 8 bits, zeros
-    to begin with (state_encode and state_decode go from values to them and back).  master: fp32 copies of bf16
-    params, which take the step.  step: the step's number, 1 for the first, or an int32 CUDA
+    to begin with (state_encode and state_decode go from values to them and back).  master: fp32
+    copies of bf16 params, which take the step.  step: the step's number, 1 for the first, or an int32 CUDA
     tensor [1] with it; lr: a number or an fp32 CUDA tensor [1] (both for captured graphs).
     norm: the gradients' norm (grad_norm); where it is not finite, nothing is changed; with
     max_norm it clips grads * grad_scale.  seed: an integer, by which 8-bit states, and bf16
@@ -805,7 +805,7 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, beta1=0.9, beta2=0.999, 
     lr_at, lr = _setting_on(lr, "lr", f32, at)
     norm_at = _on(norm, "norm", f32, (1,), at)
     for name, written in ts.lists.items():
-        if name != "grads":  # before the launch: not allowed for an inference tensor outside its mode
+        if name != "grads":  # before the launch: an inference tensor outside its mode forbids it
             increment_version(written)
     held, sizes_at, ptr = ts.arrays(sizes)
     _launch(at, lib().dflash2_adamw, ts.n, ptr["params"], ptr["grads"], ptr["exp_avg"],

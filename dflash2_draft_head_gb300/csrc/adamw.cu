@@ -87,7 +87,8 @@ struct alignas(8) Vec<uint8_t> {
 #pragma unroll
         for (int q = 0; q < kVec / 4; ++q) {
             const uint32_t* y = x + 4 * q;
-            a[q] = __byte_perm(__byte_perm(y[0], y[1], 0x0073), __byte_perm(y[2], y[3], 0x0073), 0x5410);
+            a[q] = __byte_perm(__byte_perm(y[0], y[1], 0x0073), __byte_perm(y[2], y[3], 0x0073),
+                               0x5410);
         }
     }
 };
@@ -288,7 +289,8 @@ __global__ void __launch_bounds__(kJoinThreads)
 template <bool S8>
 struct AdamShape {
     static constexpr int kThreads = S8 ? 128 : 256, kMinCtas = S8 ? 8 : 1;
-    static constexpr int kTurns = 2, kStride = kThreads * kVec;  // vectors of a thread, all loads first
+    // vectors of a thread, all loads first, and how far apart they are
+    static constexpr int kTurns = 2, kStride = kThreads * kVec;
     static constexpr long long kChunk = (long long)kTurns * kStride;
     static_assert(kChunk % kStateBlock == 0, "a block of 8-bit states lies in one chunk");
 };
@@ -410,7 +412,8 @@ __device__ __forceinline__ void adam_vectors(const Batch& b, const AdamTensor& t
                 m[j] = State8<false>::raw(mo[k].high(j));
                 v[j] = State8<true>::raw(vo[k].high(j));
             }
-            if (__any_sync(0xffffffffu, ms[k] >= State8<false>::kFar || vs[k] >= State8<true>::kFar)) {
+            if (__any_sync(0xffffffffu,
+                           ms[k] >= State8<false>::kFar || vs[k] >= State8<true>::kFar)) {
                 const float mu = State8<false>::unit(ms[k]), vu = State8<true>::unit(vs[k]);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
@@ -452,8 +455,8 @@ __device__ __forceinline__ void adam_vectors(const Batch& b, const AdamTensor& t
         for (int j = 0; j < kVec; ++j) w[j] -= fmaf(c.decay, w[j], c.rate * g[j]);
         uint32_t chance[kVec];
         if (CHANCE) {
-            // the places of 8 neighbours differ in their lowest bits, and so do those in front of the
-            // first product, by the same for all vectors
+            // the places of 8 neighbours differ in their lowest bits, and so do those in front of
+            // the first product, by the same for all vectors
             const uint32_t low = c.key1 & (kVec - 1u), first = ((uint32_t)at ^ c.key1) * kMul1;
             const uint32_t key2 = c.key2 + (uint32_t)(at >> 32) * (kMul1 * kMul2);
 #pragma unroll
@@ -793,7 +796,8 @@ cudaError_t adam_typed(const AdamwArgs& a, int param_bf16, int grad_bf16, cudaSt
     b.seed_hi = (uint32_t)(a.seed >> 32);
     using bf = __nv_bfloat16;
     if (param_bf16)
-        return grad_bf16 ? adam_states<bf, bf, N>(a, b, stream) : adam_states<bf, float, N>(a, b, stream);
+        return grad_bf16 ? adam_states<bf, bf, N>(a, b, stream)
+                         : adam_states<bf, float, N>(a, b, stream);
     return grad_bf16 ? adam_states<float, bf, N>(a, b, stream)
                      : adam_states<float, float, N>(a, b, stream);
 }
@@ -821,8 +825,8 @@ cudaError_t launch_adamw(const AdamwArgs& a, int param_bf16, int grad_bf16, cuda
                            : adam_typed<kMany>(a, param_bf16, grad_bf16, stream);
 }
 
-cudaError_t launch_state_decode(const uint8_t* codes, const uint8_t* scale, long long n, int squares,
-                                void* out, int out_bf16, cudaStream_t stream) {
+cudaError_t launch_state_decode(const uint8_t* codes, const uint8_t* scale, long long n,
+                                int squares, void* out, int out_bf16, cudaStream_t stream) {
     const bool wide = aligned(codes, 8) && aligned(out, 16);
     const unsigned grid = vec_grid(n);
     using bf = __nv_bfloat16;

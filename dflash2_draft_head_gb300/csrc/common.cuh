@@ -234,6 +234,7 @@ struct TokenLossArgs {
     void* grad;           // [rows, V], rows `grad_ld` elements apart, or nullptr
     long long grad_ld;
     int32_t* err_flag;
+    int keep = 0;         // the last rows, which a pass that follows should find in L2
     int lg = 0, per = 0, ring = 0;  // the split of a row, set by the launcher
 };
 enum class TokenLossPass { kLoss, kGrad };  // the loss (with grad when it is set); grad alone

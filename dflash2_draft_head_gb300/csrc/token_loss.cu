@@ -17,6 +17,7 @@
 // ends.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -28,13 +29,18 @@ namespace {
 
 enum class Loss { kPolicy, kPreference };
 
-// How a kernel takes wide rows.  Loss and gradient in one call read a row twice, the second time from
-// the ring and L2: three CTAs an SM with slices of 200 KB keep about 70 MB of rows under way (4096 x
-// 151936 bf16: 374 us; 408 with four CTAs, whose rows do not stay in L2, 438 with whole rows).
-// One reading wants few splits: slices of 640 KB (the loss of 1024 x 151936 bf16 45 us, of 512 x
-// 262144 fp32 84 us; 47 and 88 with 160 KB, 59 and 132 with 80 KB).
+// How a kernel takes wide rows.  Loss and gradient in one call read a row twice, the second time
+// from the ring and L2: three CTAs an SM with slices of 200 KB keep about 70 MB of rows under way
+// (4096 x 151936 bf16: 374 us; 408 with four CTAs, whose rows do not stay in L2, 438 with whole
+// rows).  One reading wants few splits: slices of 640 KB (the loss of 1024 x 151936 bf16 45 us, of
+// 512 x 262144 fp32 84 us; 47 and 88 with 160 KB, 59 and 132 with 80 KB).
 using Twice = RowGeometry<256, 3, 8, 200>;
 using Once = RowGeometry<256, 4, 6, 640>;
+
+// Of the rows that a call reads twice in two passes, the last ones stay in L2 for the second pass,
+// which goes backwards: 2048 x 151936 bf16 with the gradient 282 us, 289 without; 400 rows 64 and
+// 70 (with 96 MB 283 and 64).
+constexpr long long kKeepBytes = 64ll << 20;
 
 // As split_rows, but few rows are split only as far as their CTAs run all at once: the meetings of
 // a cluster cost more than shorter slices bring where a second wave follows (64 x 151936 bf16 with
@@ -119,21 +125,23 @@ __device__ __forceinline__ int count_tokens(const TokenLossArgs& a, int lo, int 
     return n;
 }
 
-// g of a row, by the whole block: the same in all CTAs of the row.
-template <Loss L, typename G>
-__device__ __forceinline__ float row_slope(const TokenLossArgs& a, int row) {
-    if (L == Loss::kPolicy) {
-        const float w = (a.weight != nullptr ? a.weight[row] : 1.f) * a.grad_loss[row];
-        return w == 0.f ? 0.f : w * policy(a, row, a.logp[row]).g;
-    }
+// g of a row of the policy, times its factor w.
+__device__ __forceinline__ float row_weight(const TokenLossArgs& a, int row) {
+    return (a.weight != nullptr ? a.weight[row] : 1.f) * a.grad_loss[row];
+}
+
+// g of a row of a sequence, by the whole block: the same in all CTAs of the row.
+template <typename G>
+__device__ __forceinline__ float sequence_slope(const TokenLossArgs& a, int row) {
     const int n = 2 * a.pairs, s = offsets_upto(a.offsets, n + 1, row) - 1;
     if (s < 0 || s >= n) return 0.f;
     const int start = clamp_row(a.offsets[s], a.rows), end = clamp_row(a.offsets[s + 1], a.rows);
     const int i = s < a.pairs ? s : s - a.pairs;
+    const float m = pair_margin(a, i);
     float w = a.weight != nullptr ? a.weight[i] : 1.f;
     if (a.grad_loss != nullptr) w *= a.grad_loss[i];
     if (w == 0.f || row < start || row >= end) return 0.f;
-    float g = w * pair_slope(a, pair_margin(a, i));
+    float g = w * pair_slope(a, m);
     if (s >= a.pairs) g = -g;
     if (a.average) g /= (float)count_tokens<G::kThreads>(a, start, end);
     return g;
@@ -202,7 +210,8 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
     const int row = blockIdx.x >> a.lg;
     const RowView<T> r(a.logits, a.ld, row, a.V);
     RowSlice<G> sl(r, a.per, a.ring, rank, tid >> 5, smem,
-                   GRAD ? l2_policy_evict_last() : l2_policy_evict_first());
+                   GRAD || row >= a.rows - a.keep ? l2_policy_evict_last()
+                                                  : l2_policy_evict_first());
     const Out<T> out(a, row, r.row);
     const int token = row_token(a, row, rank == 0 && tid == 0);
     const float weight = L == Loss::kPolicy && a.weight != nullptr ? a.weight[row] : 1.f;
@@ -241,12 +250,20 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
                 (1.f - pg(z) * per_s) * scale);
 }
 
+// The row of a CTA of the gradient's pass.  Behind a pass for logp and lse in the same call it goes
+// backwards: the last rows of that one are still in L2.
+template <Loss L>
+__device__ __forceinline__ int row_of(const TokenLossArgs& a) {
+    const int row = blockIdx.x >> a.lg;
+    return L == Loss::kPreference && a.grad_loss == nullptr ? a.rows - 1 - row : row;
+}
+
 // The gradient alone of a row whose lse is far from 0: its sum is taken again.  A call, so that
 // other rows keep their registers.
-template <typename T, typename G>
+template <typename T, Loss L, typename G>
 __device__ __noinline__ void far_row(const TokenLossArgs& a, char* smem, int token, float scale) {
     constexpr int E = VecOf<T>::kElems;
-    const int row = blockIdx.x >> a.lg, rank = a.lg > 0 ? (int)cluster_ctarank() : 0;
+    const int row = row_of<L>(a), rank = a.lg > 0 ? (int)cluster_ctarank() : 0;
     const RowView<T> r(a.logits, a.ld, row, a.V);
     RowSlice<G> sl(r, a.per, a.ring, rank, threadIdx.x >> 5, smem, l2_policy_evict_last());
     const Out<T> out(a, row, r.row);
@@ -269,22 +286,28 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
     extern __shared__ __align__(16) char smem[];
     if (L == Loss::kPreference) griddep_wait();
     const int tid = threadIdx.x;
-    const int row = blockIdx.x >> a.lg, rank = blockIdx.x & ((1 << a.lg) - 1);
+    const int row = row_of<L>(a), rank = blockIdx.x & ((1 << a.lg) - 1);
     const RowView<T> r(a.logits, a.ld, row, a.V);
     RowSlice<G> sl(r, a.per, a.ring, rank, tid >> 5, smem, l2_policy_evict_first());
     const Out<T> out(a, row, r.row);
     const int token = row_token(a, row, rank == 0 && tid == 0);
-    const float scale = token < 0 ? 0.f : row_slope<L, G>(a, row) * a.inv_t;
-    if (scale == 0.f) {
+    const float w = L == Loss::kPolicy && token >= 0 ? row_weight(a, row) : 1.f;
+    if (token < 0 || w == 0.f) {  // the row's logits are not read
         store_zeros<T>(r, out.row, out.on_grid, sl.wlo, sl.whi);
         return;
     }
+    sl.start(r);  // ahead of the slope, which takes several loads that wait for one another
     const float lse = a.lse[row];
-    if (fabsf(lse) >= kFarLse) {  // the same in all CTAs of the row
-        far_row<T, G>(a, smem, token, scale);
+    const float scale = (L == Loss::kPolicy ? w * policy(a, row, a.logp[row]).g
+                                            : sequence_slope<G>(a, row)) * a.inv_t;
+    if (scale == 0.f || fabsf(lse) >= kFarLse) {  // the same in all CTAs of the row
+        cp_async_wait_all();
+        if (scale == 0.f)
+            store_zeros<T>(r, out.row, out.on_grid, sl.wlo, sl.whi);
+        else
+            far_row<T, L, G>(a, smem, token, scale);
         return;
     }
-    sl.start(r);
     const int e_lo = max(sl.lo * E - r.head, 0), e_hi = min(sl.hi * E - r.head, a.V);
     const bool mine = tid == 0 && token >= e_lo && token < e_hi;
     const float z = mine ? to_f32(r.row[token]) : 0.f;
@@ -295,40 +318,55 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
 }
 
 // The sums of every sequence and the loss of every pair, one CTA a pair: in 64 bits and in an
-// order of its own, the same every time.
-constexpr int kPairThreads = 256;
+// order of the sequence's own, the same every time.
+constexpr int kPairThreads = 256, kSequenceThreads = kPairThreads / 2;
+constexpr int kSequenceWarps = kSequenceThreads / 32;
 __global__ void __launch_bounds__(kPairThreads)
     pair_loss_kernel(const __grid_constant__ TokenLossArgs a) {
-    __shared__ double part[2][kPairThreads / 32];
+    __shared__ double sums[2 * kSequenceWarps];
+    __shared__ int counts[2 * kSequenceWarps];
     griddep_launch_dependents();
+    // half of the threads to each sequence; what the pass over the rows does not write comes first
+    const int i = blockIdx.x, tid = threadIdx.x, half = tid / kSequenceThreads;
+    const int s = i + half * a.pairs, start = a.offsets[s], end = a.offsets[s + 1];
+    const float weight = a.weight != nullptr ? a.weight[i] : 1.f;
+    const float ref_c = a.ref_logp != nullptr ? a.ref_logp[i] : 0.f;
+    const float ref_r = a.ref_logp != nullptr ? a.ref_logp[a.pairs + i] : 0.f;
     griddep_wait();
-    const int i = blockIdx.x, tid = threadIdx.x;
-    int n[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int s = i + k * a.pairs, start = a.offsets[s], end = a.offsets[s + 1];
-        if (tid == 0 && a.err_flag != nullptr && (start < 0 || end < start || end > a.rows))
-            atomicOr(a.err_flag, DF2_FLAG_BAD_ID);
-        const int lo = clamp_row(start, a.rows), hi = clamp_row(end, a.rows);
-        double sum = 0;
-        for (int row = lo + tid; row < hi; row += kPairThreads) sum += a.logp[row];
-        sum = warp_sum(sum);
-        if ((tid & 31) == 0) part[k][tid >> 5] = sum;
-        n[k] = a.average ? count_tokens<kPairThreads>(a, lo, hi) : 1;
+    if (tid % kSequenceThreads == 0 && a.err_flag != nullptr &&
+        (start < 0 || end < start || end > a.rows))
+        atomicOr(a.err_flag, DF2_FLAG_BAD_ID);
+    const int lo = clamp_row(start, a.rows), hi = clamp_row(end, a.rows);
+    double sum = 0;
+    int n = 0;
+    for (int row = lo + tid % kSequenceThreads; row < hi; row += kSequenceThreads) {
+        sum += a.logp[row];
+        if (a.average) {
+            const int t = a.tokens[row];
+            n += t >= 0 && t < a.V;
+        }
+    }
+    sum = warp_sum(sum);
+    n = warp_sum(n);
+    if ((tid & 31) == 0) {
+        sums[tid >> 5] = sum;
+        counts[tid >> 5] = n;
     }
     __syncthreads();
     if (tid != 0) return;
-    double d[2];  // the log ratios; the margin from them before they are rounded
+    double d[2];  // the margin comes from the sums before they are rounded
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int s = i + k * a.pairs;
-        double sum = 0;
-        for (int w = 0; w < kPairThreads / 32; ++w) sum += part[k][w];
-        sum /= max(n[k], 1);
-        a.seq_logp[s] = (float)sum;
-        d[k] = a.ref_logp != nullptr ? sum - a.ref_logp[s] : sum;
+        double all = 0;
+        int rows = 0;
+        for (int w = k * kSequenceWarps; w < (k + 1) * kSequenceWarps; ++w) {
+            all += sums[w];
+            rows += counts[w];
+        }
+        if (a.average) all /= max(rows, 1);
+        a.seq_logp[i + k * a.pairs] = (float)all;
+        d[k] = all - (k == 0 ? ref_c : ref_r);
     }
-    const float weight = a.weight != nullptr ? a.weight[i] : 1.f;
     const float m = (float)(a.beta * (d[0] - d[1]) - a.margin);
     auto softplus = [](float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); };
     float loss = 0.f;  // a term with no weight is left out, also where it is infinite
@@ -382,8 +420,12 @@ cudaError_t launch_preference_loss(const TokenLossArgs& a, TokenLossPass pass, i
                                    cudaStream_t stream, int num_sms) {
     if (pass == TokenLossPass::kLoss) {
         if (a.rows > 0) {
+            TokenLossArgs first = a;
+            if (a.grad != nullptr)
+                first.keep = (int)std::min<long long>(
+                    a.rows, kKeepBytes / ((long long)a.V * (bf16 ? 2 : 4)));
             const cudaError_t e =
-                launch_pass<Loss::kPreference>(a, pass, bf16, stream, num_sms);
+                launch_pass<Loss::kPreference>(first, pass, bf16, stream, num_sms);
             if (e != cudaSuccess) return e;
         }
         if (a.pairs > 0) {
@@ -395,7 +437,7 @@ cudaError_t launch_preference_loss(const TokenLossArgs& a, TokenLossPass pass, i
             cfg.blockDim = dim3(kPairThreads);
             cfg.stream = stream;
             cfg.attrs = &attr;
-            cfg.numAttrs = 1;
+            cfg.numAttrs = a.rows > 0 ? 1 : 0;  // ahead of the pass over the rows, of nothing else
             const cudaError_t e = cudaLaunchKernelEx(&cfg, pair_loss_kernel, a);
             if (e != cudaSuccess) return e;
         }
