@@ -49,7 +49,8 @@ def _check(ts, **kw):
 @pytest.mark.parametrize("offset", [0, 1, 3])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_sizes(dtype, offset):
-    for sizes in ([1], [7], [0, 5, 0], [16383, 16384, 16385], [100003, 1, 33], [3_000_001]):
+    for sizes in ([1], [7], [0, 5, 0], [16383, 16384, 16385], [100003, 1, 33], [3_000_001],
+                  [5] * 32, [5] * 33, [32 * 16384], [32 * 16384 + 1], [400_001, 7]):
         _check(_lists(sizes, dtype, sum(sizes), offset))
 
 
@@ -97,7 +98,7 @@ def test_the_same_bits_every_time_and_given_outputs():
 
 def test_two_streams_and_two_graphs_beside_one_another():
     """Each call has a workspace of its own."""
-    lists = [_lists([500_000], "f32", k) for k in range(2)]
+    lists = [_lists([1_500_000], "f32", k) for k in range(2)]
     want = [df2.grad_norm(ts) for ts in lists]
     streams = [torch.cuda.Stream() for _ in lists]
     torch.cuda.synchronize()
@@ -124,7 +125,7 @@ def test_two_streams_and_two_graphs_beside_one_another():
 
 
 def test_refusals():
-    g = torch.zeros(200000, device="cuda")
+    g = torch.zeros(600000, device="cuda")
     for bad in [[], [g, g.bfloat16()], [g.half()], [g[::2]], [g.cpu()], [g, None]]:
         with pytest.raises((TypeError, ValueError)):
             df2.grad_norm(bad)

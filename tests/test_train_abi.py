@@ -119,7 +119,7 @@ def _ptrs(v):
     return _array(ctypes.c_void_p, v)
 
 
-def _norm(L, grads=(P[0], P[1]), sizes=(100, 150000), dt=0, ws=P[2], wb=88, out=P[3], count=2):
+def _norm(L, grads=(P[0], P[1]), sizes=(100, 600000), dt=0, ws=P[2], wb=304, out=P[3], count=2):
     return L.dflash2_grad_norm(count, _ptrs(grads), _array(ctypes.c_int64, sizes), dt, ws, wb, out,
                                None)
 
@@ -127,9 +127,9 @@ def _norm(L, grads=(P[0], P[1]), sizes=(100, 150000), dt=0, ws=P[2], wb=88, out=
 @pytest.mark.parametrize("kw,code", [
     (dict(count=-1), 1), (dict(grads=None), 1), (dict(sizes=None), 1), (dict(sizes=(100, -1)), 1),
     (dict(sizes=(100, (1 << 40) + 1)), 2), (dict(dt=2), 1), (dict(out=None), 1), (dict(ws=None), 1),
-    (dict(wb=87), 1), (dict(ws=P[2] + 4), 1), (dict(out=P[3] + 2), 1), (dict(grads=(P[0], None)), 1),
+    (dict(wb=303), 1), (dict(ws=P[2] + 4), 1), (dict(out=P[3] + 2), 1), (dict(grads=(P[0], None)), 1),
     (dict(grads=(P[0], P[1] + 2)), 1), (dict(grads=(P[0], P[1] + 1), dt=1), 1), (dict(out=P[1] + 796), 1),
-    (dict(ws=P[0]), 1), (dict(out=P[2] + 84), 1),
+    (dict(ws=P[0]), 1), (dict(out=P[2] + 300), 1),
 ])
 def test_grad_norm_validation(L, kw, code):
     assert _norm(L, **kw) == code
@@ -140,8 +140,9 @@ def test_grad_norm_workspace(L):
     def need(*n):
         return L.dflash2_grad_norm_workspace_bytes(len(n), _array(ctypes.c_int64, n))
     assert need() == 0 and need(0, 0) == 0 and need(-1) == 0
-    assert need(1) == 0 and need(8 * 16384) == 0 and need(*[1] * 8) == 0   # one launch does
-    assert need(8 * 16384 + 1) == 72 and need(*[1] * 9) == 72 and need(7 * 16384 + 1, 0, 1) == 72
+    assert need(1) == 0 and need(32 * 16384) == 0 and need(*[1] * 32) == 0   # one launch does
+    assert need(32 * 16384 + 1) == 264 and need(*[1] * 33) == 264
+    assert need(31 * 16384 + 1, 0, 1) == 264
     assert need(1 << 40) == (1 << 40) // 16384 * 8
 
 
