@@ -779,40 +779,70 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, beta1=0.9, beta2=0.999, 
         if any(len(v) for v in (grads, exp_avg, exp_avg_sq)):
             raise ValueError("params is empty, other lists are not")
         return
-    ts = _Lists(params=params, grads=grads, exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, master=master,
-                exp_avg_scale=exp_avg_scale, exp_avg_sq_scale=exp_avg_sq_scale)
-    f32, at = torch.float32, ts.index
+    f32, n = torch.float32, len(params)
     small = exp_avg_scale is not None or exp_avg_sq_scale is not None
-    state = torch.uint8 if small else f32
-    param_code, grad_code = _code(ts.dtype("params")), _code(ts.dtype("grads"))
-    if list(map(_shape_of, grads)) != list(map(_shape_of, params)):
-        raise ValueError("grads must have the shapes of params")
-    sizes = ts.numels[:ts.n]
-    for name, dtype in (("exp_avg", state), ("exp_avg_sq", state), ("master", f32)):
-        if name in ts.lists:
-            ts.dtype(name, dtype)
-            ts.elements(name, sizes)
+    lists = [params, grads, exp_avg, exp_avg_sq]
+    if master is not None:
+        lists.append(master)
     if small:
-        blocks = [-(-n // 32) for n in sizes]
-        for name in ("exp_avg_scale", "exp_avg_sq_scale"):
-            if name not in ts.lists:
-                raise ValueError("states in 8 bits need exp_avg_scale and exp_avg_sq_scale")
-            ts.dtype(name, torch.uint8)
-            ts.elements(name, blocks)
+        lists += [exp_avg_scale, exp_avg_sq_scale]
+    try:
+        ts = [t for part in lists for t in part]
+        at = ts[0].get_device()
+        dtypes, numels = list(map(_dtype_of, ts)), list(map(_numel, ts))
+        sizes, states = numels[:n], [torch.uint8 if small else f32] * (2 * n)
+        copies = [] if master is None else [f32] * n
+        blocks = [-(-k // 32) for k in sizes] * 2 if small else []
+        fine = (at >= 0 and set(map(_device_of, ts)) == {at} and all(map(_is_contiguous, ts)) and
+                dtypes == dtypes[:1] * n + dtypes[n:n + 1] * n + states + copies +
+                [torch.uint8] * len(blocks) and
+                numels[2 * n:] == sizes * (2 if master is None else 3) + blocks and
+                list(map(_shape_of, grads)) == list(map(_shape_of, params)) and
+                n == len(grads) == len(exp_avg) == len(exp_avg_sq))
+    except (AttributeError, TypeError):  # no tensors, or no list
+        fine = False
+    if not fine:
+        _blame_adamw(params, grads, exp_avg, exp_avg_sq, master, exp_avg_scale, exp_avg_sq_scale)
+    param_code, grad_code = _code(dtypes[0]), _code(dtypes[n])
     step_at, step = _setting_on(step, "step", torch.int32, at)
     if step_at is None and not 1 <= step < 1 << 31:  # the entry takes 32 bits
         raise ValueError(f"step={step}: the first step is 1, the last one 2^31 - 1")
     lr_at, lr = _setting_on(lr, "lr", f32, at)
     norm_at = _on(norm, "norm", f32, (1,), at)
-    for name, written in ts.lists.items():
-        if name != "grads":  # before the launch: an inference tensor outside its mode forbids it
-            increment_version(written)
-    held, sizes_at, ptr = ts.arrays(sizes)
-    _launch(at, lib().dflash2_adamw, ts.n, ptr["params"], ptr["grads"], ptr["exp_avg"],
-            ptr["exp_avg_sq"], ptr.get("master"), ptr.get("exp_avg_scale"),
-            ptr.get("exp_avg_sq_scale"), sizes_at, param_code, grad_code, step_at, lr_at, step, lr,
+    # before the launch: an inference tensor outside its mode forbids it
+    increment_version(ts[:n] + ts[2 * n:])
+    held = array.array("Q", sizes + list(map(_data_ptr, ts)))  # lives until the call returns
+    p, by = held.buffer_info()[0], 8 * n
+    more = p + 5 * by  # behind sizes and the first four lists
+    scales = more if master is None else more + by
+    _launch(at, lib().dflash2_adamw, n, p + by, p + 2 * by, p + 3 * by, p + 4 * by,
+            None if master is None else more, scales if small else None,
+            scales + by if small else None, p, param_code, grad_code, step_at, lr_at, step, lr,
             beta1, beta2, eps, weight_decay, norm_at, 0.0 if max_norm is None else max_norm,
             grad_scale, seed is not None, 0 if seed is None else seed & 0xffffffffffffffff)
+
+
+def _blame_adamw(params, grads, exp_avg, exp_avg_sq, master, exp_avg_scale, exp_avg_sq_scale):
+    """Raises what is wrong with adamw()'s lists, one after the other."""
+    ts = _Lists(params=params, grads=grads, exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, master=master,
+                exp_avg_scale=exp_avg_scale, exp_avg_sq_scale=exp_avg_sq_scale)
+    small = exp_avg_scale is not None or exp_avg_sq_scale is not None
+    state = torch.uint8 if small else torch.float32
+    _code(ts.dtype("params"))
+    _code(ts.dtype("grads"))
+    if list(map(_shape_of, grads)) != list(map(_shape_of, params)):
+        raise ValueError("grads must have the shapes of params")
+    sizes = ts.numels[:ts.n]
+    for name, dtype in (("exp_avg", state), ("exp_avg_sq", state), ("master", torch.float32)):
+        if name in ts.lists:
+            ts.dtype(name, dtype)
+            ts.elements(name, sizes)
+    for name in ("exp_avg_scale", "exp_avg_sq_scale"):
+        if name not in ts.lists:
+            raise ValueError("states in 8 bits need exp_avg_scale and exp_avg_sq_scale")
+        ts.dtype(name, torch.uint8)
+        ts.elements(name, [-(-n // 32) for n in sizes])
+    raise ValueError("the lists of tensors do not go together")
 
 
 def _setting_on(v, name, dtype, index):
