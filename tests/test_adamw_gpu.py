@@ -360,6 +360,22 @@ def test_step_and_rate_on_the_device():
             assert all(torch.equal(a, b) for a, b in zip(case.lists[name], plain.lists[name]))
 
 
+@pytest.mark.parametrize("which", ["step", "lr"])
+def test_one_setting_on_the_device(which):
+    both, one = Case([5000, 3], small=True), Case([5000, 3], small=True)
+    step = torch.tensor([9], dtype=torch.int32, device="cuda")
+    lr = torch.tensor([3e-3], device="cuda")
+    args, more = both.args()
+    df2.adamw(*args, **more, **(HYPER | dict(lr=lr)), step=step, seed=6)
+    args, more = one.args()
+    df2.adamw(*args, **more, **(HYPER | (dict(lr=lr) if which == "lr" else {})),
+              step=step if which == "step" else 9, seed=6)
+    for name in ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"):
+        assert all(torch.equal(a, b) for a, b in zip(both.lists[name], one.lists[name]))
+    for a, b, old in zip(both.lists["params"], one.lists["params"], Case([5000, 3]).lists["params"]):
+        assert ((a - b).abs() <= 2.0 ** -20 * (b - old).abs() + 2.0 ** -23 * old.abs()).all()
+
+
 def test_a_captured_step_that_is_replayed():
     """Step number, rate, norm and chance follow the device's values from replay to replay, two
     graphs of different lists beside one another."""

@@ -295,6 +295,23 @@ def test_leading_dimensions_and_given_outputs():
     assert all(equal_bits(a, b.view(a.shape)) for a, b in zip(got, want))
 
 
+def test_a_single_row_without_leading_dimensions_and_spaced_views():
+    z, tokens, g = rows_of(12, 600, "bf16", 14, pad=8)
+    old, A, ref = _around(z, tokens, 1.0, g)
+    want = df2.policy_loss(z[:1], tokens[:1], old[:1], A[:1], grad=True)
+    one = df2.policy_loss(z[0], tokens[0], old[0], A[0], grad=True)
+    assert one[0].shape == () and one[3].shape == (600,)
+    assert all(equal_bits(a.view(b.shape), b) for a, b in zip(one, want))
+    # every third row, and a view of three dimensions, of a padded buffer
+    for view, t in ((z[::3], slice(None, None, 3)), (z.unflatten(0, (3, 4)), slice(None))):
+        shape = view.shape[:-1]
+        tt, oo, aa = (v[t].contiguous().view(shape) for v in (tokens, old, A))
+        got = df2.policy_loss(view, tt, oo, aa, grad=True)
+        flat = df2.policy_loss(view.reshape(-1, 600).contiguous(), tt.view(-1), oo.view(-1),
+                               aa.view(-1), grad=True)
+        assert all(equal_bits(a.reshape(b.shape), b) for a, b in zip(got, flat))
+
+
 def test_beside_autograd():
     g = torch.Generator().manual_seed(1)
     h = torch.randn((6, 8), generator=g).cuda()
