@@ -31,10 +31,10 @@ enum class Loss { kPolicy, kPreference };
 
 // How a kernel takes wide rows.  Loss and gradient in one call read a row twice, the second time
 // from the ring and L2: three CTAs an SM with slices of 200 KB keep about 70 MB of rows under way
-// (4096 x 151936 bf16: 374 us; 408 with four CTAs, whose rows do not stay in L2, 438 with whole
+// (4096 x 151936 bf16: 373 us; 408 with four CTAs, whose rows do not stay in L2, 438 with whole
 // rows).  One reading wants few splits: slices of 640 KB (the loss of 1024 x 151936 bf16 45 us, of
 // 512 x 262144 fp32 84 us; 47 and 88 with 160 KB, 59 and 132 with 80 KB).
-using Twice = RowGeometry<256, 3, 8, 200>;
+using Twice = RowGeometry<256, 3, 9, 200>;
 using Once = RowGeometry<256, 4, 6, 640>;
 
 // Of the rows that a call reads twice in two passes, the last ones stay in L2 for the second pass,
