@@ -125,9 +125,12 @@ __device__ __forceinline__ int count_tokens(const TokenLossArgs& a, int lo, int 
     return n;
 }
 
-// g of a row of the policy, times its factor w.
-__device__ __forceinline__ float row_weight(const TokenLossArgs& a, int row) {
-    return (a.weight != nullptr ? a.weight[row] : 1.f) * a.grad_loss[row];
+// What a row's or pair's gradient is multiplied by, its weight and the gradient by its loss: 0 where
+// one of them is, whatever the other one is.
+__device__ __forceinline__ float loss_factor(const TokenLossArgs& a, int i) {
+    const float w = a.weight != nullptr ? a.weight[i] : 1.f;
+    const float up = a.grad_loss != nullptr ? a.grad_loss[i] : 1.f;
+    return w == 0.f || up == 0.f ? 0.f : w * up;
 }
 
 // g of a row of a sequence, by the whole block: the same in all CTAs of the row.
@@ -137,9 +140,7 @@ __device__ __forceinline__ float sequence_slope(const TokenLossArgs& a, int row)
     if (s < 0 || s >= n) return 0.f;
     const int start = clamp_row(a.offsets[s], a.rows), end = clamp_row(a.offsets[s + 1], a.rows);
     const int i = s < a.pairs ? s : s - a.pairs;
-    const float m = pair_margin(a, i);
-    float w = a.weight != nullptr ? a.weight[i] : 1.f;
-    if (a.grad_loss != nullptr) w *= a.grad_loss[i];
+    const float m = pair_margin(a, i), w = loss_factor(a, i);
     if (w == 0.f || row < start || row >= end) return 0.f;
     float g = w * pair_slope(a, m);
     if (s >= a.pairs) g = -g;
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
     RowSlice<G> sl(r, a.per, a.ring, rank, tid >> 5, smem, l2_policy_evict_first());
     const Out<T> out(a, row, r.row);
     const int token = row_token(a, row, rank == 0 && tid == 0);
-    const float w = L == Loss::kPolicy && token >= 0 ? row_weight(a, row) : 1.f;
+    const float w = L == Loss::kPolicy && token >= 0 ? loss_factor(a, row) : 1.f;
     if (token < 0 || w == 0.f) {  // the row's logits are not read
         store_zeros<T>(r, out.row, out.on_grid, sl.wlo, sl.whi);
         return;

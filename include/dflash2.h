@@ -452,7 +452,7 @@ int dflash2_policy_loss(const void* logits, long long ld, const int32_t* tokens,
  * loss: grad_loss [rows] fp32; logp, lse [rows] as dflash2_policy_loss wrote them; the rest as
  * there.  Where |lse| is 256 or more, or infinite, its fp32 rounding would show in the
  * gradient: the row's sum is taken again from the logits.  A row with grad_loss or weight 0 is
- * not read and its gradient is 0.
+ * not read and its gradient is 0, whatever the other one is.
  */
 int dflash2_policy_loss_backward(const float* grad_loss, const void* logits, long long ld,
                                  const int32_t* tokens, const float* old_logp,
@@ -498,7 +498,8 @@ int dflash2_preference_loss(const void* logits, long long ld, const int32_t* tok
 /*
  * The gradient of dflash2_preference_loss alone: grad_loss [pairs] fp32; seq_logp [2*pairs]
  * and lse [rows] as dflash2_preference_loss wrote them; the rest as there.  A far lse as
- * in dflash2_policy_loss_backward.
+ * in dflash2_policy_loss_backward.  A pair with grad_loss or weight 0 has gradient 0, whatever the
+ * other one is.
  */
 int dflash2_preference_loss_backward(const float* grad_loss, const void* logits, long long ld,
                                      const int32_t* tokens, const int32_t* offsets,

@@ -1,0 +1,65 @@
+"""The operators of training at calls that their documentation allows and that are easily missed:
+rows and pairs without weight beside an upstream gradient that is not finite, steps that are left
+out, given outputs and autograd, lists that do not match, the bits of weights that are rounded by
+chance, and the loops of the example that tunes a head."""
+import numpy as np
+import pytest
+import torch
+
+import dflash2_draft_head_gb300 as df2
+from dflash2_draft_head_gb300 import tune_draft
+from dflash2_draft_head_gb300.train_draft import AdamW
+from loss_rows import INF, NAN, by_numbers, equal_bits, logp64, rows_of
+from test_adamw_gpu import HYPER, Case, _chance, _expect, _one
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    df2.build_library()
+    df2.lib()
+    yield
+    torch.cuda.synchronize()
+    assert df2.take_device_faults() == 0
+
+
+# ------------------------------------------------------------------ no weight, no gradient
+
+
+@pytest.mark.parametrize("odd", [NAN, INF, -INF])
+@pytest.mark.parametrize("V,dtype", [(1000, "f32"), (151936, "bf16")])
+def test_a_policy_row_without_weight_or_upstream_gradient(V, dtype, odd):
+    """Either factor 0 makes the gradient 0 and leaves the row unread, whatever the other one is;
+    other rows do not notice."""
+    z, tokens, _ = rows_of(6, V, dtype, 21, pad=1)
+    old = logp64(z, tokens, 1.0)[0].float() - 0.05
+    A, ref = by_numbers([1.0, -1.0, 0.5, 2.0, 1.0, -0.5], [-1.0] * 6)
+    kw = dict(ref_logp=ref, kl_coef=0.1)
+    _, logp, lse, _ = df2.policy_loss(z, tokens, old, A, **kw)
+    w, up = by_numbers([1.0, 0.0, 2.0, -0.0, odd, 0.5], [1.0, odd, 0.5, odd, 0.0, 2.0])
+    silent = [1, 3, 4]
+    plain_w, plain_up = w.clone(), up.clone()
+    plain_w[silent] = plain_up[silent] = 0.0
+    want = df2.policy_loss_backward(plain_up, z, tokens, old, A, logp, lse, weight=plain_w, **kw)
+    z[silent] = NAN
+    grad = df2.policy_loss_backward(up, z, tokens, old, A, logp, lse, weight=w, **kw)
+    assert not grad[silent].any() and want[[0, 2, 5]].any(1).all()
+    assert equal_bits(grad, want)
+
+
+@pytest.mark.parametrize("odd", [NAN, INF, -INF])
+@pytest.mark.parametrize("average", [False, True])
+def test_a_pair_without_weight_or_upstream_gradient(average, odd):
+    for V, dtype in ((1000, "f32"), (151936, "bf16")):
+        z, tokens, _ = rows_of(9, V, dtype, 22, pad=1)
+        offsets = torch.tensor([0, 1, 3, 5, 6, 8, 9], dtype=torch.int32, device="cuda")
+        _, seq, _, lse, _ = df2.preference_loss(z, tokens, offsets, average=average)
+        w, up = by_numbers([0.0, 2.0, odd], [odd, 0.5, 0.0])
+        plain_w, plain_up = by_numbers([0.0, 2.0, 0.0], [0.0, 0.5, 0.0])
+        kw = dict(average=average)
+        want = df2.preference_loss_backward(plain_up, z, tokens, offsets, seq, lse, weight=plain_w,
+                                            **kw)
+        grad = df2.preference_loss_backward(up, z, tokens, offsets, seq, lse, weight=w, **kw)
+        assert not grad[[0, 3, 4, 5, 8]].any() and grad[[1, 2, 6, 7]].any(1).all()
+        assert equal_bits(grad, want)
