@@ -771,7 +771,8 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, beta1=0.9, beta2=0.999, 
     to begin with (state_encode and state_decode go from values to them and back).  master: fp32
     copies of bf16 params, which take the step.  step: the step's number, 1 for the first, or an int32 CUDA
     tensor [1] with it; lr: a number or an fp32 CUDA tensor [1] (both for captured graphs).
-    norm: the gradients' norm (grad_norm); where it is not finite, nothing is changed; with
+    norm: the gradients' norm (grad_norm); where it is not finite, nothing is changed (and a step
+    tensor should not be raised for that call: step += torch.isfinite(norm) ahead of it); with
     max_norm it clips grads * grad_scale.  seed: an integer, by which 8-bit states, and bf16
     params without master, are rounded up or down with odds by the distance (else to the
     nearest, where 8-bit states and small steps of bf16 params get stuck)."""

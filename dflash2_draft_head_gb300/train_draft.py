@@ -30,12 +30,14 @@ def accepted(draft_logits, teacher_logits, uniform, n: int) -> float:
 
 class AdamW:
     """Weights in one list with their AdamW states, clipped by the gradients' norm: fp32
-    states, or 8 bits an element with stochastic rounding from `seed`."""
+    states, or 8 bits an element with stochastic rounding from `seed`.  Steps are counted on the
+    device: one that is left out, as its norm is not finite, does not count."""
 
     def __init__(self, params, lr: float, bits: int = 32, max_norm: float | None = 1.0,
                  weight_decay: float = 0.0, seed: int = 0):
         self.params, self.lr, self.max_norm, self.seed = params, lr, max_norm, seed
-        self.weight_decay, self.step_number = weight_decay, 0
+        self.weight_decay = weight_decay
+        self.step_number = torch.zeros(1, dtype=torch.int32, device=params[0].device)
 
         def zeros(size, dtype):
             return [torch.zeros(size(p), dtype=dtype, device=p.device) for p in params]
@@ -50,8 +52,8 @@ class AdamW:
 
     def step(self, grads) -> torch.Tensor:
         """One step; the gradients' norm [1] before it is clipped."""
-        self.step_number += 1
         norm = df2.grad_norm(grads)
+        self.step_number += torch.isfinite(norm)
         df2.adamw(self.params, grads, self.exp_avg, self.exp_avg_sq, step=self.step_number,
                   lr=self.lr, weight_decay=self.weight_decay, norm=norm, max_norm=self.max_norm,
                   seed=self.seed if self.scales else None, **self.scales)

@@ -550,7 +550,8 @@ int dflash2_grad_norm(int count, const void* const* grads, const int64_t* sizes,
  *   step    number of the step, 1 for the first; step_at: not NULL, one device int32 that holds
  *           it (for a captured graph that is replayed).  lr_at likewise, one fp32 for lr
  *   norm    NULL, or one device fp32, the gradients' norm: where it is not finite nothing is
- *           changed.  max_norm > 0 clips by it; 0: no limit
+ *           changed.  The step's number is the caller's: a step that was left out counts unless
+ *           step_at rises by finite norms alone.  max_norm > 0 clips by it; 0: no limit
  *   by_chance  0: all rounding is to the nearest.  Else 8-bit states, and bf16 parameters without
  *           master copies, are rounded up or down with odds by the distance, by bits made of
  *           seed, step, the tensor's place in the list and the element's place in it: the

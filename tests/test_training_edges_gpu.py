@@ -63,3 +63,25 @@ def test_a_pair_without_weight_or_upstream_gradient(average, odd):
         grad = df2.preference_loss_backward(up, z, tokens, offsets, seq, lse, weight=w, **kw)
         assert not grad[[0, 3, 4, 5, 8]].any() and grad[[1, 2, 6, 7]].any(1).all()
         assert equal_bits(grad, want)
+
+
+# ------------------------------------------------------------------ steps that are left out
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_step_that_is_left_out_does_not_count(bits):
+    """Bad gradients at the first step and at a later one: as if they had not been."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    start = torch.randn(5000, device="cuda", generator=g)
+    grads = [torch.randn(5000, device="cuda", generator=g) for _ in range(4)]
+    bad = grads[0].clone()
+    bad[17] = NAN
+    with_bad, plain = (AdamW([start.clone()], 1e-2, bits, seed=5) for _ in range(2))
+    for k, x in enumerate(grads):
+        if k in (0, 2):
+            assert torch.isnan(with_bad.step([bad]))
+        a, b = with_bad.step([x]), plain.step([x])
+        assert equal_bits(a, b) and equal_bits(with_bad.params[0], plain.params[0])
+        assert torch.equal(with_bad.exp_avg[0], plain.exp_avg[0])
+        assert torch.equal(with_bad.exp_avg_sq[0], plain.exp_avg_sq[0])
