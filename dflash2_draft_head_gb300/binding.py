@@ -770,7 +770,8 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, beta1=0.9, beta2=0.999, 
     exp_avg_scale and exp_avg_sq_scale ([(numel + 31) // 32] uint8 each): states in 8 bits, zeros
     to begin with (state_encode and state_decode go from values to them and back).  master: fp32
     copies of bf16 params, which take the step.  step: the step's number, 1 for the first, or an int32 CUDA
-    tensor [1] with it; lr: a number or an fp32 CUDA tensor [1] (both for captured graphs).
+    tensor [1] with it; lr: a number or an fp32 CUDA tensor [1] (both for captured graphs; a
+    step below 1 or an lr that is not finite is refused, in a tensor nothing is changed).
     norm: the gradients' norm (grad_norm); where it is not finite, nothing is changed (and a step
     tensor should not be raised for that call: step += torch.isfinite(norm) ahead of it); with
     max_norm it clips grads * grad_scale.  seed: an integer, by which 8-bit states, and bf16

@@ -588,6 +588,7 @@ __global__ void __launch_bounds__(AdamShape<S8>::kThreads, AdamShape<S8>::kMinCt
     const int step = b.step_at != nullptr ? *b.step_at : b.step;
     if (b.step_at != nullptr || b.lr_at != nullptr) {
         const float lr = b.lr_at != nullptr ? *b.lr_at : b.lr;
+        if (step < 1 || !(fabsf(lr) < INFINITY)) return;  // what a call refuses on the host
         c.decay = lr * b.weight_decay;
         c.rate = lr / -expm1f((float)step * b.ln_beta1);
         c.root = rsqrtf(-expm1f((float)step * b.ln_beta2));

@@ -548,7 +548,8 @@ int dflash2_grad_norm(int count, const void* const* grads, const int64_t* sizes,
  *           they are rounded; a v above 0 keeps a code above 0.  A block with an infinite or NaN
  *           value gets scale 255 and codes 0, which read as NaN
  *   step    number of the step, 1 for the first; step_at: not NULL, one device int32 that holds
- *           it (for a captured graph that is replayed).  lr_at likewise, one fp32 for lr
+ *           it (for a captured graph that is replayed).  lr_at likewise, one fp32 for lr.  Where
+ *           step_at holds a number below 1, or lr_at one that is not finite, nothing is changed
  *   norm    NULL, or one device fp32, the gradients' norm: where it is not finite nothing is
  *           changed.  The step's number is the caller's: a step that was left out counts unless
  *           step_at rises by finite norms alone.  max_norm > 0 clips by it; 0: no limit

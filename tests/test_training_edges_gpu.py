@@ -85,3 +85,19 @@ def test_a_step_that_is_left_out_does_not_count(bits):
         assert equal_bits(a, b) and equal_bits(with_bad.params[0], plain.params[0])
         assert torch.equal(with_bad.exp_avg[0], plain.exp_avg[0])
         assert torch.equal(with_bad.exp_avg_sq[0], plain.exp_avg_sq[0])
+
+
+@pytest.mark.parametrize("setting", [dict(step=0), dict(step=-3), dict(lr=NAN), dict(lr=INF),
+                                     dict(lr=-INF)])
+def test_a_setting_on_the_device_that_a_host_call_refuses_leaves_everything_as_it_was(setting):
+    for small in (False, True):
+        case = Case([3000, 17], "bf16", "bf16", small=small, master=True, offset=1)
+        before = case.copy()
+        args, more = case.args()
+        kind = dict(step=torch.int32, lr=torch.float32)
+        kw = HYPER | dict(step=1) | {k: torch.tensor([v], dtype=kind[k], device="cuda")
+                                     for k, v in setting.items()}
+        df2.adamw(*args, seed=3, **kw, **more)
+        for name, ts in case.lists.items():
+            for t, old in zip(ts, before[name]):
+                assert torch.equal(torch.nan_to_num(t._base.float()), torch.nan_to_num(old.float()))
