@@ -583,7 +583,13 @@ __global__ void __launch_bounds__(AdamShape<S8>::kThreads, AdamShape<S8>::kMinCt
     if (b.norm != nullptr) {
         const float norm = *b.norm;
         if (!(fabsf(norm) < INFINITY)) return;  // the step is left out
-        if (b.max_norm > 0.f) c.scale *= fminf(b.max_norm / (norm * fabsf(b.grad_scale)), 1.f);
+        if (b.max_norm > 0.f) {
+            const float whole = norm * fabsf(b.grad_scale);
+            if (whole < INFINITY)
+                c.scale *= fminf(b.max_norm / whole, 1.f);
+            else  // the product alone leaves fp32
+                c.scale = copysignf(fminf(b.max_norm / norm, fabsf(c.scale)), c.scale);
+        }
     }
     const int step = b.step_at != nullptr ? *b.step_at : b.step;
     if (b.step_at != nullptr || b.lr_at != nullptr) {

@@ -101,3 +101,19 @@ def test_a_setting_on_the_device_that_a_host_call_refuses_leaves_everything_as_i
         for name, ts in case.lists.items():
             for t, old in zip(ts, before[name]):
                 assert torch.equal(torch.nan_to_num(t._base.float()), torch.nan_to_num(old.float()))
+
+
+def test_clipping_where_the_scaled_norm_leaves_fp32():
+    """norm * |grad_scale| above 3.4e38, the norm itself below: the gradient is clipped, not lost.
+    The factor max_norm / norm is a normal number; norm, factor, g' and m are rounded once each and
+    the norm's sum to 2^-21: 2^-19 is a bound on m's error."""
+    n = 40
+    x = torch.full((n,), 2.0 ** 120, device="cuda")
+    norm = df2.grad_norm([x])
+    assert torch.isfinite(norm) and norm.item() * 2.0 ** 10 > 3.5e38
+    p, m, v = (torch.zeros(n, device="cuda") for _ in range(3))
+    df2.adamw([p], [x], [m], [v], step=1, lr=1e-2, norm=norm, max_norm=1.0, grad_scale=2.0 ** 10)
+    want = 0.1 / n ** 0.5
+    assert (m.double() - want).abs().max().item() <= 2.0 ** -19 * want
+    # the first step of Adam moves by lr against the gradient; eps is 1e-8 of 0.16 beside it
+    assert (p.double() + 1e-2).abs().max().item() <= 1e-2 * 2.0 ** -17
