@@ -420,6 +420,8 @@ int run_adamw(const df2::AdamwArgs& a, int param_dtype, int grad_dtype, void* st
         return fail(DF2_ERR_INVALID_ARG, "adamw: lr, weight_decay and grad_scale must be finite");
     if (!(a.max_norm >= 0))
         return fail(DF2_ERR_INVALID_ARG, "adamw: max_norm=%g must not be negative", a.max_norm);
+    if (a.max_norm > 0 && !((float)a.max_norm > 0.f))  // it would count as no limit
+        return fail(DF2_ERR_INVALID_ARG, "adamw: max_norm=%g is 0 in fp32", a.max_norm);
     if (a.max_norm > 0 && a.norm == nullptr)
         return fail(DF2_ERR_INVALID_ARG, "adamw: max_norm needs the gradients' norm");
     if (a.step_at == nullptr && a.step < 1)

@@ -563,9 +563,9 @@ int dflash2_grad_norm(int count, const void* const* grads, const int64_t* sizes,
  * bytes (8-bit states: 8), single elements otherwise.
  * INVALID_ARG: count < 0; a negative size; NULL required pointer; bad dtype; misalignment to an
  * element; beta1 or beta2 outside [0, 1); eps not positive (in fp32) or not finite; lr, weight_decay
- * or grad_scale not finite; max_norm negative or NaN, or without norm; step < 1; one scale
- * array without the other; master with fp32 parameters; a tensor that is written overlapping any
- * other (or listed twice).  UNSUPPORTED: a tensor of more than 2^40 elements.
+ * or grad_scale not finite; max_norm negative or NaN, above 0 but 0 in fp32, or without norm;
+ * step < 1; one scale array without the other; master with fp32 parameters; a tensor that is
+ * written overlapping any other (or listed twice).  UNSUPPORTED: a tensor of more than 2^40 elements.
  */
 int dflash2_adamw(int count, void* const* params, const void* const* grads, void* const* exp_avg,
                   void* const* exp_avg_sq, float* const* master, uint8_t* const* exp_avg_scale,

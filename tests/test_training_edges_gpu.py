@@ -117,3 +117,14 @@ def test_clipping_where_the_scaled_norm_leaves_fp32():
     assert (m.double() - want).abs().max().item() <= 2.0 ** -19 * want
     # the first step of Adam moves by lr against the gradient; eps is 1e-8 of 0.16 beside it
     assert (p.double() + 1e-2).abs().max().item() <= 1e-2 * 2.0 ** -17
+
+
+# ------------------------------------------------------------------ lists
+
+
+def test_a_limit_of_the_norm_that_fp32_does_not_hold():
+    """It would count as 0, which is no limit."""
+    one = torch.ones(1, device="cuda")
+    with pytest.raises(df2.Dflash2Error, match="max_norm"):
+        df2.adamw(**_one(norm=one, max_norm=1e-60))
+    df2.adamw(**_one(norm=one, max_norm=1e-40))
