@@ -558,6 +558,14 @@ def _grad_on(grad, logits, ld):
     return grad, ptr, grad_ld
 
 
+def _written(outs):
+    """Raises the versions of the outputs that a caller gave, for autograd, which may have saved
+    them.  Before the launch, which may fail when a part of it is under way."""
+    given = [t for t in outs if isinstance(t, torch.Tensor)]
+    if given:
+        increment_version(given)
+
+
 def policy_loss(logits, tokens, old_logp, advantage, ref_logp=None, temperature=1.0, clip_low=0.2,
                 clip_high=0.2, kl_coef=0.0, weight=None, grad=False, loss=None, logp=None, lse=None,
                 err_flag=None):
@@ -576,17 +584,16 @@ def policy_loss(logits, tokens, old_logp, advantage, ref_logp=None, temperature=
     ins = (_on(tokens, "tokens", torch.int32, shape, at), _on(old_logp, "old_logp", f32, shape, at),
            _on(advantage, "advantage", f32, shape, at), _on(ref_logp, "ref_logp", f32, shape, at),
            _on(weight, "weight", f32, shape, at))
+    given = (loss, logp, lse, grad)
     loss, loss_ptr = _out_on(loss, "loss", f32, shape, dev, old_logp)
     logp, logp_ptr = _out_on(logp, "logp", f32, shape, dev, old_logp)
     lse, lse_ptr = _out_on(lse, "lse", f32, shape, dev, old_logp)
     flag = None if err_flag is None else _on(err_flag, "err_flag", torch.int32, (1,), at)
-    given = isinstance(grad, torch.Tensor)
     grad, grad_ptr, grad_ld = _grad_on(grad, logits, ld)
+    _written(given)
     _launch(at, lib().dflash2_policy_loss, logits.data_ptr(), ld, *ins, rows, V, temperature,
             clip_low, clip_high, kl_coef, _code(logits.dtype), loss_ptr, logp_ptr, lse_ptr,
             grad_ptr, grad_ld, flag)
-    if given:
-        increment_version(grad)
     return loss, logp, lse, grad
 
 
@@ -604,13 +611,12 @@ def policy_loss_backward(grad_loss, logits, tokens, old_logp, advantage, logp, l
            _on(weight, "weight", f32, shape, at), _on(logp, "logp", f32, shape, at),
            _on(lse, "lse", f32, shape, at))
     flag = _on(err_flag, "err_flag", torch.int32, (1,), at)
-    given = isinstance(grad, torch.Tensor)
+    given = (grad,)
     grad, grad_ptr, grad_ld = _grad_on(grad, logits, ld)
+    _written(given)
     _launch(at, lib().dflash2_policy_loss_backward, up, logits.data_ptr(), ld, *ins, rows, V,
             temperature, clip_low, clip_high, kl_coef, _code(logits.dtype), grad_ptr, grad_ld,
             flag)
-    if given:
-        increment_version(grad)
     return grad
 
 
@@ -642,18 +648,17 @@ def preference_loss(logits, tokens, offsets, ref_logp=None, beta=0.1, label_smoo
            _on(offsets, "offsets", torch.int32, (2 * pairs + 1,), at),
            _on(ref_logp, "ref_logp", f32, (2 * pairs,), at),
            _on(weight, "weight", f32, (pairs,), at))
+    given = (loss, seq_logp, logp, lse, grad)
     loss, loss_ptr = _out_on(loss, "loss", f32, (pairs,), dev, weight)
     seq_logp, seq_ptr = _out_on(seq_logp, "seq_logp", f32, (2 * pairs,), dev, ref_logp)
     logp, logp_ptr = _out_on(logp, "logp", f32, shape, dev)
     lse, lse_ptr = _out_on(lse, "lse", f32, shape, dev, logp)
     flag = _on(err_flag, "err_flag", torch.int32, (1,), at)
-    given = isinstance(grad, torch.Tensor)
     grad, grad_ptr, grad_ld = _grad_on(grad, logits, ld)
+    _written(given)
     _launch(at, lib().dflash2_preference_loss, logits.data_ptr(), ld, *ins, rows, V, pairs, beta,
             label_smoothing, margin, average, _code(logits.dtype), loss_ptr, seq_ptr, logp_ptr,
             lse_ptr, grad_ptr, grad_ld, flag)
-    if given:
-        increment_version(grad)
     return loss, seq_logp, logp, lse, grad
 
 
@@ -672,13 +677,12 @@ def preference_loss_backward(grad_loss, logits, tokens, offsets, seq_logp, lse, 
            _on(weight, "weight", f32, (pairs,), at),
            _on(seq_logp, "seq_logp", f32, (2 * pairs,), at), _on(lse, "lse", f32, shape, at))
     flag = _on(err_flag, "err_flag", torch.int32, (1,), at)
-    given = isinstance(grad, torch.Tensor)
+    given = (grad,)
     grad, grad_ptr, grad_ld = _grad_on(grad, logits, ld)
+    _written(given)
     _launch(at, lib().dflash2_preference_loss_backward, up, logits.data_ptr(), ld, *ins, rows, V,
             pairs, beta, label_smoothing, margin, average, _code(logits.dtype), grad_ptr, grad_ld,
             flag)
-    if given:
-        increment_version(grad)
     return grad
 
 
@@ -748,6 +752,7 @@ def grad_norm(grads, out=None, workspace=None):
     code = _code(ts.dtype("grads"))
     dev = ts.all[0].device
     held, sizes, ptrs = ts.arrays(ts.numels)
+    given = (out,)
     out, out_ptr = _out_on(out, "out", torch.float32, (1,), dev)
     ws, ws_bytes = None, 0
     if workspace is not None:
@@ -758,6 +763,7 @@ def grad_norm(grads, out=None, workspace=None):
         if ws_bytes > 0:
             workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=dev)
             ws = workspace.data_ptr()
+    _written(given)
     _launch(ts.index, L.dflash2_grad_norm, ts.n, ptrs["grads"], sizes, code, ws, ws_bytes, out_ptr)
     return out
 
@@ -811,7 +817,7 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, beta1=0.9, beta2=0.999, 
         raise ValueError(f"step={step}: the first step is 1, the last one 2^31 - 1")
     lr_at, lr = _setting_on(lr, "lr", f32, at)
     norm_at = _on(norm, "norm", f32, (1,), at)
-    # before the launch: an inference tensor outside its mode forbids it
+    # before the launch, which may fail when a part of it is under way
     increment_version(ts[:n] + ts[2 * n:])
     held = array.array("Q", sizes + list(map(_data_ptr, ts)))  # lives until the call returns
     p, by = held.buffer_info()[0], 8 * n
@@ -865,7 +871,9 @@ def state_decode(codes, scale, squares=False, dtype=torch.float32, out=None):
     s = _on(scale, "scale", torch.uint8, (-(-n // 32),), index)
     dtype = out.dtype if out is not None else dtype
     code = _code(dtype)
+    given = (out,)
     out, out_ptr = _out_on(out, "out", dtype, codes.shape, codes.device)
+    _written(given)
     _launch(index, lib().dflash2_state_decode, c, s, n, squares, code, out_ptr)
     return out
 
@@ -878,9 +886,11 @@ def state_encode(values, squares=False, codes=None, scale=None):
         raise ValueError("values must be a CUDA tensor")
     n = values.numel()
     v = _on(values, "values", values.dtype, values.shape, index)
+    code, given = _code(values.dtype), (codes, scale)
     codes, c = _out_on(codes, "codes", torch.uint8, values.shape, values.device)
     scale, s = _out_on(scale, "scale", torch.uint8, (-(-n // 32),), values.device)
-    _launch(index, lib().dflash2_state_encode, v, _code(values.dtype), n, squares, c, s)
+    _written(given)
+    _launch(index, lib().dflash2_state_encode, v, code, n, squares, c, s)
     return codes, scale
 
 

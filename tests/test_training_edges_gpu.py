@@ -119,6 +119,77 @@ def test_clipping_where_the_scaled_norm_leaves_fp32():
     assert (p.double() + 1e-2).abs().max().item() <= 1e-2 * 2.0 ** -17
 
 
+# ------------------------------------------------------------------ given outputs
+
+
+def _small_rows():
+    z, tokens, _ = rows_of(4, 100, "f32", 23)
+    return z.contiguous().clone(), tokens, torch.full((4,), -3.0, device="cuda")
+
+
+def _writers():
+    """(name, outputs, call that writes them) of every entry point that takes outputs."""
+    z, tokens, f = _small_rows()
+    A = torch.ones(4, device="cuda")
+    offsets = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+    up = torch.ones(1, device="cuda")
+
+    def new(*s, dtype=torch.float32):
+        return torch.full(s, 3, dtype=dtype, device="cuda")
+
+    _, logp, lse, _ = df2.policy_loss(z, tokens, f, A)
+    _, seq, _, plse, _ = df2.preference_loss(z, tokens, offsets)
+    codes, scale = df2.state_encode(torch.ones(70, device="cuda"))
+    return [
+        ("policy", dict(loss=new(4), logp=new(4), lse=new(4), grad=new(4, 100)),
+         lambda o: df2.policy_loss(z, tokens, f, A, **o)),
+        ("policy_back", dict(grad=new(4, 100)),
+         lambda o: df2.policy_loss_backward(A, z, tokens, f, A, logp, lse, **o)),
+        ("preference", dict(loss=new(1), seq_logp=new(2), logp=new(4), lse=new(4), grad=new(4, 100)),
+         lambda o: df2.preference_loss(z, tokens, offsets, **o)),
+        ("preference_back", dict(grad=new(4, 100)),
+         lambda o: df2.preference_loss_backward(up, z, tokens, offsets, seq, plse, **o)),
+        ("norm", dict(out=new(1)), lambda o: df2.grad_norm([z], **o)),
+        ("decode", dict(out=new(70)), lambda o: df2.state_decode(codes, scale, **o)),
+        ("encode", dict(codes=new(70, dtype=torch.uint8), scale=new(3, dtype=torch.uint8)),
+         lambda o: df2.state_encode(torch.ones(70, device="cuda"), **o)),
+    ]
+
+
+WRITERS = ["policy", "policy_back", "preference", "preference_back", "norm", "decode", "encode"]
+
+
+@pytest.mark.parametrize("k", range(len(WRITERS)), ids=WRITERS)
+def test_what_is_written_raises_its_version(k):
+    name, outs, call = _writers()[k]
+    assert name == WRITERS[k]
+    before = {n: t._version for n, t in outs.items()}
+    call(outs)
+    for n, t in outs.items():
+        assert t._version == before[n] + 1, n
+    for n, t in outs.items():
+        if not t.is_floating_point():
+            continue
+        x = torch.ones_like(t).requires_grad_()
+        later = (x * t).sum()                   # saves t
+        call(outs)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            later.backward()
+
+
+@pytest.mark.parametrize("k", range(len(WRITERS)), ids=WRITERS)
+def test_outputs_made_in_inference_mode(k):
+    """They have no version, and autograd does not save them: taken, in that mode and outside."""
+    _, outs, call = _writers()[k]
+    with torch.inference_mode():
+        inside, outside = ({n: t.clone() for n, t in outs.items()} for _ in range(2))
+        call(inside)
+    call(outside)
+    call(outs)
+    for n, t in outs.items():
+        assert torch.equal(inside[n], t) and torch.equal(outside[n], t), n
+
+
 # ------------------------------------------------------------------ lists
 
 
