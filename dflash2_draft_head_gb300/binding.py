@@ -561,9 +561,9 @@ def _grad_on(grad, logits, ld):
 def _written(outs):
     """Raises the versions of the outputs that a caller gave, for autograd, which may have saved
     them.  Before the launch, which may fail when a part of it is under way."""
-    given = [t for t in outs if isinstance(t, torch.Tensor)]
-    if given:
-        increment_version(given)
+    for t in outs:
+        if t is not None and isinstance(t, torch.Tensor):
+            increment_version(t)
 
 
 def policy_loss(logits, tokens, old_logp, advantage, ref_logp=None, temperature=1.0, clip_low=0.2,
