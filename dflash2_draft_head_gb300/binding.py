@@ -784,7 +784,8 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, beta1=0.9, beta2=0.999, 
     params without master, are rounded up or down with odds by the distance (else to the
     nearest, where 8-bit states and small steps of bf16 params get stuck)."""
     if len(params) == 0:
-        if any(len(v) for v in (grads, exp_avg, exp_avg_sq)):
+        if any(v is not None and len(v) for v in (grads, exp_avg, exp_avg_sq, master, exp_avg_scale,
+                                                  exp_avg_sq_scale)):
             raise ValueError("params is empty, other lists are not")
         return
     f32, n = torch.float32, len(params)
@@ -806,7 +807,7 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, beta1=0.9, beta2=0.999, 
                 [torch.uint8] * len(blocks) and
                 numels[2 * n:] == sizes * (2 if master is None else 3) + blocks and
                 list(map(_shape_of, grads)) == list(map(_shape_of, params)) and
-                n == len(grads) == len(exp_avg) == len(exp_avg_sq))
+                set(map(len, lists)) == {n})
     except (AttributeError, TypeError):  # no tensors, or no list
         fine = False
     if not fine:

@@ -193,6 +193,31 @@ def test_outputs_made_in_inference_mode(k):
 # ------------------------------------------------------------------ lists
 
 
+def test_scales_that_are_in_the_wrong_list():
+    """As many scales as there have to be, but one of exp_avg_sq's among exp_avg's."""
+    def small(n):
+        return torch.zeros(n, dtype=torch.uint8, device="cuda")
+
+    def lists():
+        return [[torch.zeros(40, device="cuda") for _ in range(2)] for _ in range(2)] + \
+            [[small(40) for _ in range(2)] for _ in range(2)]
+
+    for a, b in ((3, 1), (1, 3), (4, 0)):
+        with pytest.raises(ValueError, match="must have 2 tensors"):
+            df2.adamw(*lists(), step=1, lr=1e-3, exp_avg_scale=[small(2) for _ in range(a)],
+                      exp_avg_sq_scale=[small(2) for _ in range(b)])
+    df2.adamw(*lists(), step=1, lr=1e-3, exp_avg_scale=[small(2) for _ in range(2)],
+              exp_avg_sq_scale=[small(2) for _ in range(2)])
+
+
+@pytest.mark.parametrize("name,dtype", [("master", torch.float32), ("exp_avg_scale", torch.uint8),
+                                        ("exp_avg_sq_scale", torch.uint8)])
+def test_no_parameters_beside_other_lists(name, dtype):
+    with pytest.raises(ValueError):
+        df2.adamw([], [], [], [], step=1, lr=1e-3,
+                  **{name: [torch.zeros(2, dtype=dtype, device="cuda")]})
+
+
 def test_a_limit_of_the_norm_that_fp32_does_not_hold():
     """It would count as 0, which is no limit."""
     one = torch.ones(1, device="cuda")
