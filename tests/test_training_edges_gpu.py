@@ -224,3 +224,123 @@ def test_a_limit_of_the_norm_that_fp32_does_not_hold():
     with pytest.raises(df2.Dflash2Error, match="max_norm"):
         df2.adamw(**_one(norm=one, max_norm=1e-60))
     df2.adamw(**_one(norm=one, max_norm=1e-40))
+
+
+# ------------------------------------------------------------------ weights rounded by chance
+
+
+def _by_chance(w, bits):
+    """fp32's upper half after 16 bits of chance are added, from a value in 64 bits: towards 0 in
+    steps of bf16."""
+    ulp = 2.0 ** (np.frexp(np.where(w == 0, 1.0, np.abs(w)))[1] - 8.0)
+    return np.sign(w) * np.floor(np.abs(w) / ulp + bits / 65536.0) * ulp
+
+
+@pytest.mark.parametrize("small", [False, True])
+@pytest.mark.parametrize("g", ["f32", "bf16"])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_weights_rounded_by_chance_bit_by_bit(small, g, offset):
+    """bf16 weights are where the element's own bits put them.  Where the bound of the step's error
+    in fp32 reaches over the place at which they decide, the neighbour is right too: twice the bound
+    over a bf16 step of them, 2^-13 where the weight's own rounding makes up the bound."""
+    for sizes in ([1, 33, 4097, 20011], [7] * 390):       # the second goes in two launches
+        for step, seed in ((1, 5), (1000, 2 ** 40 + 12345)):
+            case = Case(sizes, "bf16", g, small, offset=offset, seed=step)
+            args, more = case.args()
+            values = case.values()
+            df2.adamw(*args, step=step, seed=seed, **HYPER, **more)
+            clear, total = 0, 0
+            for k, (_, _, (w, wb), _, _) in enumerate(_expect(values, step, 1.0, **HYPER)):
+                bits = _chance(sizes[k], seed, step, k)[2].astype(np.float64)
+                inner = np.where(np.abs(w) > wb, w - np.sign(w) * wb, 0.0)
+                a, b = _by_chance(inner, bits), _by_chance(w + np.sign(w) * wb, bits)
+                got = case.lists["params"][k].double().cpu().numpy()
+                assert ((got >= np.minimum(a, b)) & (got <= np.maximum(a, b))).all(), (k, step)
+                clear, total = clear + (a == b).sum(), total + len(a)
+            assert clear >= 0.98 * total
+
+
+# ------------------------------------------------------------------ the loops of the example
+
+
+@pytest.mark.parametrize("method", ["policy", "preference"])
+def test_the_tuning_loop_follows_its_formula(method, monkeypatch):
+    """What the loop hands on: old and reference log-probabilities of the drawn tokens, a higher
+    worth for tokens that are the target's, chosen drafts that hit more, the formula's gradient by
+    the weight, and a step against it."""
+    seen = dict(states=[], sampled=[], steps=[])
+    real = {n: getattr(tune_draft.df2, n) for n in ("sample", "policy_loss", "preference_loss")}
+    randn = torch.randn
+
+    def states(*a, **k):
+        t = randn(*a, **k)
+        seen["states"].append(t)
+        return t
+
+    def sample(z, *a, **k):
+        out = real["sample"](z, *a, **k)
+        seen["sampled"].append(out[0].clone())
+        return out
+
+    def loss(name):
+        def call(z, *a, **k):
+            if k.get("grad") is not None:
+                seen["loss"] = (z.clone(), a, {n: t for n, t in k.items() if n != "grad"})
+            return real[name](z, *a, **k)
+        return call
+
+    class Recorded(AdamW):
+        def step(self, grads):
+            before = self.params[0].clone()
+            out = super().step(grads)
+            seen["steps"].append((grads[0], before, self.params[0].clone()))
+            return out
+
+    monkeypatch.setattr(torch, "randn", states)
+    monkeypatch.setattr(tune_draft.df2, "sample", sample)
+    for name in ("policy_loss", "preference_loss"):
+        monkeypatch.setattr(tune_draft.df2, name, loss(name))
+    monkeypatch.setattr(tune_draft, "AdamW", Recorded)
+    n = 16
+    tune_draft.tune(steps=1, blocks=8, n=n, V=512, method=method)
+    # accepted() samples once before and once after the step
+    want, drawn = seen["sampled"][1], seen["sampled"][2:-1]
+    h = seen["states"][-1].double()
+    z, args, kw = seen["loss"]
+    slope, before, after = seen["steps"][0]
+    x = z.double().requires_grad_()
+    tokens = args[0].long()
+    logp = torch.log_softmax(x, 1).gather(1, tokens[:, None]).squeeze(1)
+    if method == "policy":
+        old, A = args[1], args[2]
+        assert torch.equal(args[0], drawn[0])
+        hit = args[0] == want
+        assert hit.any() and not hit.all() and (A[hit] > 0).all() and (A[~hit] < 0).all()
+        assert (old.double() - logp.detach()).abs().max() <= 1e-4
+        # the reference is the head itself at the first step
+        assert (kw["ref_logp"].double() - logp.detach()).abs().max() <= 1e-4
+        rho, d = torch.exp(logp - old.double()), kw["ref_logp"].double() - logp
+        each = kw["kl_coef"] * (torch.exp(d) - d - 1) - torch.minimum(rho * A, rho.clamp(0.8, 1.2) * A)
+        (each * kw["weight"]).sum().backward()
+    else:
+        h = h.repeat(2, 1)
+        pairs = (args[1].numel() - 1) // 2
+        assert args[1].tolist() == list(range(0, 2 * pairs * n + 1, n))
+        target = want.view(pairs, n)
+        chosen, rejected = args[0].view(2, pairs, n)
+        better, worse = ((t == target).sum(1) for t in (chosen, rejected))
+        assert (better >= worse).all() and (better > worse).any()
+        assert torch.equal(kw["weight"] > 0, better > worse)
+        S = logp.view(2 * pairs, n).sum(1)
+        assert (kw["ref_logp"].double() - S.detach()).abs().max() <= n * 1e-4
+        r = S - kw["ref_logp"].double()
+        m = kw["beta"] * (r[:pairs] - r[pairs:])
+        (kw["weight"].double() * torch.nn.functional.softplus(-m)).sum().backward()
+    # the logits' gradient is rounded to bf16 (2^-8 of the value), its shares are good to 1e-5, and
+    # so is the product with the states to 2^-23 * rows of the sum of its terms' magnitudes
+    size = x.grad.abs().t() @ h.abs()
+    bound = size * (2.0 ** -8 + 2.0 ** -23 * h.shape[0]) + 1e-4 * x.grad.abs().amax() * h.abs().sum(0)
+    assert ((slope.double() - x.grad.t() @ h).abs() <= bound).all()
+    assert slope.any() and ((after - before).double() * slope.double()).sum() < 0
+    moved = after != before
+    assert (((after - before).sign() == -slope.sign()) | (slope.abs() < 1e-6) | ~moved).all()
