@@ -1,13 +1,14 @@
 // Optimizer states in 8 bits: 32 neighbours share a power of two, and each has the bits of a
 // short float.
 //
-//   exp_avg     sign, 4 bits of exponent, 3 of mantissa (values 2^-9 to 240)
-//   exp_avg_sq  5 bits of exponent, 3 of mantissa (values 2^-17 to 61440; no sign)
+//   exp_avg     sign, 4 bits of exponent, 3 of mantissa (values 2^-9 to 480)
+//   exp_avg_sq  5 bits of exponent, 3 of mantissa (values 2^-17 to 122880; no sign)
 //
 // value = short float * 2^(scale - 127); the block's largest lies in the second highest power
-// of two, so that rounding up cannot overflow.  Both short floats are the top of an fp32
-// number's bits at the bottom of its exponents: codes << 20 is the value times 2^-120 (2^-112),
-// subnormal ones included, and back is an integer addition (the rounding) and a shift.
+// of two (below 256 and 65536), so that rounding up, to these at most, cannot overflow.  Both
+// short floats are the top of an fp32 number's bits at the bottom of its exponents: codes << 20 is
+// the value times 2^-120 (2^-112), subnormal ones included, and back is an integer addition (the
+// rounding) and a shift.
 // Each product is by a power of two, so a value has at most 4 significant bits and is
 // exact in bf16.  scale 255 stands for a block with an infinite or NaN value, which reads as NaN.
 #pragma once

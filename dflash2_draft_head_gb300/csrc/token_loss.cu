@@ -38,8 +38,8 @@ using Twice = RowGeometry<256, 3, 9, 200>;
 using Once = RowGeometry<256, 4, 6, 640>;
 
 // Of the rows that a call reads twice in two passes, the last ones stay in L2 for the second pass,
-// which goes backwards: 2048 x 151936 bf16 with the gradient 282 us, 289 without; 400 rows 64 and
-// 70 (with 96 MB 283 and 64).
+// which goes backwards: 2048 x 151936 bf16, all with a token, with the gradient 282 us, 289 without;
+// 400 rows 64 and 70 (with 96 MB 283 and 64).
 constexpr long long kKeepBytes = 64ll << 20;
 
 // As split_rows, but few rows are split only as far as their CTAs run all at once: the meetings of
@@ -98,7 +98,9 @@ __device__ __forceinline__ int offsets_upto(const int* offsets, int n, int row) 
 
 __device__ __forceinline__ int clamp_row(int v, int rows) { return min(max(v, 0), rows); }
 
-// d loss / d S of a pair's chosen sequence, without the weight (the rejected one's: minus that).
+// A pair's m for the gradient: from the sums as they are returned, in fp32 (the loss takes those in
+// 64 bits), so that the call with the loss and the gradient alone give the same bits.  Off by up to
+// beta * 2^-22 of the sums' and references' magnitudes.
 __device__ __forceinline__ float pair_margin(const TokenLossArgs& a, int i) {
     float c = a.seq_logp[i], r = a.seq_logp[a.pairs + i];
     if (a.ref_logp != nullptr) {
@@ -107,13 +109,17 @@ __device__ __forceinline__ float pair_margin(const TokenLossArgs& a, int i) {
     }
     return fmaf(a.beta, c - r, -a.margin);
 }
+// d loss / d S of a pair's chosen sequence, without the weight (the rejected one's: minus that).
 __device__ __forceinline__ float pair_slope(const TokenLossArgs& a, float m) {
     float s = (1.f - a.smoothing) / (1.f + expf(m));
     if (a.smoothing != 0.f) s -= a.smoothing / (1.f + expf(-m));
     return -a.beta * s;
 }
 
-// Rows of [lo, hi) with a token, by the whole block; every thread gets the number.
+// Rows of [lo, hi) with a token, by the whole block; every thread gets the number.  Every CTA of a
+// row counts its sequence, a block's meeting for THREADS rows: with means the work grows with the
+// square of a sequence's length (two sequences of 8192 rows x 32000 bf16 with the gradient 595 us,
+// 469 with sums; four of 1000 rows 129 and 123).
 template <int THREADS>
 __device__ __forceinline__ int count_tokens(const TokenLossArgs& a, int lo, int hi) {
     int n = 0;

@@ -483,8 +483,12 @@ int dflash2_policy_loss_backward(const float* grad_loss, const void* logits, lon
  * pair with weight 0 has loss and gradient 0.  Offsets that fall or leave [0, rows] are
  * flagged (DF2_FLAG_BAD_ID) and taken into range: no memory outside is touched, the outputs
  * of their pairs are undefined.  With the gradient the rows are read twice, as every row of
- * a pair weighs on every other's gradient.  Sums over rows are in 64 bits, in an order that
- * depends on nothing but the sequence.  rows == 0 and pairs == 0 launches nothing.
+ * a pair weighs on every other's gradient.  Sums over rows, and the loss' m from them, are in
+ * 64 bits, in an order that depends on nothing but the sequence.  The gradient takes m from
+ * seq_logp as it is returned, in fp32: there m is off by up to beta * 2^-22 * (|S_c| + |S_r| +
+ * |ref_c| + |ref_r|), 5e-4 for sums of -5000 and beta = 0.1.  With average != 0 every row's gradient counts its
+ * sequence's tokens, work that grows with the square of a sequence's length.  rows == 0 and
+ * pairs == 0 launches nothing.
  * INVALID_ARG and UNSUPPORTED as dflash2_policy_loss; pairs < 0; beta or margin not finite;
  * label_smoothing outside [0, 1]; UNSUPPORTED: pairs > 2^24.
  */
@@ -556,7 +560,11 @@ int dflash2_grad_norm(int count, const void* const* grads, const int64_t* sizes,
  *   by_chance  0: all rounding is to the nearest.  Else 8-bit states, and bf16 parameters without
  *           master copies, are rounded up or down with odds by the distance, by bits made of
  *           seed, step, the tensor's place in the list and the element's place in it: the
- *           same call gives the same bits.  With 8-bit states this is what lets v follow: it moves
+ *           same call gives the same bits.  Every rounding is fair by itself, and not correlated
+ *           with those of other places, steps and seeds; equal places of two tensors of one call
+ *           (and places 2^32 apart) are correlated, by 0.23 for m and 0.42 for v in the mean
+ *           square over seeds, not for parameters.  Where that counts, give the tensors calls with
+ *           seeds of their own.  With 8-bit states chance is what lets v follow: it moves
  *           by 1 - beta2 of itself a step, a 30th of half of a code's distance, and to the nearest
  *           it would stay where it is
  * Vectors of 8 elements are taken at once where all of a tensor's pointers are aligned to 16
