@@ -287,11 +287,11 @@ __global__ void __launch_bounds__(kJoinThreads)
 // ------------------------------------------------------------------ AdamW
 
 // How a launch takes its chunks.  The figures are those of bf16 weights and gradients, or of fp32
-// ones; other types of weights and gradients take the same shapes.  With states in 8 bits instructions bound the step, 60 a weight,
-// and warps to cover their latency count: 128 threads at 64 registers, 76 us for 40.4 M weights in
-// bf16 (5.4 TB/s; 78 us with the states' sums one by one), against 81 us at 80 registers and 94 us
-// with one vector a thread.  With states in fp32 HBM does: 535 to 550 us for 136 M fp32 weights
-// (7.1 TB/s) in all of these shapes.
+// ones; other types of weights and gradients take the same shapes.  With states in 8 bits
+// instructions bound the step, 60 a weight, and warps to cover their latency count: 128 threads at
+// 64 registers, 76 us for 40.4 M weights in bf16 (5.4 TB/s; 78 us with the states' sums one by
+// one), against 81 us at 80 registers and 94 us with one vector a thread.  With states in fp32 HBM
+// does: 535 to 550 us for 136 M fp32 weights (7.1 TB/s) in all of these shapes.
 template <bool S8>
 struct AdamShape {
     static constexpr int kThreads = S8 ? 128 : 256, kMinCtas = S8 ? 8 : 1;

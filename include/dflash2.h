@@ -452,7 +452,8 @@ int dflash2_policy_loss(const void* logits, long long ld, const int32_t* tokens,
  * loss: grad_loss [rows] fp32; logp, lse [rows] as dflash2_policy_loss wrote them; the rest as
  * there.  Where |lse| is 256 or more, or infinite, its fp32 rounding would show in the
  * gradient: the row's sum is taken again from the logits.  A row with grad_loss or weight 0 is
- * not read and its gradient is 0, whatever the other one is.
+ * not read and its gradient is 0, whatever the other one is; a grad_loss that is not finite makes
+ * any other row with a token what the product gives, NaN where g is 0.
  */
 int dflash2_policy_loss_backward(const float* grad_loss, const void* logits, long long ld,
                                  const int32_t* tokens, const float* old_logp,
@@ -486,9 +487,9 @@ int dflash2_policy_loss_backward(const float* grad_loss, const void* logits, lon
  * a pair weighs on every other's gradient.  Sums over rows, and the loss' m from them, are in
  * 64 bits, in an order that depends on nothing but the sequence.  The gradient takes m from
  * seq_logp as it is returned, in fp32: there m is off by up to beta * 2^-22 * (|S_c| + |S_r| +
- * |ref_c| + |ref_r|), 5e-4 for sums of -5000 and beta = 0.1.  With average != 0 every row's gradient counts its
- * sequence's tokens, work that grows with the square of a sequence's length.  rows == 0 and
- * pairs == 0 launches nothing.
+ * |ref_c| + |ref_r|), 5e-4 for sums of -5000 and beta = 0.1.  With average != 0 every row's
+ * gradient counts its sequence's tokens, work that grows with the square of a sequence's length.
+ * rows == 0 and pairs == 0 launches nothing.
  * INVALID_ARG and UNSUPPORTED as dflash2_policy_loss; pairs < 0; beta or margin not finite;
  * label_smoothing outside [0, 1]; UNSUPPORTED: pairs > 2^24.
  */
@@ -573,7 +574,8 @@ int dflash2_grad_norm(int count, const void* const* grads, const int64_t* sizes,
  * element; beta1 or beta2 outside [0, 1); eps not positive (in fp32) or not finite; lr, weight_decay
  * or grad_scale not finite; max_norm negative or NaN, above 0 but 0 in fp32, or without norm;
  * step < 1; one scale array without the other; master with fp32 parameters; a tensor that is
- * written overlapping any other (or listed twice).  UNSUPPORTED: a tensor of more than 2^40 elements.
+ * written overlapping any other (or listed twice).  UNSUPPORTED: a tensor of more than 2^40
+ * elements.
  */
 int dflash2_adamw(int count, void* const* params, const void* const* grads, void* const* exp_avg,
                   void* const* exp_avg_sq, float* const* master, uint8_t* const* exp_avg_scale,
